@@ -445,6 +445,202 @@ int skv_build_ecdf(const uint64_t *counts, uint32_t *ecdf, float *phat);
  * T[i] = RNE(2^26 Phi(-8 + i/512)), T[0] = 0, T[8192] = 2^26. */
 int skv_phi_table(uint32_t *table);
 
+/* ======================= a paged KV cache ================================
+ *
+ * What a decoded cache is for: attention reads it, new tokens are appended to
+ * it, sequences share, copy and give back its memory.  These calls work on the
+ * pages skv_decode_range writes (page_of_chunk): a page holds the scalars of one
+ * chunk, page_tokens x head_dim of one (layer, kv, head, token block), and a
+ * sequence's row of the table is the page_of_chunk of a container with
+ * max_blocks token blocks.
+ *
+ * Conventions, beside those at the top: all of these calls enqueue work and
+ * none synchronizes (skv_cache_status does).  Sequence slots, lengths and
+ * positions are device arrays, so a captured graph can be replayed with new
+ * ones.  Argument errors that the host can see return at once; errors in the
+ * data (a slot, length or page out of range, no free page) are gathered in
+ * *status and reported by skv_cache_status, and what they concern is left out.
+ * Calls that change the table or the counts, and calls that read what those
+ * wrote, must be ordered one after the other (one stream, or events).        */
+
+#define SKV_NO_PAGE 0xffffffffu /* a table entry without a page */
+
+/* A paged cache.  The caller owns every buffer.
+ *   dtype        SKV_BF16 or SKV_E4M3.
+ *   head_dim     a multiple of 8 (bf16) or 16 (e4m3).
+ *   page_tokens  tokens per page (the codec's token_block).
+ *   max_seqs, max_blocks   sequence slots, and token blocks of each.
+ *   flags        0.
+ *   num_pages    pages in the pool, below 2^32 - 1.
+ *   pool         device (16-byte aligned), [num_pages][page_tokens][head_dim].
+ *   table        device, u32 [max_seqs][layers][2][heads][max_blocks]: page
+ *                numbers, SKV_NO_PAGE where there is none.
+ *   refs         device, u32 [num_pages]: how many table entries name the page;
+ *                0 for a free page.
+ *   status       device, one u32, gathers errors.
+ *   scale        device, e4m3 only: fp32 [layers][heads], the value of a code
+ *                unit (keys and values are code * scale); NULL: 1.  Must be
+ *                NULL for bf16. */
+typedef struct {
+  int32_t dtype, layers, heads, head_dim, page_tokens;
+  int32_t max_seqs, max_blocks, flags;
+  uint64_t num_pages;
+  void *pool;
+  uint32_t *table;
+  uint32_t *refs;
+  uint32_t *status;
+  const float *scale;
+} skv_cache;
+
+/* An empty cache: no pages in the table, every page free, status clear.  The
+ * pool is not touched. */
+int skv_cache_init(const skv_cache *cache, skv_stream_t stream);
+
+/* The status gathered by the calls on this cache since the last
+ * skv_cache_status (or skv_cache_init), which it clears: SKV_OK, SKV_ERR_ARG,
+ * SKV_ERR_CAPACITY (no free pages).  Synchronizes `stream`. */
+int skv_cache_status(const skv_cache *cache, skv_stream_t stream);
+
+/* Workspace bytes of skv_cache_reserve and skv_cache_fork with up to n
+ * sequences and of skv_cache_compact (n = 0 is enough); 0 if invalid.  The
+ * workspace (256-byte aligned) holds nothing between calls. */
+size_t skv_cache_workspace_bytes(const skv_cache *cache, int32_t n);
+
+/* Pages for tokens to come: sequence slots[i], which has pages for old_len[i]
+ * tokens, gets pages for new_len[i].  For every i, row (layer, kv, head) and
+ * token block in ceil(old/page_tokens) .. ceil(new/page_tokens) - 1, in that
+ * order, the table gets the free page with the lowest number that is left and
+ * its count becomes 1.  All or nothing: when a slot or length is out of range,
+ * a slot is named twice or one of the entries is taken (SKV_ERR_ARG), or when
+ * there are fewer free pages than that (SKV_ERR_CAPACITY), nothing changes.
+ *   slots, old_len, new_len   device, i32 [n]. */
+int skv_cache_reserve(const skv_cache *cache, const int32_t *slots, const int32_t *old_len,
+                      const int32_t *new_len, int32_t n, void *workspace,
+                      size_t workspace_bytes, skv_stream_t stream);
+
+/* Fork sequences: slot children[i] becomes a copy of the first lens[i] tokens
+ * of slot parents[i].  Full pages are shared (their counts go up), so no page
+ * with a count above 1 is ever written; the last block, where it is not full,
+ * gets a page of its own (the lowest free ones, in the order i, row) with the
+ * filled rows copied.  children must be distinct, no parent, and empty (no
+ * pages).  All or nothing, with the errors of skv_cache_reserve; a parent
+ * without a page for one of its blocks is SKV_ERR_ARG.
+ *   parents, children, lens   device, i32 [n]. */
+int skv_cache_fork(const skv_cache *cache, const int32_t *parents, const int32_t *children,
+                   const int32_t *lens, int32_t n, void *workspace, size_t workspace_bytes,
+                   skv_stream_t stream);
+
+/* Give back every page of the sequences slots[0..n): their counts go down, a
+ * page whose count reaches 0 is free, the table entries become SKV_NO_PAGE.  A
+ * slot that is out of range, or an entry that names no page or a free one, is
+ * reported (SKV_ERR_ARG) and skipped.
+ *   slots        device, i32 [n]. */
+int skv_cache_free(const skv_cache *cache, const int32_t *slots, int32_t n, skv_stream_t stream);
+
+/* Close the holes: with n pages in use, those numbered n and above move to the
+ * free numbers below n (the highest page to the lowest hole, the next one to
+ * the next), and the tables follow.
+ *   table_out, refs_out   device, shaped like table and refs, or both NULL: the
+ *                cache's own are changed in place.  With both given the cache's
+ *                own stay as they are, and the pages they name too until a free
+ *                number is reused: work in flight may still read through them.
+ * Entries that name a free page are reported (SKV_ERR_ARG) and kept. */
+int skv_cache_compact(const skv_cache *cache, uint32_t *table_out, uint32_t *refs_out,
+                      void *workspace, size_t workspace_bytes, skv_stream_t stream);
+
+/* Copy pages: page dst[i] of dst_pool = page src[i] of src_pool, i < n.  Each
+ * pool is the cache's (NULL) or one of the caller's with pages of the same
+ * size, in device or mapped pinned host memory, 16-byte aligned, with
+ * src_pages or dst_pages pages (ignored for NULL).  Counts and tables are not
+ * touched.  No page may be both a source and a destination, or a destination
+ * twice.  Page numbers out of range are reported (SKV_ERR_ARG) and skipped.
+ *   src, dst     device, u32 [n]. */
+int skv_cache_copy_pages(const skv_cache *cache, const void *src_pool, uint64_t src_pages,
+                         const uint32_t *src, void *dst_pool, uint64_t dst_pages,
+                         const uint32_t *dst, int64_t n, skv_stream_t stream);
+
+/* Rotary positions on one or more axes (time, height, width, ...).  Of a
+ * head's first rotary_dim channels, pair p (p < rotary_dim / 2) is channels
+ * (p, p + rotary_dim/2), or (2p, 2p + 1) with SKV_ROPE_INTERLEAVED, and turns
+ * by the angle position[axis_of_pair[p]] * freqs[p] (radians):
+ * (a, b) -> (a cos - b sin, a sin + b cos).  The other channels pass.
+ *   rotary_dim   a multiple of 16, 0 <= rotary_dim <= head_dim (0: no rotation).
+ *   axes         1 .. 4.
+ *   flags        SKV_ROPE_INTERLEAVED or 0.
+ *   freqs        device, fp64 [rotary_dim / 2].
+ *   axis_of_pair device, u8 [rotary_dim / 2], each < axes; NULL: all 0.  An
+ *                axis out of range is reported (SKV_ERR_ARG) and not turned. */
+#define SKV_ROPE_INTERLEAVED 1
+typedef struct {
+  int32_t rotary_dim, axes, flags, reserved; /* reserved: 0 */
+  const double *freqs;
+  const uint8_t *axis_of_pair;
+} skv_rope;
+
+/* New tokens of one layer, as a projection leaves them: element (i, head,
+ * channel) of q is q[i * q_stride + head * q_head_stride + channel], the same
+ * for k and v; bf16.  Strides in elements, multiples of 8; pointers 16-byte
+ * aligned. */
+typedef struct {
+  const void *q, *k, *v;
+  int64_t q_stride, q_head_stride, k_stride, k_head_stride, v_stride, v_head_stride;
+} skv_tokens;
+
+/* Append new tokens to one layer: q and k are turned to their positions, q
+ * goes to q_out, k and v to their places in the pages.
+ *   rope         NULL: no rotation.
+ *   slots        device, i32 [n]: the token's sequence; a negative slot is
+ *                padding (its q is turned, nothing is written to the cache).
+ *   at           device, i32 [n]: the token's place in its sequence.
+ *   positions    device, i32 [axes][n] (NULL without rotation).
+ *   n, q_heads   tokens; query heads (0: no queries, q and q_out are not used).
+ *   q_out        device bf16 [n][q_heads][head_dim], 16-byte aligned.  May be q
+ *                itself when q has that layout; otherwise no overlap with
+ *                the inputs.
+ * Angles are formed in fp64, so positions far out lose nothing; the rotation
+ * is fp32 and rounds once, to bf16 or, divided by the scale, to e4m3
+ * (round to nearest even, saturating at 448; a NaN stays a NaN, which the
+ * codec's encoder refuses).  A place must have a page that belongs to its
+ * sequence alone (count 1: skv_cache_reserve gives such pages and a fork never
+ * shares one that is not full); otherwise it is reported (SKV_ERR_ARG) and not
+ * written.  Two tokens with the same place: one of the two is kept. */
+int skv_cache_append(const skv_cache *cache, int32_t layer, const skv_rope *rope,
+                     const skv_tokens *tokens, const int32_t *slots, const int32_t *at,
+                     const int32_t *positions, int32_t n, int32_t q_heads, void *q_out,
+                     skv_stream_t stream);
+
+/* Workspace bytes of skv_cache_attend (any lengths up to the table's); 0 if
+ * invalid.  The workspace (256-byte aligned) holds nothing between calls. */
+size_t skv_cache_attend_workspace_bytes(const skv_cache *cache, int32_t batch, int32_t q_heads);
+
+/* Attention of one new token per sequence over the pages of one layer: with
+ * head h reading the keys and values of kv head h / (q_heads / heads),
+ *   out[i][h] = sum_t w_t v_t,  w = softmax_t(softmax_scale * q[i][h] . k_t),
+ *   lse[i][h] = log sum_t exp(softmax_scale * q[i][h] . k_t),
+ * over the tokens begins[i] <= t < lens[i] of sequence slots[i].  An empty range
+ * (or a negative slot, for padding) gives zeros and -infinity.  What lies
+ * outside the range, NaN and infinities included, has no effect.
+ *   slots, lens  device, i32 [batch].
+ *   begins       device, i32 [batch], or NULL: 0 (a sliding window is lens - window).
+ *   q            device bf16, (i, head, channel) at q[i * q_stride + head *
+ *                q_head_stride + channel]; strides multiples of 8, 16-byte aligned.
+ *   q_heads      a multiple of heads.
+ *   max_len      host: no lens[i] is larger (it sizes the launch).
+ *   out          device bf16 [batch][q_heads][head_dim], 16-byte aligned; may be
+ *                q itself when q has that layout.
+ *   lse          device fp32 [batch][q_heads], or NULL.
+ * head_dim up to 256.  Products and sums are fp32 (the matrix unit's), the weights
+ * are rounded to bf16 (bf16 caches) or fp16 (e4m3 caches) before they meet the
+ * values.  The result does not depend on what else runs: a row is split and
+ * joined in a fixed order for given lens and device.  A slot, length or page
+ * out of range is reported (SKV_ERR_ARG); that row is empty, or that page's
+ * tokens are left out. */
+int skv_cache_attend(const skv_cache *cache, int32_t layer, const int32_t *slots,
+                     const int32_t *lens, const int32_t *begins, int32_t batch, const void *q,
+                     int64_t q_stride, int64_t q_head_stride, int32_t q_heads,
+                     float softmax_scale, int32_t max_len, void *out, float *lse,
+                     void *workspace, size_t workspace_bytes, skv_stream_t stream);
+
 /* Static description of a status code. */
 const char *skv_strerror(int status);
 

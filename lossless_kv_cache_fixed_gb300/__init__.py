@@ -4,7 +4,8 @@ The functions named ``skv_*`` mirror the C ABI in ``include/skv.h`` one to one
 and only marshal arguments (ctypes structs, raw device pointers, the current
 CUDA stream).  ``Codec`` is a convenience wrapper that owns the workspace and
 output buffers as torch tensors; every step of the coder runs in the CUDA
-kernels of ``csrc/``.  There is no fallback: if the library is missing, every
+kernels of ``csrc/``.  ``PagedCache`` (``paged.py``) wraps the paged cache the
+same way: page operations, the append of new tokens, attention.  There is no fallback: if the library is missing, every
 call raises.
 """
 from __future__ import annotations
@@ -33,7 +34,11 @@ EXPORTS = ("skv_max_encoded_bytes", "skv_workspace_bytes", "skv_encode", "skv_en
            "skv_model_fingerprint", "skv_merge_parts", "skv_decode",
            "skv_decode_range", "skv_decode_status", "skv_ideal_bits", "skv_model_bits",
            "skv_ideal_bits_noalloc", "skv_ideal_bits_noalloc_max_channels",
-           "skv_build_ecdf", "skv_phi_table", "skv_strerror", "skv_version")
+           "skv_build_ecdf", "skv_phi_table", "skv_strerror", "skv_version",
+           "skv_cache_init", "skv_cache_status", "skv_cache_workspace_bytes",
+           "skv_cache_reserve", "skv_cache_fork", "skv_cache_free", "skv_cache_compact",
+           "skv_cache_copy_pages", "skv_cache_append", "skv_cache_attend_workspace_bytes",
+           "skv_cache_attend")
 
 
 class SkvParams(C.Structure):
@@ -94,6 +99,7 @@ def lib():
             "skv_strerror": (C.c_char_p, [C.c_int]),
             "skv_version": (C.c_int, []),
         }
+        sig.update(SIGNATURES)
         for name, (res, args) in sig.items():
             f = getattr(L, name)
             f.restype, f.argtypes = res, args
@@ -454,3 +460,12 @@ class Codec:
         if rc:
             raise SkvError(rc, "skv_model_bits")
         return (tot, ps) if per_scalar else tot
+
+
+# ---- the paged cache (pages, append, attention) ----
+
+from .paged import (SIGNATURES, SKV_NO_PAGE, SKV_ROPE_INTERLEAVED, PagedCache, Rope,  # noqa: E402,F401
+                    SkvCache, SkvRope, SkvTokens, skv_cache_append, skv_cache_attend,
+                    skv_cache_attend_workspace_bytes, skv_cache_compact, skv_cache_copy_pages,
+                    skv_cache_fork, skv_cache_free, skv_cache_init, skv_cache_reserve,
+                    skv_cache_status, skv_cache_workspace_bytes)

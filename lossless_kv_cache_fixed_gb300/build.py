@@ -11,7 +11,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libskv.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
-SOURCES = ["skv_code.cu", "skv_bits.cu", "skv_scale.cu", "skv_adapt.cu", "skv_api.cu"]
+SOURCES = ["skv_code.cu", "skv_bits.cu", "skv_scale.cu", "skv_adapt.cu", "skv_api.cu",
+           "skv_cache_pages.cu", "skv_cache_append.cu", "skv_cache_attend.cu", "skv_cache_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -30,10 +31,11 @@ def _deps():
 
 
 def source_digest() -> str:
-    """Hash of the kernel sources, to tie measurements to the code they describe."""
+    """Hash of the coder's kernel sources, to tie its measurements to the code they
+    describe (the paged cache's sources, skv_cache*, are not part of the coder)."""
     import hashlib
     h = hashlib.sha256()
-    for f in sorted(os.listdir(CSRC)):
+    for f in sorted(f for f in os.listdir(CSRC) if not f.startswith("skv_cache")):
         with open(os.path.join(CSRC, f), "rb") as fh:
             h.update(f.encode() + b"\0" + fh.read())
     return h.hexdigest()[:16]

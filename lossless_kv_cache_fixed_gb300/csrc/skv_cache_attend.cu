@@ -1,0 +1,695 @@
+// skv_cache_attend.cu -- attention of one new token per sequence over a paged
+// KV cache.
+//
+// o_h = sum_t p_t v_t / sum_t p_t with p_t = 2^(x_t - m), x_t = log2(e) * scale *
+// q_h.k_t, m a running maximum (softmax in one pass: when m grows to m', the
+// sums so far are multiplied by 2^(m - m')).  Every key and value byte is used
+// for 2 * group (bf16) or 4 * group (e4m3) operations, far below what the matrix
+// units need per byte of HBM, so HBM bounds the call and the design is about
+// keeping loads in flight:
+//   - the work is cut into units of 4 warp tiles of one (sequence, kv head) row
+//     and dealt evenly to one wave of persistent blocks, whatever the lengths;
+//     a block may take parts of several rows, a row may lie in several blocks;
+//   - a warp loads its own tiles (cp.async into its own ring of stages, rows
+//     outside the range filled with zeros) and computes on them without any
+//     block-wide barrier; the block's 4 warps are joined once per row;
+//   - a row that lies in several blocks is joined by k_attend_join, in block
+//     order, from at most two partial results per block.
+// The products run on the matrix units transposed, tokens as rows and the group's
+// query heads as the 8 columns of m16n8k16: S^T = K Q^T, O^T = V^T P^T, so a
+// group of up to 8 heads wastes no row and the running maximum, the sum and O^T
+// share one column layout (no exchange to rescale).  P goes from the accumulator
+// to the operand layout by movmatrix.  e4m3 codes become fp16 (exact); q becomes
+// fp16 after a power-of-two scale per head, which loses nothing above 2^-24 of
+// the head's largest channel.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "skv_cache.cuh"
+
+namespace skv {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;  // x may pass m by this before the sums are rescaled (p <= 2^8)
+
+template <int ES, int DP, int NT>
+struct Cfg {
+  static constexpr int kRowB = DP * ES;              // bytes of a token's row in shared memory
+  static constexpr int kCpr = kRowB / 16;            // 16-byte chunks of it
+  static constexpr int kTok = kRowB <= 128 ? 32 : 16;  // tokens of a warp tile
+  static constexpr int kTile = kTok * kRowB;         // bytes of a tile of K or V
+  static constexpr int kStages = kTile <= 2048 ? 4 : 3;
+  static constexpr int kUnit = kWarps * kTok;        // tokens of a unit
+  static constexpr int kSmem = kWarps * kStages * 2 * kTile;
+  static constexpr int kPerSm = kSmem > 110 * 1024 ? 1 : 2;
+  static constexpr int kHeads = 8 * NT;
+  static_assert(kWarps * kHeads * (DP + 2) * 4 <= kSmem, "the join of the warps reuses the stages");
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <bool TRANS>
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  if (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+template <int ES>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (ES == 2)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// two e4m3 codes (low 16 bits) to two halves
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t v) {
+  uint32_t r;
+  asm("{.reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+template <int ES>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if (ES == 2) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// byte offset of 16-byte chunk c of row r in a tile: chunks are permuted so that
+// the 8 rows one ldmatrix reads lie in 8 different bank groups
+template <int CPR>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  if (CPR >= 8) return (uint32_t)(r * CPR + ((c & ~7) | ((c ^ r) & 7))) * 16;
+  return (uint32_t)(r * CPR + (c ^ ((r >> 1) & 3))) * 16;
+}
+
+// The tokens [begin, end) of batch entry b, its first tile's start and its units.
+struct Span {
+  int32_t slot, begin, end, start;
+  int32_t units;
+};
+__device__ __forceinline__ Span span_of(const AttendArgs &a, int b, int tok, int unit, bool tell) {
+  Span s;
+  s.slot = a.slots[b];
+  const int32_t len = a.lens[b];
+  s.begin = a.begins ? max(a.begins[b], 0) : 0;
+  s.end = len;
+  bool bad = len < 0 || len > a.max_len || (int64_t)len > (int64_t)a.c.blocks * a.c.Tb ||
+             s.slot >= a.c.seqs;
+  if (s.slot < 0) bad = false;  // padding
+  if (bad && tell) atomicOr(a.c.status, kCacheArg);
+  if (bad || s.slot < 0 || s.begin >= s.end) s.begin = s.end = 0;
+  s.start = s.begin / tok * tok;
+  s.units = (s.end - s.start + unit - 1) / unit;
+  return s;
+}
+
+template <int N>
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *tmp) {
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int64_t t = 0;
+#pragma unroll
+  for (int i = 0; i < N / 32; ++i) t += tmp[i];
+  __syncthreads();
+  return t;
+}
+
+// How the units are dealt: block c of `blocks` takes [c*W/blocks, (c+1)*W/blocks).
+__device__ __forceinline__ int64_t blocks_used(int64_t W, int64_t grid) {
+  const int64_t g = W / 2;  // at least two units each
+  return g < 1 ? 1 : g < grid ? g : grid;
+}
+
+// Partial results: per block two slots of kHeads x (DP sums, maximum, sum of weights).
+template <int DP, int NT>
+struct Part {
+  float o[8 * NT][DP];
+  float m[8 * NT], l[8 * NT];
+};
+
+template <int ES, int DP, int NT>
+__global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(AttendArgs a,
+                                                                              int head_tiles) {
+  using C = Cfg<ES, DP, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t s_tmp[kWarps];
+  __shared__ int64_t s_find[2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const CacheView &c = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int j = lane & 3, g8 = lane >> 2;
+  const int HV = c.heads * head_tiles;  // rows per batch entry
+  const int group = a.q_heads / c.heads;
+
+  // this block's share of the units
+  int64_t W = 0;
+  for (int b = threadIdx.x; b < a.batch; b += kThreads)
+    W += (int64_t)span_of(a, b, C::kTok, C::kUnit, blockIdx.x == 0).units * HV;
+  W = block_sum<kThreads>(W, s_tmp);
+  const int64_t nblk = blocks_used(W, gridDim.x);
+  if ((int64_t)blockIdx.x >= nblk) return;
+  int64_t pos = (int64_t)blockIdx.x * W / nblk;
+  const int64_t stop = ((int64_t)blockIdx.x + 1) * W / nblk;
+  if (pos >= stop) return;
+  // the batch entry that unit `pos` lies in
+  int64_t before = 0;
+  int b = 0;
+  for (int b0 = 0;; b0 += kThreads) {
+    const int bb = b0 + threadIdx.x;
+    const int64_t u =
+        bb < a.batch ? (int64_t)span_of(a, bb, C::kTok, C::kUnit, false).units * HV : 0;
+    int64_t x = u;  // inclusive prefix over the block
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(~0u, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_tmp[warp] = x;
+    __syncthreads();
+    int64_t all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) x += s_tmp[w];
+      all += s_tmp[w];
+    }
+    if (u && pos >= before + x - u && pos < before + x) {
+      s_find[0] = bb;
+      s_find[1] = before + x - u;
+    }
+    __syncthreads();
+    if (pos < before + all) break;
+    before += all;
+  }
+  b = (int)s_find[0];
+  before = s_find[1];
+
+  const uint32_t tile0 = smem_addr(smem) + warp * (C::kStages * 2 * C::kTile);
+  const bool whole = c.Tb % C::kTok == 0;  // a tile lies in one page
+
+  while (pos < stop) {
+    Span sp = span_of(a, b, C::kTok, C::kUnit, false);
+    if (sp.units == 0 || pos >= before + (int64_t)sp.units * HV) {
+      before += (int64_t)sp.units * HV;
+      ++b;
+      continue;
+    }
+    const int row = (int)((pos - before) / sp.units);
+    const int u0 = (int)(pos - before - (int64_t)row * sp.units);
+    const int nu = (int)min((int64_t)(sp.units - u0), stop - pos);
+    pos += nu;
+    const int h = row / head_tiles, h0 = h * group + (row - h * head_tiles) * C::kHeads;
+    const int nh = min(C::kHeads, h * group + group - h0);  // query heads of this row
+    const uint32_t *tab_k =
+        c.table + ((int64_t)sp.slot * c.rows + ((int64_t)a.layer * 2) * c.heads + h) * c.blocks;
+    const uint32_t *tab_v = tab_k + (int64_t)c.heads * c.blocks;
+
+    // set when a token in the range has no page: its rows are zeros and it is masked
+    bool holes = false;
+
+    auto load = [&](int u, int stage) {
+      const int t0 = sp.start + ((u0 + u) * kWarps + warp) * C::kTok;
+      if (u < nu && t0 < sp.end) {
+        const uint32_t sk = tile0 + stage * 2 * C::kTile, sv = sk + C::kTile;
+        // byte offsets in the pool of row 0 (the tile lies in one page) or of row lane % kTok
+        const int t = whole ? t0 : min(t0 + lane % C::kTok, sp.end - 1);
+        const int blk = t / c.Tb;
+        const uint32_t pk = tab_k[blk], pv = tab_v[blk];
+        const uint32_t off = (uint32_t)(t - blk * c.Tb) * c.row_bytes;
+        const bool has = pk < c.pages && pv < c.pages;
+        if (__any_sync(~0u, !has)) {
+          holes = true;
+          if (lane == 0) atomicOr(c.status, kCacheArg);
+        }
+        const uint64_t bk = has ? (uint64_t)pk * c.page_bytes + off : 0;
+        const uint64_t bv = has ? (uint64_t)pv * c.page_bytes + off : 0;
+#pragma unroll
+        for (int i = 0; i < C::kTok * C::kCpr / 32; ++i) {
+          const int id = i * 32 + lane, r = id / C::kCpr, ch = id % C::kCpr;
+          const bool in = t0 + r >= sp.begin && t0 + r < sp.end && ch * 16 < (int)c.row_bytes;
+          uint64_t rk, rv;
+          bool ok;
+          if (whole) {
+            rk = bk + (uint32_t)r * c.row_bytes;
+            rv = bv + (uint32_t)r * c.row_bytes;
+            ok = has;
+          } else {
+            rk = __shfl_sync(~0u, bk, r);
+            rv = __shfl_sync(~0u, bv, r);
+            ok = __shfl_sync(~0u, (int)has, r);
+          }
+          const bool on = in && ok;
+          cp_async16(sk + swz<C::kCpr>(r, ch), c.pool + (on ? rk + ch * 16 : 0), on);
+          cp_async16(sv + swz<C::kCpr>(r, ch), c.pool + (on ? rv + ch * 16 : 0), on);
+        }
+      }
+      cp_commit();
+    };
+
+#pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s) load(s, s);
+
+    // q as the B operand: column n = head g8 (+ 8), rows k = channels.  e4m3 tiles
+    // give lane j channels 4j..4j+3 of each 16, so q takes the same order.
+    uint32_t qf[NT][DP / 16][2];
+    float f[NT][2];  // x = f * (product), of heads 2j and 2j + 1
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int hq = n * 8 + g8;
+      const uint16_t *qp = a.q + (int64_t)b * a.qs + (int64_t)(h0 + hq) * a.qhs;
+      const bool on = hq < nh;
+      float e = 1.f;
+      if (ES == 2) {
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const int d = k * 16 + 2 * j;
+          qf[n][k][0] = on && d < c.D ? *reinterpret_cast<const uint32_t *>(qp + d) : 0;
+          qf[n][k][1] = on && d + 8 < c.D ? *reinterpret_cast<const uint32_t *>(qp + d + 8) : 0;
+        }
+      } else {
+        float mx = 0.f;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const int d = k * 16 + 4 * j;
+          uint2 v = make_uint2(0, 0);
+          if (on && d < c.D) v = *reinterpret_cast<const uint2 *>(qp + d);
+          qf[n][k][0] = v.x;
+          qf[n][k][1] = v.y;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w = qf[n][k][i];
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w << 16)),
+                                 fabsf(__uint_as_float(w & 0xffff0000u))));
+          }
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+        // the largest channel to [1, 2): e = 2^exponent, kept where 1/e is normal
+        const uint32_t ex = __float_as_uint(mx) >> 23;
+        if (ex >= 1 && ex < 253) e = __uint_as_float(ex << 23);
+        const float r = 1.f / e;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w = qf[n][k][i];
+            qf[n][k][i] = pack2<1>(__uint_as_float(w << 16) * r,
+                                   __uint_as_float(w & 0xffff0000u) * r);
+          }
+      }
+      float s = a.scale * kLog2e;
+      if (ES == 1 && c.scale) s *= c.scale[a.layer * c.heads + h];
+      f[n][0] = s * __shfl_sync(~0u, e, 8 * j);      // head 2j: any lane of group 2j
+      f[n][1] = s * __shfl_sync(~0u, e, 8 * j + 4);
+    }
+
+    float o[DP / 16][NT][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int d = 0; d < DP / 16; ++d)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[d][n][i] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
+
+    int stage = 0;
+    for (int u = 0; u < nu; ++u) {
+      cp_wait<C::kStages - 2>();
+      __syncwarp();
+      {
+        int s = stage + C::kStages - 1;
+        if (s >= C::kStages) s -= C::kStages;
+        load(u + C::kStages - 1, s);
+      }
+      const int t0 = sp.start + ((u0 + u) * kWarps + warp) * C::kTok;
+      const uint32_t sk = tile0 + stage * 2 * C::kTile, sv = sk + C::kTile;
+      if (++stage == C::kStages) stage = 0;
+      if (t0 >= sp.end) continue;  // the whole warp
+
+      // S^T = K Q^T
+      float x[C::kTok / 16][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < C::kTok / 16; ++mt) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[mt][n][i] = 0.f;
+        const int r = mt * 16 + (lane & 15);
+        if (ES == 2) {
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            uint32_t t[4];
+            ldsm4<false>(t, sk + swz<C::kCpr>(r, 2 * k + (lane >> 4)));
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma<ES>(x[mt][n], t[0], t[1], t[2], t[3], qf[n][k][0], qf[n][k][1]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < DP / 16; k += 2) {
+            uint32_t t[4];
+            ldsm4<false>(t, sk + swz<C::kCpr>(r, k + (lane >> 4)));
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+              const uint32_t lo = t[2 * kk], hi = t[2 * kk + 1];
+              const uint32_t a0 = e4m3x2(lo), a2 = e4m3x2(lo >> 16);
+              const uint32_t a1 = e4m3x2(hi), a3 = e4m3x2(hi >> 16);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma<ES>(x[mt][n], a0, a1, a2, a3, qf[n][k + kk][0], qf[n][k + kk][1]);
+            }
+          }
+        }
+      }
+      // scale, mask, running maximum
+      const bool edge = holes || t0 < sp.begin || t0 + C::kTok > sp.end;
+      bool grow = false;
+      float top[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        top[n][0] = top[n][1] = -INFINITY;
+#pragma unroll
+        for (int mt = 0; mt < C::kTok / 16; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = x[mt][n][i] * f[n][i & 1];
+            if (edge) {
+              const int t = t0 + mt * 16 + g8 + (i >> 1) * 8;
+              if (t < sp.begin || t >= sp.end) v = -INFINITY;
+              else if (holes && (tab_k[t / c.Tb] >= c.pages || tab_v[t / c.Tb] >= c.pages))
+                v = -INFINITY;
+            }
+            x[mt][n][i] = v;
+            top[n][i & 1] = fmaxf(top[n][i & 1], v);
+          }
+        grow = grow || top[n][0] > m[n][0] + kSlack || top[n][1] > m[n][1] + kSlack;
+      }
+      if (__any_sync(~0u, grow)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float t = top[n][i];
+            t = fmaxf(t, __shfl_xor_sync(~0u, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(~0u, t, 8));
+            t = fmaxf(t, __shfl_xor_sync(~0u, t, 16));
+            const float mn = fmaxf(m[n][i], t);
+            const float s = mn == -INFINITY ? 1.f : ex2(m[n][i] - mn);
+            m[n][i] = mn;
+            l[n][i] *= s;
+#pragma unroll
+            for (int d = 0; d < DP / 16; ++d) {
+              o[d][n][i] *= s;
+              o[d][n][i + 2] *= s;
+            }
+          }
+      }
+      // P, its sum, and P as the B operand
+      uint32_t pf[C::kTok / 16][NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
+        const float m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+        for (int mt = 0; mt < C::kTok / 16; ++mt) {
+          const float p0 = ex2(x[mt][n][0] - m0), p1 = ex2(x[mt][n][1] - m1);
+          const float p2 = ex2(x[mt][n][2] - m0), p3 = ex2(x[mt][n][3] - m1);
+          l[n][0] += p0 + p2;
+          l[n][1] += p1 + p3;
+          pf[mt][n][0] = transpose8x8(pack2<ES>(p0, p1));
+          pf[mt][n][1] = transpose8x8(pack2<ES>(p2, p3));
+        }
+      }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int mt = 0; mt < C::kTok / 16; ++mt) {
+        if (ES == 2) {
+          const int r = mt * 16 + (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+          for (int d = 0; d < DP / 16; ++d) {
+            uint32_t t[4];
+            ldsm4<true>(t, sv + swz<C::kCpr>(r, 2 * d + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma<ES>(o[d][n], t[0], t[1], t[2], t[3], pf[mt][n][0], pf[mt][n][1]);
+          }
+        } else {
+          const int r = mt * 16 + (lane & 15);
+#pragma unroll
+          for (int d = 0; d < DP / 16; d += 2) {
+            uint32_t t[4];
+            ldsm4<true>(t, sv + swz<C::kCpr>(r, d + (lane >> 4)));
+#pragma unroll
+            for (int dd = 0; dd < 2; ++dd) {
+              // bytes: token 2j channels (2r, 2r+1), token 2j+1 the same
+              const uint32_t lo = __byte_perm(t[2 * dd], 0, 0x3120);
+              const uint32_t hi = __byte_perm(t[2 * dd + 1], 0, 0x3120);
+              const uint32_t a0 = e4m3x2(lo), a1 = e4m3x2(lo >> 16);
+              const uint32_t a2 = e4m3x2(hi), a3 = e4m3x2(hi >> 16);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma<ES>(o[d + dd][n], a0, a1, a2, a3, pf[mt][n][0], pf[mt][n][1]);
+            }
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+
+    // join the warps in the stages' memory, then write the row or a partial result
+    float *so = reinterpret_cast<float *>(smem);
+    float *sm = so + kWarps * C::kHeads * DP, *sl = sm + kWarps * C::kHeads;
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float s = l[n][i];
+        s += __shfl_xor_sync(~0u, s, 4);
+        s += __shfl_xor_sync(~0u, s, 8);
+        s += __shfl_xor_sync(~0u, s, 16);
+        const int hh = n * 8 + 2 * j + i;
+        if (g8 == 0) {
+          sm[warp * C::kHeads + hh] = m[n][i];
+          sl[warp * C::kHeads + hh] = s;
+        }
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d) {
+          const int d0 = ES == 2 ? d * 16 + g8 : d * 16 + 2 * g8;
+          const int d1 = ES == 2 ? d0 + 8 : d0 + 1;
+          so[(warp * C::kHeads + hh) * DP + d0] = o[d][n][i];
+          so[(warp * C::kHeads + hh) * DP + d1] = o[d][n][i + 2];
+        }
+      }
+    __syncthreads();
+    const bool done = u0 == 0 && nu == sp.units;
+    Part<DP, NT> *part = reinterpret_cast<Part<DP, NT> *>(a.ws) + ((int64_t)blockIdx.x * 2 + (u0 == 0));
+    float osc = 1.f;
+    if (ES == 1 && c.scale) osc = c.scale[a.layer * c.heads + h];
+    for (int x = threadIdx.x; x < nh * DP; x += kThreads) {
+      const int hh = x / DP, d = x - hh * DP;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w * C::kHeads + hh]);
+      const float m0 = M == -INFINITY ? 0.f : M;
+      float acc = 0.f, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float s = ex2(sm[w * C::kHeads + hh] - m0);
+        acc += s * so[(w * C::kHeads + hh) * DP + d];
+        L += s * sl[w * C::kHeads + hh];
+      }
+      if (done) {
+        const int64_t oh = (int64_t)b * a.q_heads + h0 + hh;
+        if (d < c.D) {
+          const __nv_bfloat16 v = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L * osc);
+          a.out[oh * c.D + d] = *reinterpret_cast<const uint16_t *>(&v);
+        }
+        if (d == 0 && a.lse) a.lse[oh] = (m0 + log2f(L)) * kLn2;
+      } else {
+        part->o[hh][d] = acc;
+        if (d == 0) {
+          part->m[hh] = M;
+          part->l[hh] = L;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// One block per (batch entry, query head): joins the parts of a row that lies in
+// several blocks, in block order, and writes rows without tokens.
+template <int ES, int DP, int NT>
+__global__ void __launch_bounds__(256) k_attend_join(AttendArgs a, int head_tiles, int grid) {
+  using C = Cfg<ES, DP, NT>;
+  __shared__ int64_t s_tmp[8];
+  __shared__ float s_o[256];
+  const CacheView &c = a.c;
+  const int HV = c.heads * head_tiles;
+  const int group = a.q_heads / c.heads;
+  const int b = blockIdx.x / a.q_heads, hq = blockIdx.x - b * a.q_heads;
+  int64_t W = 0, first = 0;
+  for (int i = threadIdx.x; i < a.batch; i += 256) {
+    const int64_t u = (int64_t)span_of(a, i, C::kTok, C::kUnit, false).units * HV;
+    W += u;
+    if (i < b) first += u;
+  }
+  W = block_sum<256>(W, s_tmp);
+  first = block_sum<256>(first, s_tmp);
+  const int units = span_of(a, b, C::kTok, C::kUnit, false).units;
+  const int64_t oh = (int64_t)b * a.q_heads + hq;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (units == 0) {
+    for (int d = threadIdx.x; d < c.D; d += 256) a.out[oh * c.D + d] = 0;
+    if (threadIdx.x == 0 && a.lse) a.lse[oh] = -INFINITY;
+    return;
+  }
+  const int h = hq / group, in = hq - h * group;
+  const int row = h * head_tiles + in / C::kHeads, hh = in % C::kHeads;
+  const int64_t lo = first + (int64_t)row * units, hi = lo + units;
+  const int64_t nblk = blocks_used(W, grid);
+  // the block that unit u lies in: the largest i with i*W/nblk <= u
+  const int64_t c0 = ((lo + 1) * nblk - 1) / W, c1 = (hi * nblk - 1) / W;
+  if (c0 == c1) return;  // written by its block
+  const Part<DP, NT> *parts = reinterpret_cast<const Part<DP, NT> *>(a.ws);
+  float M = -INFINITY;
+  for (int64_t i = c0; i <= c1; ++i) M = fmaxf(M, parts[i * 2 + (i == c0)].m[hh]);
+  const float m0 = M == -INFINITY ? 0.f : M;
+  // threads: kSplit groups over the parts, DP channels
+  constexpr int kSplit = 256 / DP;
+  const int d = threadIdx.x % DP, sg = threadIdx.x / DP;
+  float acc = 0.f, L = 0.f;
+  for (int64_t i = c0 + sg; i <= c1; i += kSplit) {
+    const Part<DP, NT> &p = parts[i * 2 + (i == c0)];
+    const float s = ex2(p.m[hh] - m0);
+    acc += s * p.o[hh][d];
+  }
+  for (int64_t i = c0; i <= c1; ++i) {
+    const Part<DP, NT> &p = parts[i * 2 + (i == c0)];
+    L += ex2(p.m[hh] - m0) * p.l[hh];
+  }
+  s_o[threadIdx.x] = acc;
+  __syncthreads();
+  if (sg) return;
+#pragma unroll
+  for (int s = 1; s < kSplit; ++s) acc += s_o[s * DP + d];
+  float osc = 1.f;
+  if (ES == 1 && c.scale) osc = c.scale[a.layer * c.heads + h];
+  if (d < c.D) {
+    const __nv_bfloat16 v = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L * osc);
+    a.out[oh * c.D + d] = *reinterpret_cast<const uint16_t *>(&v);
+  }
+  if (d == 0 && a.lse) a.lse[oh] = (m0 + log2f(L)) * kLn2;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return n;
+}
+
+template <int ES, int DP, int NT>
+cudaError_t run(const AttendArgs &a, int head_tiles, cudaStream_t st) {
+  using C = Cfg<ES, DP, NT>;
+  auto kern = k_attend<ES, DP, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count();
+  if (!sms) return cudaErrorInvalidDevice;
+  const int64_t rows = (int64_t)a.batch * a.c.heads * head_tiles;
+  // a tile may start up to kTok - 1 tokens before the range
+  const int64_t units = rows * (((int64_t)a.max_len + C::kTok - 1 + C::kUnit - 1) / C::kUnit);
+  int64_t grid = (int64_t)sms * C::kPerSm;
+  if (grid > units / 2) grid = units / 2;
+  if (grid < 1) grid = 1;
+  kern<<<(unsigned)grid, kThreads, C::kSmem, st>>>(a, head_tiles);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)a.batch * a.q_heads));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_attend_join<ES, DP, NT>, a, head_tiles, (int)grid);
+}
+
+template <int ES, int DP>
+cudaError_t run_nt(const AttendArgs &a, cudaStream_t st) {
+  const int group = a.q_heads / a.c.heads;
+  if (group <= 8) return run<ES, DP, 1>(a, 1, st);
+  return run<ES, DP, 2>(a, (group + 15) / 16, st);
+}
+
+template <int ES>
+cudaError_t run_d(const AttendArgs &a, cudaStream_t st) {
+  if (a.c.D <= 64) return run_nt<ES, 64>(a, st);
+  if (a.c.D <= 128) return run_nt<ES, 128>(a, st);
+  return run_nt<ES, 256>(a, st);
+}
+
+}  // namespace
+
+size_t attend_ws_bytes(const CacheView &c, int32_t, int32_t q_heads) {
+  const int sms = sm_count();
+  if (!sms) return 0;
+  const int heads = q_heads / c.heads <= 8 ? 8 : 16;
+  const int DP = c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256;
+  // two partial results for each of at most two blocks per SM
+  return (size_t)sms * 2 * 2 * heads * (DP + 2) * sizeof(float);
+}
+
+cudaError_t launch_attend(const AttendArgs &a, cudaStream_t st) {
+  return a.c.dtype == 1 ? run_d<1>(a, st) : run_d<2>(a, st);
+}
+
+}  // namespace skv
