@@ -85,7 +85,7 @@ struct AttendArgs {
   float scale;
   int32_t batch, q_heads, layer, max_len;
 };
-size_t attend_ws_bytes(const CacheView &c, int32_t batch, int32_t q_heads);
+size_t attend_ws_bytes(const CacheView &c, int32_t q_heads);
 cudaError_t launch_attend(const AttendArgs &a, cudaStream_t st);
 
 }  // namespace skv

@@ -236,7 +236,7 @@ int skv_cache_append(const skv_cache *cache, int32_t layer, const skv_rope *rope
 size_t skv_cache_attend_workspace_bytes(const skv_cache *cache, int32_t batch, int32_t q_heads) {
   CacheView c;
   if (make_view(cache, &c) || batch < 0 || q_heads <= 0 || q_heads % c.heads || c.D > 256) return 0;
-  return attend_ws_bytes(c, batch, q_heads);
+  return attend_ws_bytes(c, q_heads);
 }
 
 int skv_cache_attend(const skv_cache *cache, int32_t layer, const int32_t *slots,
@@ -257,7 +257,7 @@ int skv_cache_attend(const skv_cache *cache, int32_t layer, const int32_t *slots
     return SKV_ERR_ARG;
   if (q_stride % 8 || q_head_stride % 8) return SKV_ERR_ARG;
   if (!workspace || !aligned(workspace, kAlign)) return SKV_ERR_ARG;
-  const size_t need = attend_ws_bytes(c, batch, q_heads);
+  const size_t need = attend_ws_bytes(c, q_heads);
   if (!need) return SKV_ERR_CUDA;  // no device
   if (workspace_bytes < need) return SKV_ERR_CAPACITY;
   a.slots = slots;

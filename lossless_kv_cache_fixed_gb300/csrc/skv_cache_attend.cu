@@ -13,8 +13,9 @@
 //   - a warp loads its own tiles (cp.async into its own ring of stages, rows
 //     outside the range filled with zeros) and computes on them without any
 //     block-wide barrier; the block's 4 warps are joined once per row;
-//   - a row that lies in several blocks is joined by k_attend_join, in block
-//     order, from at most two partial results per block.
+//   - a row that lies in several blocks leaves a partial result in each (at most
+//     two per block) and is joined by k_attend_join, in block order;
+//   - a batch of few short rows is not cut: one block per row and no join.
 // The products run on the matrix units transposed, tokens as rows and the group's
 // query heads as the 8 columns of m16n8k16: S^T = K Q^T, O^T = V^T P^T, so a
 // group of up to 8 heads wastes no row and the running maximum, the sum and O^T
@@ -34,6 +35,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kRowUnits = 8;  // rows of up to so many units are not cut (see run)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;  // x may pass m by this before the sums are rescaled (p <= 2^8)
@@ -146,16 +148,37 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int b, int tok, int
   return s;
 }
 
-template <int N>
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *tmp) {
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int64_t t = 0;
-#pragma unroll
-  for (int i = 0; i < N / 32; ++i) t += tmp[i];
-  __syncthreads();
-  return t;
+// All units W of the batch; each lane owns `per` neighbouring entries with `mine`
+// units, `before` of all lie before them; `below` lie before entry `upto`.  One warp,
+// no block barrier: every warp of a block does the same.
+struct Sums {
+  int64_t W, before, mine, below;
+  int per;
+};
+template <typename C>
+__device__ __forceinline__ Sums sums_of(const AttendArgs &a, int HV, int upto, bool tell) {
+  const int lane = threadIdx.x & 31;
+  Sums r;
+  r.per = (a.batch + 31) / 32;
+  int64_t mine = 0, below = 0;
+  const int lo = lane * r.per, hi = min(lo + r.per, a.batch);
+#pragma unroll 4
+  for (int b = lo; b < hi; ++b) {
+    const int64_t u = (int64_t)span_of(a, b, C::kTok, C::kUnit, tell).units * HV;
+    mine += u;
+    if (b < upto) below += u;
+  }
+  int64_t x = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(~0u, x, o);
+    if (lane >= o) x += y;
+    below += __shfl_xor_sync(~0u, below, o);
+  }
+  r.W = __shfl_sync(~0u, x, 31);
+  r.mine = mine;
+  r.before = x - mine;
+  r.below = below;
+  return r;
 }
 
 // How the units are dealt: block c of `blocks` takes [c*W/blocks, (c+1)*W/blocks).
@@ -171,59 +194,71 @@ struct Part {
   float m[8 * NT], l[8 * NT];
 };
 
-template <int ES, int DP, int NT>
+// Zeros and -infinity for heads h0 .. h0 + nh - 1 of an entry without tokens.
+__device__ __forceinline__ void write_empty(const AttendArgs &a, int b, int h0, int nh,
+                                            int threads) {
+  const int64_t oh = (int64_t)b * a.q_heads + h0;
+  for (int x = threadIdx.x; x < nh * a.c.D; x += threads) a.out[oh * a.c.D + x] = 0;
+  for (int x = threadIdx.x; a.lse && x < nh; x += threads) a.lse[oh + x] = -INFINITY;
+}
+
+// ROWS: block i takes row i whole (entry i / HV); otherwise the units are dealt.
+template <int ES, int DP, int NT, bool ROWS>
 __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(AttendArgs a,
                                                                               int head_tiles) {
   using C = Cfg<ES, DP, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_tmp[kWarps];
-  __shared__ int64_t s_find[2];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!ROWS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const CacheView &c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int j = lane & 3, g8 = lane >> 2;
   const int HV = c.heads * head_tiles;  // rows per batch entry
   const int group = a.q_heads / c.heads;
 
-  // this block's share of the units
-  int64_t W = 0;
-  for (int b = threadIdx.x; b < a.batch; b += kThreads)
-    W += (int64_t)span_of(a, b, C::kTok, C::kUnit, blockIdx.x == 0).units * HV;
-  W = block_sum<kThreads>(W, s_tmp);
-  const int64_t nblk = blocks_used(W, gridDim.x);
-  if ((int64_t)blockIdx.x >= nblk) return;
-  int64_t pos = (int64_t)blockIdx.x * W / nblk;
-  const int64_t stop = ((int64_t)blockIdx.x + 1) * W / nblk;
-  if (pos >= stop) return;
-  // the batch entry that unit `pos` lies in
-  int64_t before = 0;
-  int b = 0;
-  for (int b0 = 0;; b0 += kThreads) {
-    const int bb = b0 + threadIdx.x;
-    const int64_t u =
-        bb < a.batch ? (int64_t)span_of(a, bb, C::kTok, C::kUnit, false).units * HV : 0;
-    int64_t x = u;  // inclusive prefix over the block
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(~0u, x, o);
-      if (lane >= o) x += y;
+  int64_t pos, stop, before = 0;
+  int b;
+  if (ROWS) {
+    b = blockIdx.x / HV;
+    const Span sp = span_of(a, b, C::kTok, C::kUnit, warp == 0 && blockIdx.x % HV == 0);
+    pos = (int64_t)(blockIdx.x - b * HV) * sp.units;
+    stop = pos + sp.units;
+    if (!sp.units) {
+      const int row = blockIdx.x - b * HV, h = row / head_tiles;
+      const int h0 = h * group + (row - h * head_tiles) * C::kHeads;
+      write_empty(a, b, h0, min(C::kHeads, h * group + group - h0), kThreads);
+      return;
     }
-    if (lane == 31) s_tmp[warp] = x;
-    __syncthreads();
-    int64_t all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) x += s_tmp[w];
-      all += s_tmp[w];
+  } else {
+    // this block's share of the units
+    const Sums all = sums_of<C>(a, HV, 0, blockIdx.x == 0 && warp == 0);
+    const int64_t nblk = blocks_used(all.W, gridDim.x);
+    if ((int64_t)blockIdx.x >= nblk) return;
+    pos = (int64_t)blockIdx.x * all.W / nblk;
+    stop = ((int64_t)blockIdx.x + 1) * all.W / nblk;
+    if (pos >= stop) return;
+    // the batch entry b that unit `pos` lies in, and the units before that entry
+    const int owner = __ffs(__ballot_sync(~0u, pos < all.before + all.mine)) - 1;
+    before = __shfl_sync(~0u, all.before, owner);
+    b = owner * all.per;
+    for (int b0 = b;; b0 += 32) {
+      const int bb = b0 + lane;
+      const int64_t u =
+          bb < a.batch ? (int64_t)span_of(a, bb, C::kTok, C::kUnit, false).units * HV : 0;
+      int64_t x = u;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(~0u, x, o);
+        if (lane >= o) x += y;
+      }
+      const uint32_t hit = __ballot_sync(~0u, pos < before + x);
+      if (hit) {
+        const int i = __ffs(hit) - 1;
+        b = b0 + i;
+        before += __shfl_sync(~0u, x - u, i);
+        break;
+      }
+      before += __shfl_sync(~0u, x, 31);
     }
-    if (u && pos >= before + x - u && pos < before + x) {
-      s_find[0] = bb;
-      s_find[1] = before + x - u;
-    }
-    __syncthreads();
-    if (pos < before + all) break;
-    before += all;
   }
-  b = (int)s_find[0];
-  before = s_find[1];
 
   const uint32_t tile0 = smem_addr(smem) + warp * (C::kStages * 2 * C::kTile);
   const bool whole = c.Tb % C::kTok == 0;  // a tile lies in one page
@@ -528,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
         }
       }
     __syncthreads();
-    const bool done = u0 == 0 && nu == sp.units;
+    const bool done = ROWS || (u0 == 0 && nu == sp.units);
     Part<DP, NT> *part = reinterpret_cast<Part<DP, NT> *>(a.ws) + ((int64_t)blockIdx.x * 2 + (u0 == 0));
     float osc = 1.f;
     if (ES == 1 && c.scale) osc = c.scale[a.layer * c.heads + h];
@@ -565,95 +600,121 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
 }
 
 // One block per (batch entry, query head): joins the parts of a row that lies in
-// several blocks, in block order, and writes rows without tokens.
+// several blocks and writes rows without tokens.  The warps take every kJoinWarps-th
+// part each and are added up in warp order.  It is launched while k_attend still runs
+// and finds its parts before it waits, so only the reading of the parts (one
+// round of loads for up to kJoinWarps of them) comes after k_attend's end.
+constexpr int kJoinWarps = 8;
 template <int ES, int DP, int NT>
-__global__ void __launch_bounds__(256) k_attend_join(AttendArgs a, int head_tiles, int grid) {
+__global__ void __launch_bounds__(kJoinWarps * 32) k_attend_join(AttendArgs a, int head_tiles,
+                                                                 int grid) {
   using C = Cfg<ES, DP, NT>;
-  __shared__ int64_t s_tmp[8];
-  __shared__ float s_o[256];
+  constexpr int kVec = DP / 32;  // channels per lane
+  __shared__ float s_o[kJoinWarps][DP];
   const CacheView &c = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int HV = c.heads * head_tiles;
   const int group = a.q_heads / c.heads;
   const int b = blockIdx.x / a.q_heads, hq = blockIdx.x - b * a.q_heads;
-  int64_t W = 0, first = 0;
-  for (int i = threadIdx.x; i < a.batch; i += 256) {
-    const int64_t u = (int64_t)span_of(a, i, C::kTok, C::kUnit, false).units * HV;
-    W += u;
-    if (i < b) first += u;
-  }
-  W = block_sum<256>(W, s_tmp);
-  first = block_sum<256>(first, s_tmp);
+  const Sums all = sums_of<C>(a, HV, b, false);
   const int units = span_of(a, b, C::kTok, C::kUnit, false).units;
   const int64_t oh = (int64_t)b * a.q_heads + hq;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (units == 0) {
-    for (int d = threadIdx.x; d < c.D; d += 256) a.out[oh * c.D + d] = 0;
-    if (threadIdx.x == 0 && a.lse) a.lse[oh] = -INFINITY;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    write_empty(a, b, hq, 1, kJoinWarps * 32);
     return;
   }
   const int h = hq / group, in = hq - h * group;
   const int row = h * head_tiles + in / C::kHeads, hh = in % C::kHeads;
-  const int64_t lo = first + (int64_t)row * units, hi = lo + units;
-  const int64_t nblk = blocks_used(W, grid);
+  const int64_t lo = all.below + (int64_t)row * units, hi = lo + units;
+  const int64_t nblk = blocks_used(all.W, grid);
   // the block that unit u lies in: the largest i with i*W/nblk <= u
-  const int64_t c0 = ((lo + 1) * nblk - 1) / W, c1 = (hi * nblk - 1) / W;
-  if (c0 == c1) return;  // written by its block
-  const Part<DP, NT> *parts = reinterpret_cast<const Part<DP, NT> *>(a.ws);
-  float M = -INFINITY;
-  for (int64_t i = c0; i <= c1; ++i) M = fmaxf(M, parts[i * 2 + (i == c0)].m[hh]);
-  const float m0 = M == -INFINITY ? 0.f : M;
-  // threads: kSplit groups over the parts, DP channels
-  constexpr int kSplit = 256 / DP;
-  const int d = threadIdx.x % DP, sg = threadIdx.x / DP;
-  float acc = 0.f, L = 0.f;
-  for (int64_t i = c0 + sg; i <= c1; i += kSplit) {
-    const Part<DP, NT> &p = parts[i * 2 + (i == c0)];
-    const float s = ex2(p.m[hh] - m0);
-    acc += s * p.o[hh][d];
-  }
-  for (int64_t i = c0; i <= c1; ++i) {
-    const Part<DP, NT> &p = parts[i * 2 + (i == c0)];
-    L += ex2(p.m[hh] - m0) * p.l[hh];
-  }
-  s_o[threadIdx.x] = acc;
-  __syncthreads();
-  if (sg) return;
-#pragma unroll
-  for (int s = 1; s < kSplit; ++s) acc += s_o[s * DP + d];
+  const int64_t c0 = ((lo + 1) * nblk - 1) / all.W, c1 = (hi * nblk - 1) / all.W;
+  const int n = (int)(c1 - c0) + 1;
+  const Part<DP, NT> *parts = reinterpret_cast<const Part<DP, NT> *>(a.ws) + c0 * 2;
   float osc = 1.f;
   if (ES == 1 && c.scale) osc = c.scale[a.layer * c.heads + h];
-  if (d < c.D) {
-    const __nv_bfloat16 v = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L * osc);
-    a.out[oh * c.D + d] = *reinterpret_cast<const uint16_t *>(&v);
+  // Every block waits, also one whose row is complete: what follows this grid in the
+  // stream waits for it alone, so it must not end before k_attend.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (n == 1) return;
+  // the first block's part is the one that begins the row (slot 1)
+  float om = -INFINITY, o[kVec], L = 0.f, M = -INFINITY;
+  if (warp < n) {  // this warp's first part, loaded together with the maxima
+    const Part<DP, NT> &p = parts[2 * warp + (warp == 0)];
+    om = p.m[hh];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) o[k] = p.o[hh][k * 32 + lane];
   }
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, parts[2 * i + (i == 0)].m[hh]);
+#pragma unroll
+  for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
+  const float m0 = M == -INFINITY ? 0.f : M;
+  for (int i = lane; i < n; i += 32) {
+    const Part<DP, NT> &p = parts[2 * i + (i == 0)];
+    L += ex2(p.m[hh] - m0) * p.l[hh];
+  }
+  float acc[kVec];
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) acc[k] = warp < n ? ex2(om - m0) * o[k] : 0.f;
+#pragma unroll 4
+  for (int i = warp + kJoinWarps; i < n; i += kJoinWarps) {
+    const Part<DP, NT> &p = parts[2 * i];
+    const float w = ex2(p.m[hh] - m0);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) acc[k] += w * p.o[hh][k * 32 + lane];
+  }
+#pragma unroll
+  for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(~0u, L, s);
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) s_o[warp][k * 32 + lane] = acc[k];
+  __syncthreads();
+  const int d = threadIdx.x;
+  if (d >= c.D) return;
+  float v = 0.f;
+  for (int w = 0; w < min(n, kJoinWarps); ++w) v += s_o[w][d];
+  const __nv_bfloat16 r = __float2bfloat16_rn(L == 0.f ? 0.f : v / L * osc);
+  a.out[oh * c.D + d] = *reinterpret_cast<const uint16_t *>(&r);
   if (d == 0 && a.lse) a.lse[oh] = (m0 + log2f(L)) * kLn2;
 }
 
 int sm_count() {
+  static std::atomic<int> known[64];  // by device; a device's SMs do not change
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed))) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
 template <int ES, int DP, int NT>
 cudaError_t run(const AttendArgs &a, int head_tiles, cudaStream_t st) {
   using C = Cfg<ES, DP, NT>;
-  auto kern = k_attend<ES, DP, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (!sms) return cudaErrorInvalidDevice;
   const int64_t rows = (int64_t)a.batch * a.c.heads * head_tiles;
   // a tile may start up to kTok - 1 tokens before the range
-  const int64_t units = rows * (((int64_t)a.max_len + C::kTok - 1 + C::kUnit - 1) / C::kUnit);
-  int64_t grid = (int64_t)sms * C::kPerSm;
-  if (grid > units / 2) grid = units / 2;
+  const int64_t row_units = ((int64_t)a.max_len + C::kTok - 1 + C::kUnit - 1) / C::kUnit;
+  const int64_t wave = (int64_t)sms * C::kPerSm;
+  if (row_units <= kRowUnits && rows <= wave) {
+    auto kern = k_attend<ES, DP, NT, true>;
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)rows, kThreads, C::kSmem, st>>>(a, head_tiles);
+    return cudaGetLastError();
+  }
+  auto kern = k_attend<ES, DP, NT, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  int64_t grid = rows * row_units / 2;
+  if (grid > wave) grid = wave;
   if (grid < 1) grid = 1;
   kern<<<(unsigned)grid, kThreads, C::kSmem, st>>>(a, head_tiles);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)a.batch * a.q_heads));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -679,7 +740,7 @@ cudaError_t run_d(const AttendArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-size_t attend_ws_bytes(const CacheView &c, int32_t, int32_t q_heads) {
+size_t attend_ws_bytes(const CacheView &c, int32_t q_heads) {
   const int sms = sm_count();
   if (!sms) return 0;
   const int heads = q_heads / c.heads <= 8 ? 8 : 16;

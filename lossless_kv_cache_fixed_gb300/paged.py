@@ -141,6 +141,7 @@ class Rope:
         self.struct = SkvRope(2 * freqs.numel(), self.axes,
                               SKV_ROPE_INTERLEAVED if interleaved else 0, 0, freqs.data_ptr(),
                               None if axis_of_pair is None else axis_of_pair.data_ptr())
+        self.ref = C.byref(self.struct)
 
 
 class PagedCache:
@@ -202,6 +203,12 @@ class PagedCache:
                                table.data_ptr(), refs.data_ptr(), self._status.data_ptr(),
                                None if scale is None else scale.data_ptr())
         self._ref = C.byref(self.struct)
+        self._index = self.device.index
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._int32, self._bf16, self._empty = torch.int32, torch.bfloat16, torch.empty
+        self._attend_bytes = {}    # workspace bytes by q_heads
+        self._pages_bytes = {}     # and of the page operations by n
+        self._default_scale = head_dim ** -0.5
         self._lib = lib()
         self._ws = {}
         if skv_cache_workspace_bytes(self.struct, 0) == 0:
@@ -212,7 +219,7 @@ class PagedCache:
     # -- helpers --
 
     def _stream(self):
-        return self.torch.cuda.current_stream(self.device).cuda_stream
+        return self._raw_stream(self._index)
 
     def _on(self, stream, tensors, call):
         """`call` with `stream` current: what it allocates belongs to that stream, and the
@@ -224,28 +231,30 @@ class PagedCache:
             return call()
 
     def _workspace(self, kind, stream, nbytes):
-        torch = self.torch
-        if torch.cuda.is_current_stream_capturing():
-            # belongs to the graph that is being captured
-            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        ws = self._ws.get((kind, stream))
+        capturing = self.torch.cuda.is_current_stream_capturing()
+        ws = None if capturing else self._ws.get((kind, stream))
         if ws is None or ws.numel() < nbytes:
-            ws = self._ws[kind, stream] = torch.empty(nbytes, dtype=torch.uint8,
-                                                      device=self.device)
+            ws = self.torch.empty(nbytes, dtype=self.torch.uint8, device=self.device)
+            if not capturing:       # a captured one belongs to its graph
+                self._ws[kind, stream] = ws
         return ws
 
     def _ints(self, what, n, *tensors):
+        i32 = self._int32
         for t in tensors:
-            if (t.dtype != self.torch.int32 or t.dim() != 1 or t.numel() != n or
-                    t.device != self.device or not t.is_contiguous()):
+            if (t.dtype is not i32 or t.dim() != 1 or t.numel() != n or
+                    t.get_device() != self._index or not t.is_contiguous()):
                 raise _bad("%s: int32 vectors of one length on the cache's device" % what)
 
     def _heads(self, what, t, n, heads=None):
-        if (t.dtype != self.torch.bfloat16 or t.dim() != 3 or t.shape[0] != n or
-                t.shape[2] != self.head_dim or t.device != self.device or
-                (heads is not None and t.shape[1] != heads) or
-                (t.stride(2) != 1 and t.numel())):
+        """Strides of a [tokens, heads, head_dim] tensor."""
+        shape = t.shape
+        st = t.stride()
+        if (t.dtype is not self._bf16 or len(shape) != 3 or shape[0] != n or
+                shape[2] != self.head_dim or t.get_device() != self._index or
+                (heads is not None and shape[1] != heads) or (st[2] != 1 and t.numel())):
             raise _bad("%s: bf16 [tokens, heads, head_dim], channels contiguous" % what)
+        return st
 
     def _check(self, rc, what):
         if rc:
@@ -270,7 +279,10 @@ class PagedCache:
     # -- pages --
 
     def _pages_ws(self, n, stream):
-        return self._workspace("pages", stream, skv_cache_workspace_bytes(self.struct, n))
+        nb = self._pages_bytes.get(n)
+        if nb is None:
+            nb = self._pages_bytes[n] = skv_cache_workspace_bytes(self.struct, n)
+        return self._workspace("pages", stream, nb)
 
     def reserve(self, slots, old_len, new_len, stream=None):
         """Pages for the tokens old_len .. new_len - 1 of each sequence."""
@@ -355,39 +367,37 @@ class PagedCache:
         strides that keep channels contiguous; q may be None) turned by rope at
         positions [axes, n], k and v written to place at[i] of sequence slots[i].
         Returns the turned q."""
-        torch = self.torch
         if stream is not None:
             return self._on(stream, (slots, at, q, k, v, positions, q_out,
                                      rope and rope.freqs, rope and rope.axis_of_pair),
                             lambda: self.append(layer, slots, at, q, k, v, rope, positions, q_out))
         n = slots.numel()
         self._ints("append", n, slots, at)
-        self._heads("append: k", k, n, self.heads)
-        self._heads("append: v", v, n, self.heads)
-        q_heads = 0
+        ks = self._heads("append: k", k, n, self.heads)
+        vs = self._heads("append: v", v, n, self.heads)
+        qs, q_heads, q_ptr, out_ptr = (0, 0), 0, None, None
         if q is not None:
-            self._heads("append: q", q, n)
+            qs = self._heads("append: q", q, n)
             q_heads = q.shape[1]
             if q_out is None:
-                q_out = torch.empty((n, q_heads, self.head_dim), dtype=q.dtype, device=q.device)
+                q_out = self._empty((n, q_heads, self.head_dim), dtype=self._bf16, device=self.device)
             else:
                 self._heads("append: q_out", q_out, n, q_heads)
                 if not q_out.is_contiguous():
                     raise _bad("append: q_out must be contiguous")
-        if rope is not None and (positions is None or positions.dtype != torch.int32 or
-                                 tuple(positions.shape) != (rope.axes, n) or
-                                 positions.device != self.device or
-                                 rope.freqs.device != self.device or
-                                 not positions.is_contiguous()):
-            raise _bad("append: positions must be contiguous int32 [axes, n]")
-        t = SkvTokens(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                      0 if q is None else q.stride(0), 0 if q is None else q.stride(1),
-                      k.stride(0), k.stride(1), v.stride(0), v.stride(1))
+            q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+        rope_ref = pos_ptr = None
+        if rope is not None:
+            if (positions is None or positions.dtype is not self._int32 or
+                    tuple(positions.shape) != (rope.axes, n) or
+                    positions.get_device() != self._index or
+                    rope.freqs.get_device() != self._index or not positions.is_contiguous()):
+                raise _bad("append: positions must be contiguous int32 [axes, n]")
+            rope_ref, pos_ptr = rope.ref, positions.data_ptr()
+        t = SkvTokens(q_ptr, k.data_ptr(), v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1])
         self._check(self._lib.skv_cache_append(
-            self._ref, layer, None if rope is None else C.byref(rope.struct), C.byref(t),
-            slots.data_ptr(), at.data_ptr(), None if rope is None else positions.data_ptr(), n,
-            q_heads, None if q is None else q_out.data_ptr(), self._stream()),
-            "skv_cache_append")
+            self._ref, layer, rope_ref, C.byref(t), slots.data_ptr(), at.data_ptr(), pos_ptr, n,
+            q_heads, out_ptr, self._stream()), "skv_cache_append")
         return q_out
 
     def attend(self, layer, slots, lens, q, max_len, begins=None, scale=None, out=None, lse=False,
@@ -396,7 +406,6 @@ class PagedCache:
         tokens begins[i] .. lens[i] - 1 of sequence slots[i] (max_len: no length is
         larger).  scale: default 1 / sqrt(head_dim).  Returns out [batch, q_heads, D],
         with lse=True also the log of the sum of exponentials [batch, q_heads]."""
-        torch = self.torch
         if stream is not None:
             return self._on(stream, (slots, lens, begins, q, out),
                             lambda: self.attend(layer, slots, lens, q, max_len, begins, scale,
@@ -405,24 +414,28 @@ class PagedCache:
         self._ints("attend", n, slots, lens)
         if begins is not None:
             self._ints("attend", n, begins)
-        self._heads("attend: q", q, n)
+        qs = self._heads("attend: q", q, n)
         q_heads = q.shape[1]
         if out is None:
-            out = torch.empty((n, q_heads, self.head_dim), dtype=q.dtype, device=q.device)
+            out = self._empty((n, q_heads, self.head_dim), dtype=self._bf16, device=self.device)
         else:
             self._heads("attend: out", out, n, q_heads)
             if not out.is_contiguous():
                 raise _bad("attend: out must be contiguous")
-        s = torch.empty((n, q_heads), dtype=torch.float32, device=q.device) if lse else None
+        s = None
+        if lse:
+            s = self._empty((n, q_heads), dtype=self.torch.float32, device=self.device)
+        nb = self._attend_bytes.get(q_heads)
+        if nb is None:
+            nb = skv_cache_attend_workspace_bytes(self.struct, n, q_heads)
+            if nb == 0:
+                raise _bad("attend: q_heads a multiple of the cache's heads, head_dim up to 256")
+            self._attend_bytes[q_heads] = nb
         st = self._stream()
-        nb = self._lib.skv_cache_attend_workspace_bytes(self._ref, n, q_heads)
-        if nb == 0:
-            raise _bad("attend: q_heads a multiple of the cache's heads, head_dim up to 256")
         ws = self._workspace("attend", st, nb)
         self._check(self._lib.skv_cache_attend(
             self._ref, layer, slots.data_ptr(), lens.data_ptr(),
-            None if begins is None else begins.data_ptr(), n, q.data_ptr(), q.stride(0),
-            q.stride(1), q_heads, self.head_dim ** -0.5 if scale is None else scale, max_len,
-            out.data_ptr(), None if s is None else s.data_ptr(), ws.data_ptr(), ws.numel(), st),
-            "skv_cache_attend")
+            None if begins is None else begins.data_ptr(), n, q.data_ptr(), qs[0], qs[1], q_heads,
+            self._default_scale if scale is None else scale, max_len, out.data_ptr(),
+            None if s is None else s.data_ptr(), ws.data_ptr(), nb, st), "skv_cache_attend")
         return (out, s) if lse else out
