@@ -625,14 +625,15 @@ size_t skv_cache_attend_workspace_bytes(const skv_cache *cache, int32_t batch, i
  *   q            device bf16, (i, head, channel) at q[i * q_stride + head *
  *                q_head_stride + channel]; strides multiples of 8, 16-byte aligned.
  *   q_heads      a multiple of heads.
- *   max_len      host: no lens[i] is larger (it sizes the launch).
+ *   max_len      host: no lens[i] is larger (it sizes the launch); batch *
+ *                q_heads * (max_len / 64 + 2) must be below 2^31.
  *   out          device bf16 [batch][q_heads][head_dim], 16-byte aligned; may be
  *                q itself when q has that layout.
  *   lse          device fp32 [batch][q_heads], or NULL.
  * head_dim up to 256.  Products and sums are fp32 (the matrix unit's), the weights
  * are rounded to bf16 (bf16 caches) or fp16 (e4m3 caches) before they meet the
  * values.  The result does not depend on what else runs: a row is split and
- * joined in a fixed order for given lens and device.  A slot, length or page
+ * joined in a fixed order for given lens, max_len and device.  A slot, length or page
  * out of range is reported (SKV_ERR_ARG); that row is empty, or that page's
  * tokens are left out. */
 int skv_cache_attend(const skv_cache *cache, int32_t layer, const int32_t *slots,

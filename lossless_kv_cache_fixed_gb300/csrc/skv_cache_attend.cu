@@ -148,11 +148,11 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int b, int tok, int
   return s;
 }
 
-// All units W of the batch; each lane owns `per` neighbouring entries with `mine`
-// units, `before` of all lie before them; `below` lie before entry `upto`.  One warp,
-// no block barrier: every warp of a block does the same.
+// All units W of the batch (below 2^31, checked by the host); each lane owns `per`
+// neighbouring entries with `mine` units, `before` of all lie before them; `below` lie
+// before entry `upto`.  One warp, no block barrier: every warp of a block does the same.
 struct Sums {
-  int64_t W, before, mine, below;
+  uint32_t W, before, mine, below;
   int per;
 };
 template <typename C>
@@ -160,31 +160,38 @@ __device__ __forceinline__ Sums sums_of(const AttendArgs &a, int HV, int upto, b
   const int lane = threadIdx.x & 31;
   Sums r;
   r.per = (a.batch + 31) / 32;
-  int64_t mine = 0, below = 0;
+  uint32_t mine = 0, below = 0;
   const int lo = lane * r.per, hi = min(lo + r.per, a.batch);
 #pragma unroll 4
   for (int b = lo; b < hi; ++b) {
-    const int64_t u = (int64_t)span_of(a, b, C::kTok, C::kUnit, tell).units * HV;
+    const uint32_t u = (uint32_t)span_of(a, b, C::kTok, C::kUnit, tell).units * HV;
     mine += u;
     if (b < upto) below += u;
   }
-  int64_t x = mine;
+  uint32_t x = mine;
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(~0u, x, o);
+    const uint32_t y = __shfl_up_sync(~0u, x, o);
     if (lane >= o) x += y;
-    below += __shfl_xor_sync(~0u, below, o);
   }
   r.W = __shfl_sync(~0u, x, 31);
   r.mine = mine;
   r.before = x - mine;
-  r.below = below;
+  r.below = __reduce_add_sync(~0u, below);
   return r;
 }
 
-// How the units are dealt: block c of `blocks` takes [c*W/blocks, (c+1)*W/blocks).
-__device__ __forceinline__ int64_t blocks_used(int64_t W, int64_t grid) {
-  const int64_t g = W / 2;  // at least two units each
-  return g < 1 ? 1 : g < grid ? g : grid;
+// How the units are dealt: block i of n takes [deal(i), deal(i + 1)), deal(i) =
+// floor(i * W / n) = i * (W / n) + floor(i * (W % n) / n); n is at most a wave of blocks.
+__device__ __forceinline__ uint32_t blocks_used(uint32_t W, uint32_t grid) {
+  return max(1u, min(W / 2, grid));  // at least two units each
+}
+__device__ __forceinline__ uint32_t deal(uint32_t W, uint32_t n, uint32_t i) {
+  const uint32_t q = W / n;
+  return i * q + i * (W - q * n) / n;
+}
+// the block that unit u lies in: the largest i with i * W / n <= u
+__device__ __forceinline__ int block_of(uint32_t W, uint32_t n, uint32_t u) {
+  return (int)((((uint64_t)u + 1) * n - 1) / W);
 }
 
 // Partial results: per block two slots of kHeads x (DP sums, maximum, sum of weights).
@@ -215,38 +222,38 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
   const int HV = c.heads * head_tiles;  // rows per batch entry
   const int group = a.q_heads / c.heads;
 
-  int64_t pos, stop, before = 0;
+  uint32_t pos, stop, before = 0;
   int b;
   if (ROWS) {
     b = blockIdx.x / HV;
-    const Span sp = span_of(a, b, C::kTok, C::kUnit, warp == 0 && blockIdx.x % HV == 0);
-    pos = (int64_t)(blockIdx.x - b * HV) * sp.units;
+    const int row = blockIdx.x - b * HV;
+    const Span sp = span_of(a, b, C::kTok, C::kUnit, warp == 0 && row == 0);
+    pos = row * sp.units;
     stop = pos + sp.units;
     if (!sp.units) {
-      const int row = blockIdx.x - b * HV, h = row / head_tiles;
-      const int h0 = h * group + (row - h * head_tiles) * C::kHeads;
+      const int h = row / head_tiles, h0 = h * group + (row - h * head_tiles) * C::kHeads;
       write_empty(a, b, h0, min(C::kHeads, h * group + group - h0), kThreads);
       return;
     }
   } else {
     // this block's share of the units
     const Sums all = sums_of<C>(a, HV, 0, blockIdx.x == 0 && warp == 0);
-    const int64_t nblk = blocks_used(all.W, gridDim.x);
-    if ((int64_t)blockIdx.x >= nblk) return;
-    pos = (int64_t)blockIdx.x * all.W / nblk;
-    stop = ((int64_t)blockIdx.x + 1) * all.W / nblk;
+    const uint32_t nblk = blocks_used(all.W, gridDim.x);
+    if (blockIdx.x >= nblk) return;
+    pos = deal(all.W, nblk, blockIdx.x);
+    stop = deal(all.W, nblk, blockIdx.x + 1);
     if (pos >= stop) return;
     // the batch entry b that unit `pos` lies in, and the units before that entry
     const int owner = __ffs(__ballot_sync(~0u, pos < all.before + all.mine)) - 1;
     before = __shfl_sync(~0u, all.before, owner);
     b = owner * all.per;
-    for (int b0 = b;; b0 += 32) {
+    for (int b0 = b; all.per > 1; b0 += 32) {
       const int bb = b0 + lane;
-      const int64_t u =
-          bb < a.batch ? (int64_t)span_of(a, bb, C::kTok, C::kUnit, false).units * HV : 0;
-      int64_t x = u;
+      const uint32_t u =
+          bb < a.batch ? (uint32_t)span_of(a, bb, C::kTok, C::kUnit, false).units * HV : 0;
+      uint32_t x = u;
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(~0u, x, o);
+        const uint32_t y = __shfl_up_sync(~0u, x, o);
         if (lane >= o) x += y;
       }
       const uint32_t hit = __ballot_sync(~0u, pos < before + x);
@@ -265,14 +272,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
 
   while (pos < stop) {
     Span sp = span_of(a, b, C::kTok, C::kUnit, false);
-    if (sp.units == 0 || pos >= before + (int64_t)sp.units * HV) {
-      before += (int64_t)sp.units * HV;
+    if (pos >= before + (uint32_t)sp.units * HV) {
+      before += (uint32_t)sp.units * HV;
       ++b;
       continue;
     }
-    const int row = (int)((pos - before) / sp.units);
-    const int u0 = (int)(pos - before - (int64_t)row * sp.units);
-    const int nu = (int)min((int64_t)(sp.units - u0), stop - pos);
+    const int row = (pos - before) / (uint32_t)sp.units;
+    const int u0 = pos - before - (uint32_t)row * sp.units;
+    const int nu = min((uint32_t)(sp.units - u0), stop - pos);
     pos += nu;
     const int h = row / head_tiles, h0 = h * group + (row - h * head_tiles) * C::kHeads;
     const int nh = min(C::kHeads, h * group + group - h0);  // query heads of this row
@@ -600,17 +607,17 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
 }
 
 // One block per (batch entry, query head): joins the parts of a row that lies in
-// several blocks and writes rows without tokens.  The warps take every kJoinWarps-th
-// part each and are added up in warp order.  It is launched while k_attend still runs
-// and finds its parts before it waits, so only the reading of the parts (one
-// round of loads for up to kJoinWarps of them) comes after k_attend's end.
-constexpr int kJoinWarps = 8;
-template <int ES, int DP, int NT>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_attend_join(AttendArgs a, int head_tiles,
-                                                                 int grid) {
+// several blocks and writes rows without tokens.  The warps take every WARPS-th part
+// each and are added up in warp order.  It is launched while k_attend still runs and
+// finds its parts before it waits, so only the reading of the parts (one round of
+// loads for up to kPre * WARPS of them) comes after k_attend's end.
+template <int ES, int DP, int NT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) k_attend_join(AttendArgs a, int head_tiles,
+                                                            int grid) {
   using C = Cfg<ES, DP, NT>;
   constexpr int kVec = DP / 32;  // channels per lane
-  __shared__ float s_o[kJoinWarps][DP];
+  constexpr int kPre = 32 / kVec > 4 ? 4 : 32 / kVec;  // parts a warp loads in the first round
+  __shared__ float s_o[WARPS][DP];
   const CacheView &c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int HV = c.heads * head_tiles;
@@ -619,63 +626,78 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attend_join(AttendArgs a, i
   const Sums all = sums_of<C>(a, HV, b, false);
   const int units = span_of(a, b, C::kTok, C::kUnit, false).units;
   const int64_t oh = (int64_t)b * a.q_heads + hq;
-  if (units == 0) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    write_empty(a, b, hq, 1, kJoinWarps * 32);
-    return;
-  }
   const int h = hq / group, in = hq - h * group;
   const int row = h * head_tiles + in / C::kHeads, hh = in % C::kHeads;
-  const int64_t lo = all.below + (int64_t)row * units, hi = lo + units;
-  const int64_t nblk = blocks_used(all.W, grid);
-  // the block that unit u lies in: the largest i with i*W/nblk <= u
-  const int64_t c0 = ((lo + 1) * nblk - 1) / all.W, c1 = (hi * nblk - 1) / all.W;
-  const int n = (int)(c1 - c0) + 1;
+  const uint32_t lo = all.below + (uint32_t)row * units, nblk = blocks_used(all.W, grid);
+  int c0 = 0, n = 0;
+  if (units) {
+    c0 = block_of(all.W, nblk, lo);
+    n = block_of(all.W, nblk, lo + units - 1) - c0 + 1;
+  }
+  // the first block's part is the one that begins the row (slot 1)
   const Part<DP, NT> *parts = reinterpret_cast<const Part<DP, NT> *>(a.ws) + c0 * 2;
   float osc = 1.f;
   if (ES == 1 && c.scale) osc = c.scale[a.layer * c.heads + h];
   // Every block waits, also one whose row is complete: what follows this grid in the
   // stream waits for it alone, so it must not end before k_attend.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (n == 1) return;
-  // the first block's part is the one that begins the row (slot 1)
-  float om = -INFINITY, o[kVec], L = 0.f, M = -INFINITY;
-  if (warp < n) {  // this warp's first part, loaded together with the maxima
-    const Part<DP, NT> &p = parts[2 * warp + (warp == 0)];
-    om = p.m[hh];
+  if (n == 0) write_empty(a, b, hq, 1, WARPS * 32);
+  if (n <= 1) return;
+  float pm[kPre], po[kPre][kVec];
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) o[k] = p.o[hh][k * 32 + lane];
+  for (int i = 0; i < kPre; ++i) {
+    const int k = warp + i * WARPS;
+    pm[i] = -INFINITY;
+    if (k < n) {
+      const Part<DP, NT> &p = parts[2 * k + (k == 0)];
+      pm[i] = p.m[hh];
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) po[i][v] = p.o[hh][v * 32 + lane];
+    }
   }
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, parts[2 * i + (i == 0)].m[hh]);
+  float m1 = -INFINITY, l1 = 0.f;  // of part `lane`
+  if (lane < n) {
+    const Part<DP, NT> &p = parts[2 * lane + (lane == 0)];
+    m1 = p.m[hh];
+    l1 = p.l[hh];
+  }
+  float M = m1;
+  for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, parts[2 * i].m[hh]);
 #pragma unroll
   for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
   const float m0 = M == -INFINITY ? 0.f : M;
-  for (int i = lane; i < n; i += 32) {
-    const Part<DP, NT> &p = parts[2 * i + (i == 0)];
-    L += ex2(p.m[hh] - m0) * p.l[hh];
-  }
+  float L = ex2(m1 - m0) * l1;
+  for (int i = lane + 32; i < n; i += 32) L += ex2(parts[2 * i].m[hh] - m0) * parts[2 * i].l[hh];
   float acc[kVec];
 #pragma unroll
-  for (int k = 0; k < kVec; ++k) acc[k] = warp < n ? ex2(om - m0) * o[k] : 0.f;
+  for (int v = 0; v < kVec; ++v) acc[v] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPre; ++i)
+    if (warp + i * WARPS < n) {
+      const float w = ex2(pm[i] - m0);
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) acc[v] += w * po[i][v];
+    }
 #pragma unroll 4
-  for (int i = warp + kJoinWarps; i < n; i += kJoinWarps) {
+  for (int i = warp + kPre * WARPS; i < n; i += WARPS) {
     const Part<DP, NT> &p = parts[2 * i];
     const float w = ex2(p.m[hh] - m0);
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) acc[k] += w * p.o[hh][k * 32 + lane];
+    for (int v = 0; v < kVec; ++v) acc[v] += w * p.o[hh][v * 32 + lane];
   }
 #pragma unroll
   for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(~0u, L, s);
 #pragma unroll
-  for (int k = 0; k < kVec; ++k) s_o[warp][k * 32 + lane] = acc[k];
+  for (int v = 0; v < kVec; ++v) s_o[warp][v * 32 + lane] = acc[v];
   __syncthreads();
-  const int d = threadIdx.x;
-  if (d >= c.D) return;
-  float v = 0.f;
-  for (int w = 0; w < min(n, kJoinWarps); ++w) v += s_o[w][d];
-  const __nv_bfloat16 r = __float2bfloat16_rn(L == 0.f ? 0.f : v / L * osc);
-  a.out[oh * c.D + d] = *reinterpret_cast<const uint16_t *>(&r);
-  if (d == 0 && a.lse) a.lse[oh] = (m0 + log2f(L)) * kLn2;
+  for (int d = threadIdx.x; d < c.D; d += WARPS * 32) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) v += s_o[w][d];
+    const __nv_bfloat16 r = __float2bfloat16_rn(L == 0.f ? 0.f : v / L * osc);
+    a.out[oh * c.D + d] = *reinterpret_cast<const uint16_t *>(&r);
+  }
+  if (threadIdx.x == 0 && a.lse) a.lse[oh] = (m0 + log2f(L)) * kLn2;
 }
 
 int sm_count() {
@@ -712,16 +734,21 @@ cudaError_t run(const AttendArgs &a, int head_tiles, cudaStream_t st) {
   if (grid > wave) grid = wave;
   if (grid < 1) grid = 1;
   kern<<<(unsigned)grid, kThreads, C::kSmem, st>>>(a, head_tiles);
+  // 8 warps for a row where few rows have many parts each; 2 where the rows are many, so
+  // that all blocks are resident at once when k_attend ends
+  const int64_t joins = (int64_t)a.batch * a.q_heads;
+  const bool wide = joins <= 3 * sms;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.batch * a.q_heads));
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.gridDim = dim3((unsigned)joins);
+  cfg.blockDim = dim3(wide ? 256 : 64);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_attend_join<ES, DP, NT>, a, head_tiles, (int)grid);
+  return wide ? cudaLaunchKernelEx(&cfg, k_attend_join<ES, DP, NT, 8>, a, head_tiles, (int)grid)
+              : cudaLaunchKernelEx(&cfg, k_attend_join<ES, DP, NT, 2>, a, head_tiles, (int)grid);
 }
 
 template <int ES, int DP>
