@@ -46,12 +46,17 @@ struct Cfg {
   static constexpr int kCpr = kRowB / 16;            // 16-byte chunks of it
   static constexpr int kTok = kRowB <= 128 ? 32 : 16;  // tokens of a warp tile
   static constexpr int kTile = kTok * kRowB;         // bytes of a tile of K or V
-  static constexpr int kStages = kTile <= 2048 ? 4 : 3;
+  // 2 stages leave room for 3 blocks (12 warps) per SM, which hide one another's latency:
+  // 107 us against 111 with 3 stages and 2 blocks for 32 rows of up to 16384 e4m3 tokens
+  static constexpr int kStages = kTile <= 2048 ? 4 : DP == 256 ? 3 : 2;
   static constexpr int kUnit = kWarps * kTok;        // tokens of a unit
   static constexpr int kSmem = kWarps * kStages * 2 * kTile;
-  static constexpr int kPerSm = kSmem > 110 * 1024 ? 1 : 2;
+  static constexpr int kPerSm = 220 * 1024 / (kSmem + 1024) < 4 ? 220 * 1024 / (kSmem + 1024) : 4;
   static constexpr int kHeads = 8 * NT;
-  static_assert(kWarps * kHeads * (DP + 2) * 4 <= kSmem, "the join of the warps reuses the stages");
+  // floats of a head's row where the warps are joined: the 4 padding floats put what a
+  // warp stores at once (8 channels of 4 heads) in different banks
+  static constexpr int kPad = DP + 4;
+  static_assert(kWarps * kHeads * (kPad + 2) * 4 <= kSmem, "the join of the warps reuses the stages");
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
@@ -60,6 +65,9 @@ __device__ __forceinline__ uint32_t smem_addr(const void *p) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
                : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -269,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
 
   const uint32_t tile0 = smem_addr(smem) + warp * (C::kStages * 2 * C::kTile);
   const bool whole = c.Tb % C::kTok == 0;  // a tile lies in one page
+  const bool plain = whole && c.row_bytes == C::kRowB;  // and is one run of bytes
 
   while (pos < stop) {
     Span sp = span_of(a, b, C::kTok, C::kUnit, false);
@@ -290,15 +299,31 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
     // set when a token in the range has no page: its rows are zeros and it is masked
     bool holes = false;
 
+    // block and token in it of this warp's next tile to load (tiles that lie in one page)
+    int ld_t = sp.start + (u0 * kWarps + warp) * C::kTok;
+    int ld_blk = ld_t / c.Tb, ld_off = ld_t - ld_blk * c.Tb;
+
+    auto advance = [&]() {
+      ld_t += C::kUnit;
+      ld_off += C::kUnit;
+      while (ld_off >= c.Tb) {
+        ld_off -= c.Tb;
+        ++ld_blk;
+      }
+    };
     auto load = [&](int u, int stage) {
-      const int t0 = sp.start + ((u0 + u) * kWarps + warp) * C::kTok;
+      const int t0 = ld_t;
       if (u < nu && t0 < sp.end) {
         const uint32_t sk = tile0 + stage * 2 * C::kTile, sv = sk + C::kTile;
         // byte offsets in the pool of row 0 (the tile lies in one page) or of row lane % kTok
-        const int t = whole ? t0 : min(t0 + lane % C::kTok, sp.end - 1);
-        const int blk = t / c.Tb;
+        int blk = ld_blk, tin = ld_off;
+        if (!whole) {
+          const int t = min(t0 + lane % C::kTok, sp.end - 1);
+          blk = t / c.Tb;
+          tin = t - blk * c.Tb;
+        }
         const uint32_t pk = tab_k[blk], pv = tab_v[blk];
-        const uint32_t off = (uint32_t)(t - blk * c.Tb) * c.row_bytes;
+        const uint32_t off = (uint32_t)tin * c.row_bytes;
         const bool has = pk < c.pages && pv < c.pages;
         if (__any_sync(~0u, !has)) {
           holes = true;
@@ -306,6 +331,21 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
         }
         const uint64_t bk = has ? (uint64_t)pk * c.page_bytes + off : 0;
         const uint64_t bv = has ? (uint64_t)pv * c.page_bytes + off : 0;
+        if (plain && has && t0 >= sp.begin && t0 + C::kTok <= sp.end) {
+          // the tile is one run of bytes and all of it counts: only constants are added
+          const uint8_t *gk = c.pool + bk + lane * 16, *gv = c.pool + bv + lane * 16;
+#pragma unroll
+          for (int i = 0; i < C::kTok * C::kCpr / 32; ++i) {
+            constexpr int kRows = 32 / C::kCpr > 0 ? 32 / C::kCpr : 1;  // rows an instruction covers
+            const uint32_t d = swz<C::kCpr>((i * kRows) % 8 + lane / C::kCpr, lane % C::kCpr) +
+                               (i * kRows) / 8 * 8 * C::kRowB;
+            cp_async16(sk + d, gk + i * 512);
+            cp_async16(sv + d, gv + i * 512);
+          }
+          cp_commit();
+          advance();
+          return;
+        }
 #pragma unroll
         for (int i = 0; i < C::kTok * C::kCpr / 32; ++i) {
           const int id = i * 32 + lane, r = id / C::kCpr, ch = id % C::kCpr;
@@ -327,6 +367,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
         }
       }
       cp_commit();
+      if (whole) advance();
+      else ld_t += C::kUnit;
     };
 
 #pragma unroll
@@ -546,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
 
     // join the warps in the stages' memory, then write the row or a partial result
     float *so = reinterpret_cast<float *>(smem);
-    float *sm = so + kWarps * C::kHeads * DP, *sl = sm + kWarps * C::kHeads;
+    float *sm = so + kWarps * C::kHeads * C::kPad, *sl = sm + kWarps * C::kHeads;
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -565,8 +607,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
         for (int d = 0; d < DP / 16; ++d) {
           const int d0 = ES == 2 ? d * 16 + g8 : d * 16 + 2 * g8;
           const int d1 = ES == 2 ? d0 + 8 : d0 + 1;
-          so[(warp * C::kHeads + hh) * DP + d0] = o[d][n][i];
-          so[(warp * C::kHeads + hh) * DP + d1] = o[d][n][i + 2];
+          so[(warp * C::kHeads + hh) * C::kPad + d0] = o[d][n][i];
+          so[(warp * C::kHeads + hh) * C::kPad + d1] = o[d][n][i + 2];
         }
       }
     __syncthreads();
@@ -574,28 +616,34 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
     Part<DP, NT> *part = reinterpret_cast<Part<DP, NT> *>(a.ws) + ((int64_t)blockIdx.x * 2 + (u0 == 0));
     float osc = 1.f;
     if (ES == 1 && c.scale) osc = c.scale[a.layer * c.heads + h];
-    for (int x = threadIdx.x; x < nh * DP; x += kThreads) {
-      const int hh = x / DP, d = x - hh * DP;
+    for (int x = threadIdx.x; x < nh * (DP / 4); x += kThreads) {
+      const int hh = x / (DP / 4), d = (x - hh * (DP / 4)) * 4;
       float M = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w * C::kHeads + hh]);
       const float m0 = M == -INFINITY ? 0.f : M;
-      float acc = 0.f, L = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      float L = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float s = ex2(sm[w * C::kHeads + hh] - m0);
-        acc += s * so[(w * C::kHeads + hh) * DP + d];
+        const float4 t = *reinterpret_cast<const float4 *>(so + (w * C::kHeads + hh) * C::kPad + d);
+        v.x += s * t.x;
+        v.y += s * t.y;
+        v.z += s * t.z;
+        v.w += s * t.w;
         L += s * sl[w * C::kHeads + hh];
       }
       if (done) {
         const int64_t oh = (int64_t)b * a.q_heads + h0 + hh;
         if (d < c.D) {
-          const __nv_bfloat16 v = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L * osc);
-          a.out[oh * c.D + d] = *reinterpret_cast<const uint16_t *>(&v);
+          const float r = L == 0.f ? 0.f : osc / L;
+          *reinterpret_cast<uint2 *>(a.out + oh * c.D + d) =
+              make_uint2(pack2<2>(v.x * r, v.y * r), pack2<2>(v.z * r, v.w * r));
         }
         if (d == 0 && a.lse) a.lse[oh] = (m0 + log2f(L)) * kLn2;
       } else {
-        part->o[hh][d] = acc;
+        *reinterpret_cast<float4 *>(&part->o[hh][d]) = v;
         if (d == 0) {
           part->m[hh] = M;
           part->l[hh] = L;
@@ -773,7 +821,7 @@ size_t attend_ws_bytes(const CacheView &c, int32_t q_heads) {
   const int heads = q_heads / c.heads <= 8 ? 8 : 16;
   const int DP = c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256;
   // two partial results for each of at most two blocks per SM
-  return (size_t)sms * 2 * 2 * heads * (DP + 2) * sizeof(float);
+  return (size_t)sms * 4 * 2 * heads * (DP + 2) * sizeof(float);
 }
 
 cudaError_t launch_attend(const AttendArgs &a, cudaStream_t st) {
