@@ -93,6 +93,7 @@ int skv_cache_status(const skv_cache *cache, skv_stream_t stream) {
       cudaMemsetAsync(c.status, 0, sizeof(v), st) != cudaSuccess ||
       cudaStreamSynchronize(st) != cudaSuccess)
     return SKV_ERR_CUDA;
+  if (v & kCacheStuck) return SKV_ERR_CUDA;
   if (v & kCacheArg) return SKV_ERR_ARG;
   return v & kCacheCapacity ? SKV_ERR_CAPACITY : SKV_OK;
 }
@@ -212,8 +213,8 @@ int skv_cache_append(const skv_cache *cache, int32_t layer, const skv_rope *rope
   if ((q_heads && (tokens->q_stride % 8 || tokens->q_head_stride % 8)) || tokens->k_stride % 8 ||
       tokens->k_head_stride % 8 || tokens->v_stride % 8 || tokens->v_head_stride % 8)
     return SKV_ERR_ARG;
-  // a block's units (up to 4 tokens x heads x 16-channel pieces) are 32-bit
-  if (((int64_t)q_heads + 2 * c.heads) * ((c.D + 15) / 16) > INT_MAX / 4) return SKV_ERR_ARG;
+  // the kernel's index arithmetic; a token's places and scales fit shared memory
+  if (c.D > 4096 || c.heads > 8192 || q_heads > 16384) return SKV_ERR_ARG;
   a.q = static_cast<const uint16_t *>(tokens->q);
   a.k = static_cast<const uint16_t *>(tokens->k);
   a.v = static_cast<const uint16_t *>(tokens->v);
