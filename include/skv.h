@@ -473,10 +473,10 @@ int skv_phi_table(uint32_t *table);
  *   flags        0.
  *   num_pages    pages in the pool, below 2^32 - 1.
  *   pool         device (16-byte aligned), [num_pages][page_tokens][head_dim].
- *   table        device, u32 [max_seqs][layers][2][heads][max_blocks]: page
- *                numbers, SKV_NO_PAGE where there is none.
- *   refs         device, u32 [num_pages]: how many table entries name the page;
- *                0 for a free page.
+ *   table        device (16-byte aligned), u32 [max_seqs][layers][2][heads]
+ *                [max_blocks]: page numbers, SKV_NO_PAGE where there is none.
+ *   refs         device (16-byte aligned), u32 [num_pages]: how many table
+ *                entries name the page; 0 for a free page.
  *   status       device, one u32, gathers errors.
  *   scale        device, e4m3 only: fp32 [layers][heads], the value of a code
  *                unit (keys and values are code * scale); NULL: 1.  Must be
@@ -503,7 +503,8 @@ int skv_cache_init(const skv_cache *cache, skv_stream_t stream);
 int skv_cache_status(const skv_cache *cache, skv_stream_t stream);
 
 /* Workspace bytes of skv_cache_reserve and skv_cache_fork with up to n
- * sequences and of skv_cache_compact (n = 0 is enough); 0 if invalid.  The
+ * sequences (4096 at most, in each list below) and of skv_cache_compact (n = 0 is
+ * enough); 0 if invalid.  The
  * workspace (256-byte aligned) holds nothing between calls. */
 size_t skv_cache_workspace_bytes(const skv_cache *cache, int32_t n);
 
@@ -541,7 +542,7 @@ int skv_cache_free(const skv_cache *cache, const int32_t *slots, int32_t n, skv_
 /* Close the holes: with n pages in use, those numbered n and above move to the
  * free numbers below n (the highest page to the lowest hole, the next one to
  * the next), and the tables follow.
- *   table_out, refs_out   device, shaped like table and refs, or both NULL: the
+ *   table_out, refs_out   device, like table and refs, or both NULL: the
  *                cache's own are changed in place.  With both given the cache's
  *                own stay as they are, and the pages they name too until a free
  *                number is reused: work in flight may still read through them.

@@ -48,7 +48,7 @@ __device__ __forceinline__ void st_stream(void *p, const uint4 &v) {
 
 // Workspace of the page operations, byte offsets (see skv_cache_pages.cu).
 struct PagesWs {
-  size_t need, base, bad, counts, list, rank, top_refs, total;
+  size_t go, base, need, bad, counts, list, rank, top_refs, total;
 };
 PagesWs pages_ws(uint64_t pages, int64_t n);
 

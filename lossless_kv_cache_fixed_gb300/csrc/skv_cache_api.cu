@@ -12,6 +12,7 @@ using namespace skv;
 namespace {
 
 constexpr size_t kAlign = 256;
+constexpr int32_t kMaxList = 4096;  // sequences of one page operation
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 cudaStream_t stream_of(skv_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 int status_of(cudaError_t e) { return e == cudaSuccess ? SKV_OK : SKV_ERR_CUDA; }
@@ -26,7 +27,7 @@ int make_view(const skv_cache *k, CacheView *out) {
   if (k->head_dim * (int64_t)size % 16) return SKV_ERR_ARG;
   if (k->num_pages == 0 || k->num_pages >= SKV_NO_PAGE) return SKV_ERR_ARG;
   if (!k->pool || !k->table || !k->refs || !k->status) return SKV_ERR_ARG;
-  if (!aligned(k->pool, 16) || !aligned(k->table, 4) || !aligned(k->refs, 4) ||
+  if (!aligned(k->pool, 16) || !aligned(k->table, 16) || !aligned(k->refs, 16) ||
       !aligned(k->status, 4) || !aligned(k->scale, 4))
     return SKV_ERR_ARG;
   if (k->scale && k->dtype != SKV_E4M3) return SKV_ERR_ARG;
@@ -59,7 +60,7 @@ int make_view(const skv_cache *k, CacheView *out) {
 // A list of n sequences for the page operations.
 int check_list(const CacheView &c, const int32_t *p, int32_t n) {
   (void)c;
-  if (n < 0 || n > 65535 || (n && !p) || !aligned(p, 4)) return SKV_ERR_ARG;
+  if (n < 0 || n > kMaxList || (n && !p) || !aligned(p, 4)) return SKV_ERR_ARG;
   return SKV_OK;
 }
 
@@ -100,7 +101,7 @@ int skv_cache_status(const skv_cache *cache, skv_stream_t stream) {
 
 size_t skv_cache_workspace_bytes(const skv_cache *cache, int32_t n) {
   CacheView c;
-  if (make_view(cache, &c) || n < 0 || n > 65535) return 0;
+  if (make_view(cache, &c) || n < 0 || n > kMaxList) return 0;
   return pages_ws(c.pages, n).total;
 }
 
@@ -144,7 +145,7 @@ int skv_cache_compact(const skv_cache *cache, uint32_t *table_out, uint32_t *ref
   CacheView c;
   int rc = make_view(cache, &c);
   if (rc) return rc;
-  if (!table_out != !refs_out || !aligned(table_out, 4) || !aligned(refs_out, 4))
+  if (!table_out != !refs_out || !aligned(table_out, 16) || !aligned(refs_out, 16))
     return SKV_ERR_ARG;
   if (!table_out) {
     table_out = c.table;

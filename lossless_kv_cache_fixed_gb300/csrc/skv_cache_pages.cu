@@ -2,64 +2,68 @@
 // free, compact, copy.
 //
 // The counts (refs) are the only record of which pages are free, so the k-th
-// lowest free page is a prefix sum over them: each block of k_count counts the
-// free pages of 4096 consecutive counts, k_free_list adds up the blocks before
-// its own and writes its pages to their places in a list, and the third kernel
-// hands them out by index.  No atomics decide an order, so the same cache gives
-// the same pages on every run.
+// lowest free page is a prefix sum over them.  k_check counts the free pages of each
+// kChunk consecutive counts and checks the request; in k_free_list each block adds up
+// the blocks before its own and writes its pages to their places in a list; the third
+// kernel hands them out by index.  No atomics decide an order, so the same cache gives
+// the same pages on every run.  Each of the first two is one round of loads and one
+// barrier deep (they are bound by latency), and every kernel here is launched while the
+// one before it still runs (programmatic dependent launch) and waits for its end before
+// its first read.
 #include "skv_cache.cuh"
 
 namespace skv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kPer = 16;                     // counts per thread
 constexpr int kChunk = kThreads * kPer;      // counts per block
-constexpr int kCheckSplit = 8;               // blocks that check one request
+constexpr int kPart = 2048;                  // table entries a block of k_check takes at once
+constexpr int kMostParts = 2048;             // blocks that check, in all (or one per sequence)
 constexpr int kUnit = 2048;                  // bytes a warp copies at a time
 constexpr size_t kWsAlign = 256;
 
 size_t up(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
 
-__device__ __forceinline__ uint64_t block_sum(uint64_t v) {
-  __shared__ uint64_t s[kThreads / 32];
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  uint64_t t = 0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) t += s[i];
-  __syncthreads();
-  return t;
+// First thing in every kernel.
+__device__ __forceinline__ void begin() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Exclusive prefix of v over the block's threads.
-__device__ __forceinline__ uint32_t block_prefix(uint32_t v) {
-  __shared__ uint32_t s[kThreads / 32];
+// Inclusive prefix over a warp.
+__device__ __forceinline__ uint32_t warp_prefix(uint32_t v) {
   const int lane = threadIdx.x & 31;
-  uint32_t x = v;
+#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    uint32_t y = __shfl_up_sync(~0u, x, o);
-    if (lane >= o) x += y;
+    const uint32_t y = __shfl_up_sync(~0u, v, o);
+    if (lane >= o) v += y;
   }
-  if (lane == 31) s[threadIdx.x >> 5] = x;
-  __syncthreads();
-  uint32_t before = 0;
-  for (int i = 0; i < (int)(threadIdx.x >> 5); ++i) before += s[i];
-  __syncthreads();
-  return before + x - v;
+  return v;
 }
 
-__device__ __forceinline__ uint64_t sum_of(const uint32_t *v, int64_t n) {
-  uint64_t t = 0;
-  for (int64_t i = threadIdx.x; i < n; i += kThreads) t += v[i];
-  return block_sum(t);
+// This thread's kPer counts from p on, 1 where there is none.
+__device__ __forceinline__ void counts_at(const CacheView &c, uint64_t p, uint32_t *v) {
+  if (p + kPer <= c.pages) {
+#pragma unroll
+    for (int i = 0; i < kPer / 4; ++i) {
+      const uint4 x = reinterpret_cast<const uint4 *>(c.refs + p)[i];
+      v[4 * i] = x.x;
+      v[4 * i + 1] = x.y;
+      v[4 * i + 2] = x.z;
+      v[4 * i + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = p + i < c.pages ? c.refs[p + i] : 1u;
+  }
 }
-
-__device__ __forceinline__ uint64_t sum_of(const uint64_t *v, int64_t n) {
-  uint64_t t = 0;
-  for (int64_t i = threadIdx.x; i < n; i += kThreads) t += v[i];
-  return block_sum(t);
+__device__ __forceinline__ uint32_t zeros(const uint32_t *v) {
+  uint32_t f = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) f += v[i] == 0;
+  return f;
 }
 
 // A request for pages: fork (parents given) or reserve.
@@ -104,112 +108,182 @@ __device__ __forceinline__ Item item_of(const CacheView &c, const Request &q, in
   return t;
 }
 
-// Blocks 0 .. n*kCheckSplit-1 check the requests, the others count free pages.
-// bad[i*kCheckSplit + s] is set or cleared by one block each; need[i] too.
-__global__ void __launch_bounds__(kThreads) k_count(CacheView c, Request q, uint64_t *need,
-                                                    uint32_t *bad, uint32_t *counts) {
-  const int64_t nb = (int64_t)q.n * kCheckSplit;
-  if ((int64_t)blockIdx.x >= nb) {
-    const uint64_t chunk = blockIdx.x - nb;
-    const uint64_t p0 = chunk * kChunk;
-    uint32_t f = 0;
-    for (int i = 0; i < kPer; ++i) {
-      const uint64_t p = p0 + (uint64_t)i * kThreads + threadIdx.x;
-      if (p < c.pages && c.refs[p] == 0) ++f;
-    }
-    const uint64_t t = block_sum(f);
-    if (threadIdx.x == 0) counts[chunk] = (uint32_t)t;
-    return;
-  }
-  const int i = blockIdx.x / kCheckSplit, part = blockIdx.x % kCheckSplit;
-  const Item t = item_of(c, q, i);
-  bool wrong = !t.ok;
-  // named twice, or as a parent as well
-  for (int j = part * kThreads + threadIdx.x; j < q.n; j += kCheckSplit * kThreads) {
-    if (j != i && q.slots[j] == t.slot) wrong = true;
-    if (q.parents && q.parents[j] == t.slot) wrong = true;
-  }
-  if (t.ok) {
-    // fork: the parent's blocks have pages, the child has none; reserve: the
-    // blocks to fill are empty
-    const int32_t lo = q.parents ? 0 : t.b0;
-    const int32_t width = q.parents ? c.blocks : t.nb;
-    const int32_t used = t.full + t.nb;
-    const uint32_t total = (uint32_t)c.rows * (uint32_t)width;
-    const uint32_t *own = c.table + (int64_t)t.slot * c.rows * c.blocks;
-    const uint32_t *par = c.table + (int64_t)(q.parents ? t.parent : 0) * c.rows * c.blocks;
-#pragma unroll 4
-    for (uint32_t k = part * kThreads + threadIdx.x; k < total; k += kCheckSplit * kThreads) {
-      const int64_t r = k / (uint32_t)width;
-      const int32_t b = lo + (int32_t)(k - (uint32_t)r * (uint32_t)width);
-      if (own[r * c.blocks + b] != kNoPage) wrong = true;
-      if (q.parents && b < used && par[r * c.blocks + b] >= c.pages) wrong = true;
-    }
-  }
-  const int any = __syncthreads_or(wrong);
-  if (threadIdx.x == 0) {
-    bad[blockIdx.x] = any ? 1u : 0u;
-    if (part == 0) need[i] = (uint64_t)c.rows * (uint64_t)t.nb;
-  }
-}
-
-// What k_free_list found: go != 0 where the request goes through, and the first
-// list index of each item (base).
+// What k_free_list found: *go != 0 where the request goes through, and the first list
+// index of each item (base).
 struct Go {
   uint32_t *go;
   uint32_t *base;
 };
 
-// Whether the request goes through: every check passed and there are pages enough.
-__device__ __forceinline__ uint32_t verdict(const Request &q, const uint64_t *need,
-                                            const uint32_t *bad, const uint32_t *counts,
-                                            int64_t nchunks, uint64_t *want) {
-  if (sum_of(bad, (int64_t)q.n * kCheckSplit)) return kCacheArg;
-  *want = sum_of(need, q.n);
-  if (*want == 0) return 0;
-  return sum_of(counts, nchunks) < *want ? kCacheCapacity : 0;
-}
+// Where k_check leaves what it found: need[i] pages for item i, bad[i*parts + part], free
+// pages of each chunk.
+struct Found {
+  uint32_t *need, *bad, *counts;
+  int parts;
+  int64_t chunks;
+};
 
-__global__ void __launch_bounds__(kThreads) k_free_list(CacheView c, Request q,
-                                                        const uint64_t *need, const uint32_t *bad,
-                                                        const uint32_t *counts, int64_t nchunks,
-                                                        Go go, uint32_t *list) {
-  uint64_t want = 0;
-  const uint32_t v = verdict(q, need, bad, counts, nchunks, &want);
-  if (blockIdx.x == 0) {
+// Blocks 0 .. chunks-1 count, block chunks + i*parts + part checks a part of item i: a
+// fork's parent has pages for the tokens and its child none, the entries that reserve
+// fills are empty, no slot is named twice.
+__global__ void __launch_bounds__(kThreads) k_check(CacheView c, Request q, Found f) {
+  begin();
+  if (blockIdx.x < f.chunks) {
+    __shared__ uint32_t s_f[kWarps];
+    uint32_t v[kPer];
+    counts_at(c, (uint64_t)blockIdx.x * kChunk + (uint64_t)threadIdx.x * kPer, v);
+    const uint32_t w = __reduce_add_sync(~0u, zeros(v));
+    if ((threadIdx.x & 31) == 0) s_f[threadIdx.x >> 5] = w;
+    __syncthreads();
     if (threadIdx.x == 0) {
-      *go.go = v ? 0u : 1u;
-      if (v) atomicOr(c.status, v);
+      uint32_t t = 0;
+      for (int i = 0; i < kWarps; ++i) t += s_f[i];
+      f.counts[blockIdx.x] = t;
     }
-    // the items' first list indices (below 2^32: want pages are free)
-    uint32_t sum = 0;
-    for (int i0 = 0; !v && i0 < q.n; i0 += kThreads) {
-      const int i = i0 + threadIdx.x;
-      const uint32_t x = i < q.n ? (uint32_t)need[i] : 0u;
-      const uint32_t before = block_prefix(x);
-      if (i < q.n) go.base[i] = sum + before;
-      sum += (uint32_t)block_sum(x);
+    return;
+  }
+  const uint32_t x = blockIdx.x - (uint32_t)f.chunks;
+  const int i = x / f.parts, part = x - i * f.parts;
+  const Item t = item_of(c, q, i);
+  bool wrong = !t.ok;
+  for (int j = part * kThreads + threadIdx.x; j < q.n; j += f.parts * kThreads) {
+    if (j != i && q.slots[j] == t.slot) wrong = true;
+    if (q.parents && q.parents[j] == t.slot) wrong = true;
+  }
+  const uint32_t entries = (uint32_t)c.rows * (uint32_t)c.blocks, blocks = c.blocks;
+  if (t.ok) {
+    const uint32_t *own = c.table + (int64_t)t.slot * entries;
+    if (!q.parents) {
+      for (uint32_t r = part * kThreads + threadIdx.x; r < (uint32_t)c.rows;
+           r += f.parts * kThreads)
+        for (int b = 0; b < t.nb; ++b) wrong |= own[(int64_t)r * blocks + t.b0 + b] != kNoPage;
+    } else {
+      const uint32_t *par = c.table + (int64_t)t.parent * entries;
+      const uint32_t used = t.full + t.nb;
+      if (entries % 4 == 0) {
+        for (uint64_t k = (uint64_t)part * kPart; k < entries; k += (uint64_t)f.parts * kPart) {
+          uint4 o[kPart / kThreads / 4], p[kPart / kThreads / 4];
+#pragma unroll
+          for (int y = 0; y < kPart / kThreads / 4; ++y) {
+            const uint64_t e = k + y * kThreads * 4 + threadIdx.x * 4;
+            if (e < entries) {
+              o[y] = *reinterpret_cast<const uint4 *>(own + e);
+              p[y] = *reinterpret_cast<const uint4 *>(par + e);
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < kPart / kThreads / 4; ++y) {
+            const uint64_t e = k + y * kThreads * 4 + threadIdx.x * 4;
+            if (e >= entries) continue;
+            wrong |= (o[y].x & o[y].y & o[y].z & o[y].w) != kNoPage;
+            uint32_t b = (uint32_t)e % blocks;
+            const uint32_t w[4] = {p[y].x, p[y].y, p[y].z, p[y].w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              wrong |= b < used && w[z] >= c.pages;
+              if (++b == blocks) b = 0;
+            }
+          }
+        }
+      } else {
+        for (uint64_t e = (uint64_t)part * kThreads + threadIdx.x; e < entries;
+             e += (uint64_t)f.parts * kThreads) {
+          wrong |= own[e] != kNoPage;
+          wrong |= (uint32_t)e % blocks < used && par[e] >= c.pages;
+        }
+      }
     }
   }
-  if (v) return;
-  if (!want) return;
-  const uint64_t before = sum_of(counts, blockIdx.x);
-  if (before >= want) return;
+  const int any = __syncthreads_or(wrong);
+  if (threadIdx.x == 0) {
+    f.bad[x] = any ? 1u : 0u;
+    if (part == 0) f.need[i] = (uint32_t)c.rows * (uint32_t)t.nb;  // below 2^31
+  }
+}
+
+// Blocks 0 .. chunks-1 list their free pages, the last block writes go, base and status.
+__global__ void __launch_bounds__(kThreads) k_free_list(CacheView c, Request q, Found f, Go go,
+                                                        uint32_t *list) {
+  __shared__ uint32_t s[6][kWarps];
+  begin();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t p0 = (uint64_t)blockIdx.x * kChunk + (uint64_t)threadIdx.x * kPer;
-  uint32_t mask = 0;
-  for (int i = 0; i < kPer; ++i)
-    if (p0 + i < c.pages && c.refs[p0 + i] == 0) mask |= 1u << i;
-  uint64_t k = before + block_prefix(__popc(mask));
-  for (int i = 0; i < kPer; ++i)
-    if (mask >> i & 1) {
-      if (k < want) list[k] = (uint32_t)(p0 + i);
-      ++k;
+  uint32_t v[kPer];
+  counts_at(c, p0, v);
+  // sums of need in two halves of 16 bits, each below 2^32 for 4096 items
+  uint32_t bad = 0, lo = 0, hi = 0, before = 0, all = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < q.n * f.parts; i += kThreads) bad |= f.bad[i];
+#pragma unroll 4
+  for (int i = threadIdx.x; i < q.n; i += kThreads) {
+    lo += f.need[i] & 0xffff;
+    hi += f.need[i] >> 16;
+  }
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < f.chunks; i += kThreads) {
+    const uint32_t x = f.counts[i];
+    all += x;
+    if (i < blockIdx.x) before += x;
+  }
+  const uint32_t mine = zeros(v), upto = warp_prefix(mine);
+  const uint32_t sums[5] = {__reduce_or_sync(~0u, bad), __reduce_add_sync(~0u, lo),
+                            __reduce_add_sync(~0u, hi), __reduce_add_sync(~0u, before),
+                            __reduce_add_sync(~0u, all)};
+  if (lane == 31) {
+#pragma unroll
+    for (int k = 0; k < 5; ++k) s[k][warp] = sums[k];
+    s[5][warp] = upto;
+  }
+  __syncthreads();
+  bad = lo = hi = before = all = 0;
+  uint32_t within = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    bad |= s[0][w];
+    lo += s[1][w];
+    hi += s[2][w];
+    before += s[3][w];
+    all += s[4][w];
+    if (w < warp) within += s[5][w];
+  }
+  const uint64_t want = lo + ((uint64_t)hi << 16);
+  const uint32_t verdict = bad ? kCacheArg : want > all ? kCacheCapacity : 0;
+  if (blockIdx.x < f.chunks) {
+    if (verdict) return;
+    uint64_t k = (uint64_t)before + within + upto - mine;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (v[i] == 0) {
+        if (k < want) list[k] = (uint32_t)(p0 + i);
+        ++k;
+      }
+    return;
+  }
+  if (threadIdx.x == 0) {
+    *go.go = verdict ? 0u : 1u;
+    if (verdict) atomicOr(c.status, verdict);
+  }
+  if (verdict) return;
+  uint32_t sum = 0;  // want is below 2^32
+  for (int i0 = 0; i0 < q.n; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
+    const uint32_t x = i < q.n ? f.need[i] : 0u, y = warp_prefix(x);
+    __syncthreads();
+    if (lane == 31) s[5][warp] = y;
+    __syncthreads();
+    uint32_t b = sum;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) b += s[5][w];
+      sum += s[5][w];
     }
+    if (i < q.n) go.base[i] = b + y - x;
+  }
 }
 
 // Hands out the pages: table entries and counts (reserve).
 __global__ void __launch_bounds__(kThreads) k_reserve(CacheView c, Request q, Go go,
                                                       const uint32_t *list) {
+  begin();
   if (!*go.go) return;
   const int i = blockIdx.y;
   const Item t = item_of(c, q, i);
@@ -230,6 +304,7 @@ __global__ void __launch_bounds__(kThreads) k_reserve(CacheView c, Request q, Go
 // a parent's page comes from HBM once and from L2 for its other children.
 __global__ void __launch_bounds__(kThreads) k_fork(CacheView c, Request q, Go go,
                                                    const uint32_t *list) {
+  begin();
   if (!*go.go) return;
   const uint32_t r = blockIdx.x / (uint32_t)q.n;
   const int i = (int)(blockIdx.x - r * (uint32_t)q.n);
@@ -250,20 +325,21 @@ __global__ void __launch_bounds__(kThreads) k_fork(CacheView c, Request q, Go go
   const uint8_t *src = c.pool + (uint64_t)par[t.full] * c.page_bytes;
   uint8_t *dst = c.pool + (uint64_t)p * c.page_bytes;
   const uint32_t bytes = (uint32_t)t.tail * c.row_bytes;
-  constexpr uint32_t kStep = kThreads * 16;
-  for (uint32_t o = threadIdx.x * 16; o < bytes; o += 4 * kStep) {
+  constexpr uint32_t kRow = kThreads * 16;
+  for (uint32_t o = threadIdx.x * 16; o < bytes; o += 4 * kRow) {
     uint4 v[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      if (o + u * kStep < bytes) v[u] = *reinterpret_cast<const uint4 *>(src + o + u * kStep);
+      if (o + u * kRow < bytes) v[u] = *reinterpret_cast<const uint4 *>(src + o + u * kRow);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      if (o + u * kStep < bytes) st_stream(dst + o + u * kStep, v[u]);
+      if (o + u * kRow < bytes) st_stream(dst + o + u * kRow, v[u]);
   }
 }
 
 // One thread per table entry of the slots given.
 __global__ void __launch_bounds__(kThreads) k_free(CacheView c, const int32_t *slots) {
+  begin();
   const int32_t slot = slots[blockIdx.y];
   if (slot < 0 || slot >= c.seqs) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(c.status, kCacheArg);
@@ -291,41 +367,77 @@ __global__ void __launch_bounds__(kThreads) k_free(CacheView c, const int32_t *s
 // h its rank from the top, so both sides are prefix sums and need not know how
 // many holes there are.
 
+struct CompactPlan {
+  uint64_t used, moves;
+};
+
 __global__ void __launch_bounds__(kThreads) k_compact_list(CacheView c, const uint32_t *counts,
-                                                           int64_t nchunks, uint32_t *holes,
+                                                           int64_t chunks, uint32_t *holes,
                                                            uint32_t *tops, uint32_t *rank,
-                                                           uint32_t *top_refs, uint64_t *moves) {
-  const uint64_t n = c.pages - sum_of(counts, nchunks);  // pages in use
-  const uint64_t free_before = sum_of(counts, blockIdx.x);
+                                                           uint32_t *top_refs, CompactPlan *plan) {
+  __shared__ uint32_t s[3][kWarps];
+  begin();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t p0 = (uint64_t)blockIdx.x * kChunk + (uint64_t)threadIdx.x * kPer;
   uint32_t v[kPer];
-  uint32_t f = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    v[i] = p0 + i < c.pages ? c.refs[p0 + i] : 1u;
-    f += v[i] == 0;
+  counts_at(c, p0, v);
+  uint32_t before = 0, all = 0;
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < chunks; i += kThreads) {
+    const uint32_t x = counts[i];
+    all += x;
+    if (i < blockIdx.x) before += x;
   }
-  uint64_t k = free_before + block_prefix(f);  // free pages below this thread's first
+  const uint32_t mine = zeros(v), upto = warp_prefix(mine);
+  const uint32_t sb = __reduce_add_sync(~0u, before), sa = __reduce_add_sync(~0u, all);
+  if (lane == 31) {
+    s[0][warp] = sb;
+    s[1][warp] = sa;
+    s[2][warp] = upto;
+  }
+  __syncthreads();
+  before = all = 0;
+  uint32_t within = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    before += s[0][w];
+    all += s[1][w];
+    if (w < warp) within += s[2][w];
+  }
+  const uint64_t n = c.pages - all;                  // pages in use
+  uint64_t k = (uint64_t)before + within + upto - mine;  // free pages below this thread's first
+  if (p0 == 0) {
+    plan->used = n;
+    if (n == c.pages) plan->moves = 0;
+  }
+  uint32_t r[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const uint64_t p = p0 + i;
-    // the number of holes: the free pages below n
-    if (p == n || (p + 1 == c.pages && n == c.pages)) *moves = p == n ? k : k + (v[i] == 0);
-    if (p < c.pages) {
-      uint32_t r = kNoPage;
-      if (p < n) {
-        if (v[i] == 0) {
-          r = (uint32_t)k;
-          holes[k] = (uint32_t)p;
-        }
-      } else if (v[i]) {
-        r = (uint32_t)(n - 1 - (p - k));  // p - k pages in use lie below p
-        tops[r] = (uint32_t)p;
-        top_refs[r] = v[i];
+    r[i] = kNoPage;
+    if (p >= c.pages) continue;
+    if (p == n) plan->moves = k;  // the holes: the free pages below n
+    if (p < n) {
+      if (v[i] == 0) {
+        r[i] = (uint32_t)k;
+        holes[k] = (uint32_t)p;
       }
-      rank[p] = r;
+    } else if (v[i]) {
+      r[i] = (uint32_t)(n - 1 - (p - k));  // p - k pages in use lie below p
+      tops[r[i]] = (uint32_t)p;
+      top_refs[r[i]] = v[i];
     }
     k += v[i] == 0;
+  }
+  if (p0 + kPer <= c.pages) {
+#pragma unroll
+    for (int i = 0; i < kPer / 4; ++i)
+      reinterpret_cast<uint4 *>(rank + p0)[i] =
+          make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (p0 + i < c.pages) rank[p0 + i] = r[i];
   }
 }
 
@@ -366,19 +478,20 @@ __device__ __forceinline__ void copy_units(const Copy &c, uint64_t moves, uint64
 }
 
 __global__ void __launch_bounds__(kThreads) k_copy(Copy c, int64_t n) {
+  begin();
   copy_units(c, (uint64_t)n, ((uint64_t)blockIdx.x * kThreads + threadIdx.x) >> 5,
              (uint64_t)gridDim.x * kThreads / 32);
 }
 
 // Moves the pages and rewrites counts and tables.  In place each thread reads
 // only the entries it writes: a moved page's count comes from top_refs.
-__global__ void __launch_bounds__(kThreads) k_compact(CacheView c, const uint32_t *counts,
-                                                      int64_t nchunks, const uint32_t *holes,
+__global__ void __launch_bounds__(kThreads) k_compact(CacheView c, const uint32_t *holes,
                                                       const uint32_t *tops, const uint32_t *rank,
                                                       const uint32_t *top_refs,
-                                                      const uint64_t *moves, uint32_t *table_out,
-                                                      uint32_t *refs_out) {
-  const uint64_t n = c.pages - sum_of(counts, nchunks);
+                                                      const CompactPlan *plan,
+                                                      uint32_t *table_out, uint32_t *refs_out) {
+  begin();
+  const uint64_t n = plan->used, moves = plan->moves;
   const uint64_t tid = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
   const uint64_t threads = (uint64_t)gridDim.x * kThreads;
   for (uint64_t p = tid; p < c.pages; p += threads) {
@@ -400,7 +513,7 @@ __global__ void __launch_bounds__(kThreads) k_compact(CacheView c, const uint32_
     table_out[k] = e;
   }
   const Copy m{c.pool, c.pool, tops, holes, c.pages, c.pages, c.page_bytes, c.status};
-  copy_units(m, *moves, tid >> 5, threads >> 5);
+  copy_units(m, moves, tid >> 5, threads >> 5);
 }
 
 int copy_grid(uint64_t units) {
@@ -411,17 +524,34 @@ int copy_grid(uint64_t units) {
 
 int64_t chunks_of(const CacheView &c) { return (int64_t)((c.pages + kChunk - 1) / kChunk); }
 
+// Launches with programmatic dependent launch.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kern)(P...), dim3 grid, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 }  // namespace
 
 PagesWs pages_ws(uint64_t pages, int64_t n) {
   PagesWs w;
   size_t o = 0;
-  w.need = o;  // also the number of moves of a compaction
-  o = up(o + sizeof(uint64_t) * (size_t)(n > 0 ? n : 1));
+  w.go = o;  // also a compaction's plan
+  o = up(o + 64);
   w.base = o;
-  o = up(o + sizeof(uint32_t) * (size_t)(n + 1));
+  o = up(o + sizeof(uint32_t) * (size_t)n);
+  w.need = o;
+  o = up(o + sizeof(uint32_t) * (size_t)n);
   w.bad = o;
-  o = up(o + sizeof(uint32_t) * (size_t)n * kCheckSplit);
+  o = up(o + sizeof(uint32_t) * (size_t)(n ? (n > kMostParts ? n : kMostParts) : 0));
   w.counts = o;
   o = up(o + sizeof(uint32_t) * (size_t)((pages + kChunk - 1) / kChunk));
   // the free list; or a compaction's holes and tops, which are at most half of the pages each
@@ -438,23 +568,23 @@ PagesWs pages_ws(uint64_t pages, int64_t n) {
 namespace {
 cudaError_t run_request(const CacheView &c, const Request &q, uint8_t *ws, cudaStream_t st) {
   const PagesWs w = pages_ws(c.pages, q.n);
-  uint64_t *need = reinterpret_cast<uint64_t *>(ws + w.need);
-  uint32_t *bad = reinterpret_cast<uint32_t *>(ws + w.bad);
-  uint32_t *counts = reinterpret_cast<uint32_t *>(ws + w.counts);
-  uint32_t *list = reinterpret_cast<uint32_t *>(ws + w.list);
-  const Go go{reinterpret_cast<uint32_t *>(ws + w.base) + q.n,
-              reinterpret_cast<uint32_t *>(ws + w.base)};
-  const int64_t nc = chunks_of(c);
-  k_count<<<(unsigned)(nc + (int64_t)q.n * kCheckSplit), kThreads, 0, st>>>(c, q, need, bad, counts);
-  k_free_list<<<(unsigned)nc, kThreads, 0, st>>>(c, q, need, bad, counts, nc, go, list);
-  if (q.parents) {
-    k_fork<<<(unsigned)(c.rows * q.n), kThreads, 0, st>>>(c, q, go, list);
-  } else {
-    const int64_t most = (c.rows * c.blocks + kThreads - 1) / kThreads;
-    k_reserve<<<dim3((unsigned)(most < 16 ? most : 16), (unsigned)q.n), kThreads, 0, st>>>(
-        c, q, go, list);
-  }
-  return cudaGetLastError();
+  auto at = [&](size_t o) { return reinterpret_cast<uint32_t *>(ws + o); };
+  const Go go{at(w.go), at(w.base)};
+  Found f{at(w.need), at(w.bad), at(w.counts), 1, chunks_of(c)};
+  // a block for each kPart entries (fork) or kThreads rows (reserve), kMostParts in all
+  const int64_t whole = q.parents ? (c.rows * c.blocks + kPart - 1) / kPart
+                                  : (c.rows + kThreads - 1) / kThreads;
+  const int64_t most = kMostParts / q.n > 1 ? kMostParts / q.n : 1;
+  f.parts = (int)(whole < most ? whole : most);
+  uint32_t *list = at(w.list);
+  cudaError_t e = launch(k_check, dim3((unsigned)(f.chunks + (int64_t)q.n * f.parts)), st, c, q, f);
+  if (e != cudaSuccess) return e;
+  e = launch(k_free_list, dim3((unsigned)(f.chunks + 1)), st, c, q, f, go, list);
+  if (e != cudaSuccess) return e;
+  if (q.parents) return launch(k_fork, dim3((unsigned)(c.rows * q.n)), st, c, q, go, list);
+  const int64_t blocks = (c.rows * c.blocks + kThreads - 1) / kThreads;
+  return launch(k_reserve, dim3((unsigned)(blocks < 16 ? blocks : 16), (unsigned)q.n), st, c, q,
+                go, list);
 }
 }  // namespace
 
@@ -470,28 +600,28 @@ cudaError_t launch_fork(const CacheView &c, const int32_t *parents, const int32_
 
 cudaError_t launch_free(const CacheView &c, const int32_t *slots, int32_t n, cudaStream_t st) {
   const int64_t most = (c.rows * c.blocks + kThreads - 1) / kThreads;
-  k_free<<<dim3((unsigned)(most < 128 ? most : 128), (unsigned)n), kThreads, 0, st>>>(c, slots);
-  return cudaGetLastError();
+  return launch(k_free, dim3((unsigned)(most < 128 ? most : 128), (unsigned)n), st, c, slots);
 }
 
 cudaError_t launch_compact(const CacheView &c, uint32_t *table_out, uint32_t *refs_out,
                            uint8_t *ws, cudaStream_t st) {
   const PagesWs w = pages_ws(c.pages, 0);
-  uint64_t *moves = reinterpret_cast<uint64_t *>(ws + w.need);
-  uint32_t *counts = reinterpret_cast<uint32_t *>(ws + w.counts);
+  CompactPlan *plan = reinterpret_cast<CompactPlan *>(ws + w.go);
   uint32_t *holes = reinterpret_cast<uint32_t *>(ws + w.list);
   uint32_t *tops = holes + (c.pages / 2 + 1);
   uint32_t *rank = reinterpret_cast<uint32_t *>(ws + w.rank);
   uint32_t *top_refs = reinterpret_cast<uint32_t *>(ws + w.top_refs);
-  const int64_t nc = chunks_of(c);
+  uint32_t *counts = reinterpret_cast<uint32_t *>(ws + w.counts);
   const Request none{nullptr, nullptr, nullptr, nullptr, 0};
-  k_count<<<(unsigned)nc, kThreads, 0, st>>>(c, none, nullptr, nullptr, counts);
-  k_compact_list<<<(unsigned)nc, kThreads, 0, st>>>(c, counts, nc, holes, tops, rank, top_refs,
-                                                    moves);
+  const Found f{nullptr, nullptr, counts, 1, chunks_of(c)};
+  cudaError_t e = launch(k_check, dim3((unsigned)f.chunks), st, c, none, f);
+  if (e != cudaSuccess) return e;
+  e = launch(k_compact_list, dim3((unsigned)f.chunks), st, c, counts, f.chunks, holes, tops, rank,
+             top_refs, plan);
+  if (e != cudaSuccess) return e;
   const uint64_t most = (c.pages / 2 + 1) * ((c.page_bytes + kUnit - 1) / kUnit);
-  k_compact<<<copy_grid(most), kThreads, 0, st>>>(c, counts, nc, holes, tops, rank, top_refs,
-                                                  moves, table_out, refs_out);
-  return cudaGetLastError();
+  return launch(k_compact, dim3((unsigned)copy_grid(most)), st, c, holes, tops, rank, top_refs,
+                plan, table_out, refs_out);
 }
 
 cudaError_t launch_copy_pages(const CacheView &c, const uint8_t *src_pool, uint64_t src_pages,
@@ -499,8 +629,7 @@ cudaError_t launch_copy_pages(const CacheView &c, const uint8_t *src_pool, uint6
                               const uint32_t *dst, int64_t n, cudaStream_t st) {
   const Copy m{src_pool, dst_pool, src, dst, src_pages, dst_pages, c.page_bytes, c.status};
   const uint64_t units = (uint64_t)n * ((c.page_bytes + kUnit - 1) / kUnit);
-  k_copy<<<copy_grid(units), kThreads, 0, st>>>(m, n);
-  return cudaGetLastError();
+  return launch(k_copy, dim3((unsigned)copy_grid(units)), st, m, n);
 }
 
 }  // namespace skv
