@@ -44,6 +44,30 @@ __device__ __forceinline__ void st_stream(void *p, const uint4 &v) {
                : "memory");
 }
 
+// Every kernel of the paged cache is launched while the one before it in the stream may
+// still run (programmatic dependent launch), which hides its launch, and calls begin()
+// (k_attend and k_attend_join: their own order of the two) before its first read: it
+// returns when all of the earlier work is complete.
+__device__ __forceinline__ void begin() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                   A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // ---- launchers (each enqueues on the stream and returns the launch status) ----
 
 // Workspace of the page operations, byte offsets (see skv_cache_pages.cu).

@@ -95,6 +95,7 @@ struct Unit {
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads, 5) k_append(AppendArgs a, Plan pl) {
   extern __shared__ __align__(16) uint8_t smem[];
+  begin();
   const CacheView &c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pairs = a.rotary / 2, kv = 2 * c.heads;
@@ -268,8 +269,7 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t st) {
                                          (int)smem);
     if (e != cudaSuccess) return e;
   }
-  kern<<<(unsigned)((a.n + p.toks - 1) / p.toks), kThreads, smem, st>>>(a, p);
-  return cudaGetLastError();
+  return launch(kern, dim3((unsigned)((a.n + p.toks - 1) / p.toks)), kThreads, smem, st, a, p);
 }
 
 }  // namespace skv

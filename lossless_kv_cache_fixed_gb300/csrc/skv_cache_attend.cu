@@ -127,6 +127,14 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// the upper halves of two floats, and what cutting p to its upper half leaves
+__device__ __forceinline__ uint32_t high2(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ float rest(float p) {
+  return fmaf(p, 1.f + 0x1p-18f, -__uint_as_float(__float_as_uint(p) & 0xffff0000u));
+}
+
 // byte offset of 16-byte chunk c of row r in a tile: chunks are permuted so that
 // the 8 rows one ldmatrix reads lie in 8 different bank groups
 template <int CPR>
@@ -223,7 +231,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
                                                                               int head_tiles) {
   using C = Cfg<ES, DP, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  if (!ROWS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // In this order: k_attend_join reads the lengths before it waits, and it is launched once
+  // every block here has seen the end of the work that wrote them.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const CacheView &c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int j = lane & 3, g8 = lane >> 2;
@@ -534,8 +545,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
             }
           }
       }
-      // P, its sum, and P as the B operand
-      uint32_t pf[C::kTok / 16][NT][2];
+      // P, its sum, and P as the B operand.  bf16 holds 8 bits of a weight, so a weight is
+      // cut to bf16 and what that leaves goes in a second bf16 operand (2^-16 in all; 57.3
+      // us with it and 57.2 without for 16 x 8192 tokens); fp16 holds 11 bits.  The rest
+      // is kept above 0 (p * 2^-18 more), so that no weight above 0 meets an infinite
+      // value as 0 times it.
+      uint32_t pf[C::kTok / 16][NT][2], pl[C::kTok / 16][NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
@@ -546,8 +561,15 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
           const float p2 = ex2(x[mt][n][2] - m0), p3 = ex2(x[mt][n][3] - m1);
           l[n][0] += p0 + p2;
           l[n][1] += p1 + p3;
-          pf[mt][n][0] = transpose8x8(pack2<ES>(p0, p1));
-          pf[mt][n][1] = transpose8x8(pack2<ES>(p2, p3));
+          if (ES == 2) {
+            pf[mt][n][0] = transpose8x8(high2(p0, p1));
+            pf[mt][n][1] = transpose8x8(high2(p2, p3));
+            pl[mt][n][0] = transpose8x8(pack2<ES>(rest(p0), rest(p1)));
+            pl[mt][n][1] = transpose8x8(pack2<ES>(rest(p2), rest(p3)));
+          } else {
+            pf[mt][n][0] = transpose8x8(pack2<ES>(p0, p1));
+            pf[mt][n][1] = transpose8x8(pack2<ES>(p2, p3));
+          }
         }
       }
       // O^T += V^T P^T
@@ -560,8 +582,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
             uint32_t t[4];
             ldsm4<true>(t, sv + swz<C::kCpr>(r, 2 * d + ((lane >> 3) & 1)));
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
               mma<ES>(o[d][n], t[0], t[1], t[2], t[3], pf[mt][n][0], pf[mt][n][1]);
+              mma<ES>(o[d][n], t[0], t[1], t[2], t[3], pl[mt][n][0], pl[mt][n][1]);
+            }
           }
         } else {
           const int r = mt * 16 + (lane & 15);
@@ -687,7 +711,8 @@ __global__ void __launch_bounds__(WARPS * 32) k_attend_join(AttendArgs a, int he
   float osc = 1.f;
   if (ES == 1 && c.scale) osc = c.scale[a.layer * c.heads + h];
   // Every block waits, also one whose row is complete: what follows this grid in the
-  // stream waits for it alone, so it must not end before k_attend.
+  // stream waits for it alone, so it must not end before k_attend.  (It does not let its
+  // successor start early: the next call's blocks would take the places of its own.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (n == 0) write_empty(a, b, hq, 1, WARPS * 32);
   if (n <= 1) return;
@@ -772,8 +797,7 @@ cudaError_t run(const AttendArgs &a, int head_tiles, cudaStream_t st) {
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)rows, kThreads, C::kSmem, st>>>(a, head_tiles);
-    return cudaGetLastError();
+    return launch(kern, dim3((unsigned)rows), kThreads, C::kSmem, st, a, head_tiles);
   }
   auto kern = k_attend<ES, DP, NT, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
@@ -781,22 +805,15 @@ cudaError_t run(const AttendArgs &a, int head_tiles, cudaStream_t st) {
   int64_t grid = rows * row_units / 2;
   if (grid > wave) grid = wave;
   if (grid < 1) grid = 1;
-  kern<<<(unsigned)grid, kThreads, C::kSmem, st>>>(a, head_tiles);
+  e = launch(kern, dim3((unsigned)grid), kThreads, C::kSmem, st, a, head_tiles);
+  if (e != cudaSuccess) return e;
   // 8 warps for a row where few rows have many parts each; 2 where the rows are many, so
   // that all blocks are resident at once when k_attend ends
   const int64_t joins = (int64_t)a.batch * a.q_heads;
   const bool wide = joins <= 3 * sms;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)joins);
-  cfg.blockDim = dim3(wide ? 256 : 64);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return wide ? cudaLaunchKernelEx(&cfg, k_attend_join<ES, DP, NT, 8>, a, head_tiles, (int)grid)
-              : cudaLaunchKernelEx(&cfg, k_attend_join<ES, DP, NT, 2>, a, head_tiles, (int)grid);
+  const dim3 jg((unsigned)joins);
+  return wide ? launch(k_attend_join<ES, DP, NT, 8>, jg, 256, 0, st, a, head_tiles, (int)grid)
+              : launch(k_attend_join<ES, DP, NT, 2>, jg, 64, 0, st, a, head_tiles, (int)grid);
 }
 
 template <int ES, int DP>

@@ -7,9 +7,7 @@
 // the blocks before its own and writes its pages to their places in a list; the third
 // kernel hands them out by index.  No atomics decide an order, so the same cache gives
 // the same pages on every run.  Each of the first two is one round of loads and one
-// barrier deep (they are bound by latency), and every kernel here is launched while the
-// one before it still runs (programmatic dependent launch) and waits for its end before
-// its first read.
+// barrier deep: they are bound by latency.
 #include "skv_cache.cuh"
 
 namespace skv {
@@ -25,12 +23,6 @@ constexpr int kUnit = 2048;                  // bytes a warp copies at a time
 constexpr size_t kWsAlign = 256;
 
 size_t up(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
-
-// First thing in every kernel.
-__device__ __forceinline__ void begin() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
 
 // Inclusive prefix over a warp.
 __device__ __forceinline__ uint32_t warp_prefix(uint32_t v) {
@@ -524,21 +516,6 @@ int copy_grid(uint64_t units) {
 
 int64_t chunks_of(const CacheView &c) { return (int64_t)((c.pages + kChunk - 1) / kChunk); }
 
-// Launches with programmatic dependent launch.
-template <typename... P, typename... A>
-cudaError_t launch(void (*kern)(P...), dim3 grid, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
-}
-
 }  // namespace
 
 PagesWs pages_ws(uint64_t pages, int64_t n) {
@@ -577,13 +554,13 @@ cudaError_t run_request(const CacheView &c, const Request &q, uint8_t *ws, cudaS
   const int64_t most = kMostParts / q.n > 1 ? kMostParts / q.n : 1;
   f.parts = (int)(whole < most ? whole : most);
   uint32_t *list = at(w.list);
-  cudaError_t e = launch(k_check, dim3((unsigned)(f.chunks + (int64_t)q.n * f.parts)), st, c, q, f);
+  cudaError_t e = launch(k_check, dim3((unsigned)(f.chunks + (int64_t)q.n * f.parts)), kThreads, 0, st, c, q, f);
   if (e != cudaSuccess) return e;
-  e = launch(k_free_list, dim3((unsigned)(f.chunks + 1)), st, c, q, f, go, list);
+  e = launch(k_free_list, dim3((unsigned)(f.chunks + 1)), kThreads, 0, st, c, q, f, go, list);
   if (e != cudaSuccess) return e;
-  if (q.parents) return launch(k_fork, dim3((unsigned)(c.rows * q.n)), st, c, q, go, list);
+  if (q.parents) return launch(k_fork, dim3((unsigned)(c.rows * q.n)), kThreads, 0, st, c, q, go, list);
   const int64_t blocks = (c.rows * c.blocks + kThreads - 1) / kThreads;
-  return launch(k_reserve, dim3((unsigned)(blocks < 16 ? blocks : 16), (unsigned)q.n), st, c, q,
+  return launch(k_reserve, dim3((unsigned)(blocks < 16 ? blocks : 16), (unsigned)q.n), kThreads, 0, st, c, q,
                 go, list);
 }
 }  // namespace
@@ -600,7 +577,7 @@ cudaError_t launch_fork(const CacheView &c, const int32_t *parents, const int32_
 
 cudaError_t launch_free(const CacheView &c, const int32_t *slots, int32_t n, cudaStream_t st) {
   const int64_t most = (c.rows * c.blocks + kThreads - 1) / kThreads;
-  return launch(k_free, dim3((unsigned)(most < 128 ? most : 128), (unsigned)n), st, c, slots);
+  return launch(k_free, dim3((unsigned)(most < 128 ? most : 128), (unsigned)n), kThreads, 0, st, c, slots);
 }
 
 cudaError_t launch_compact(const CacheView &c, uint32_t *table_out, uint32_t *refs_out,
@@ -614,13 +591,13 @@ cudaError_t launch_compact(const CacheView &c, uint32_t *table_out, uint32_t *re
   uint32_t *counts = reinterpret_cast<uint32_t *>(ws + w.counts);
   const Request none{nullptr, nullptr, nullptr, nullptr, 0};
   const Found f{nullptr, nullptr, counts, 1, chunks_of(c)};
-  cudaError_t e = launch(k_check, dim3((unsigned)f.chunks), st, c, none, f);
+  cudaError_t e = launch(k_check, dim3((unsigned)f.chunks), kThreads, 0, st, c, none, f);
   if (e != cudaSuccess) return e;
-  e = launch(k_compact_list, dim3((unsigned)f.chunks), st, c, counts, f.chunks, holes, tops, rank,
+  e = launch(k_compact_list, dim3((unsigned)f.chunks), kThreads, 0, st, c, counts, f.chunks, holes, tops, rank,
              top_refs, plan);
   if (e != cudaSuccess) return e;
   const uint64_t most = (c.pages / 2 + 1) * ((c.page_bytes + kUnit - 1) / kUnit);
-  return launch(k_compact, dim3((unsigned)copy_grid(most)), st, c, holes, tops, rank, top_refs,
+  return launch(k_compact, dim3((unsigned)copy_grid(most)), kThreads, 0, st, c, holes, tops, rank, top_refs,
                 plan, table_out, refs_out);
 }
 
@@ -629,7 +606,7 @@ cudaError_t launch_copy_pages(const CacheView &c, const uint8_t *src_pool, uint6
                               const uint32_t *dst, int64_t n, cudaStream_t st) {
   const Copy m{src_pool, dst_pool, src, dst, src_pages, dst_pages, c.page_bytes, c.status};
   const uint64_t units = (uint64_t)n * ((c.page_bytes + kUnit - 1) / kUnit);
-  return launch(k_copy, dim3((unsigned)copy_grid(units)), st, m, n);
+  return launch(k_copy, dim3((unsigned)copy_grid(units)), kThreads, 0, st, m, n);
 }
 
 }  // namespace skv

@@ -140,6 +140,22 @@ def test_special_values_inside_the_range():
     assert torch.all(torch.isnan(out)) and math.isnan(float(lse))
 
 
+def test_infinite_values_inside_the_range():
+    c = filled(0, 1, 1, 64, 16, 1, 40)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = torch.randn(1, 4, 64, generator=g, device="cuda").bfloat16()
+    want = c.attend(0, ints([0]), ints([40]), q, 40)
+    v = lambda t: c.pool.view(torch.bfloat16)[int(c.table[0, 0, 1, 0, t // 16]), t % 16]  # noqa: E731
+    for t in range(0, 40, 3):
+        v(t)[5], v(t)[9] = math.inf, -math.inf
+    v(0)[11], v(1)[11] = math.inf, -math.inf
+    out = c.attend(0, ints([0]), ints([40]), q, 40)
+    assert torch.all(out[0, :, 5] == math.inf) and torch.all(out[0, :, 9] == -math.inf)
+    assert torch.all(torch.isnan(out[0, :, 11]))
+    rest = [d for d in range(64) if d not in (5, 9, 11)]
+    assert torch.equal(out[0, :, rest], want[0, :, rest])
+
+
 @pytest.mark.parametrize("dtype", [0, 1], ids=["bf16", "e4m3"])
 def test_large_and_growing_scores(dtype):
     """Scores that grow along the row by far more than the slack of the running maximum,
@@ -277,3 +293,31 @@ def test_two_streams_at_once():
     for i in (0, 1):
         assert all(torch.equal(want[i], o) for o in got[i])
     c.status()
+
+
+def test_lengths_and_queries_written_just_before():
+    """The lengths, the queries and the pages come from work that is enqueued right before
+    the call, on the same stream, without a wait: long rows that are split and joined."""
+    c = filled(1, 1, 2, 128, 128, 2, 9000)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q0 = torch.randn(2, 16, 128, generator=g, device="cuda")
+    slots = ints([0, 1])
+    cases = [([9000, 17], 1.0), ([64, 9000], 0.5), ([8999, 8999], 2.0), ([0, 5000], 1.0)]
+    want = []
+    for n, f in cases:
+        want.append(c.attend(0, slots, ints(n), (q0 * f).bfloat16(), 9000, lse=True))
+        torch.cuda.synchronize()
+    slow = torch.randn(4096, 4096, device="cuda")
+    lens, q = ints([0, 0]), torch.zeros(2, 16, 128, device="cuda").bfloat16()
+    new = [ints(n) for n, _ in cases]
+    got = []
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for i, (n, f) in enumerate(cases):
+            slow = slow @ slow * 1e-3
+            lens.copy_(new[i])
+            q.copy_(q0 * f)
+            got.append((i, c.attend(0, slots, lens, q, 9000, lse=True)))
+    torch.cuda.synchronize()
+    for i, (o, l) in got:
+        assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
