@@ -35,12 +35,11 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRowUnits = 8;  // rows of up to so many units are not cut (see run)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;  // x may pass m by this before the sums are rescaled (p <= 2^8)
 
-template <int ES, int DP, int NT>
+template <int ES, int DP, int NT, bool ROWS>
 struct Cfg {
   static constexpr int kRowB = DP * ES;              // bytes of a token's row in shared memory
   static constexpr int kCpr = kRowB / 16;            // 16-byte chunks of it
@@ -48,7 +47,7 @@ struct Cfg {
   static constexpr int kTile = kTok * kRowB;         // bytes of a tile of K or V
   // 2 stages leave room for 3 blocks (12 warps) per SM, which hide one another's latency:
   // 107 us against 111 with 3 stages and 2 blocks for 32 rows of up to 16384 e4m3 tokens
-  static constexpr int kStages = kTile <= 2048 ? 4 : DP == 256 ? 3 : 2;
+  static constexpr int kStages = ROWS ? 3 : kTile <= 2048 ? 4 : DP == 256 ? 3 : 2;
   static constexpr int kUnit = kWarps * kTok;        // tokens of a unit
   static constexpr int kSmem = kWarps * kStages * 2 * kTile;
   static constexpr int kPerSm = 220 * 1024 / (kSmem + 1024) < 4 ? 220 * 1024 / (kSmem + 1024) : 4;
@@ -227,9 +226,9 @@ __device__ __forceinline__ void write_empty(const AttendArgs &a, int b, int h0, 
 
 // ROWS: block i takes row i whole (entry i / HV); otherwise the units are dealt.
 template <int ES, int DP, int NT, bool ROWS>
-__global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(AttendArgs a,
+__global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT, ROWS>::kPerSm)) k_attend(AttendArgs a,
                                                                               int head_tiles) {
-  using C = Cfg<ES, DP, NT>;
+  using C = Cfg<ES, DP, NT, ROWS>;
   extern __shared__ __align__(128) uint8_t smem[];
   // In this order: k_attend_join reads the lengths before it waits, and it is launched once
   // every block here has seen the end of the work that wrote them.
@@ -686,9 +685,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
 template <int ES, int DP, int NT, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32) k_attend_join(AttendArgs a, int head_tiles,
                                                             int grid) {
-  using C = Cfg<ES, DP, NT>;
+  using C = Cfg<ES, DP, NT, false>;
   constexpr int kVec = DP / 32;  // channels per lane
-  constexpr int kPre = 32 / kVec > 4 ? 4 : 32 / kVec;  // parts a warp loads in the first round
+  constexpr int kMost = WARPS == 8 ? 8 : 4;
+  constexpr int kPre = 32 / kVec > kMost ? kMost : 32 / kVec;  // parts a warp loads at first
   __shared__ float s_o[WARPS][DP];
   const CacheView &c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -785,19 +785,24 @@ int sm_count() {
 
 template <int ES, int DP, int NT>
 cudaError_t run(const AttendArgs &a, int head_tiles, cudaStream_t st) {
-  using C = Cfg<ES, DP, NT>;
+  using C = Cfg<ES, DP, NT, false>;
   const int sms = sm_count();
   if (!sms) return cudaErrorInvalidDevice;
   const int64_t rows = (int64_t)a.batch * a.c.heads * head_tiles;
   // a tile may start up to kTok - 1 tokens before the range
   const int64_t row_units = ((int64_t)a.max_len + C::kTok - 1 + C::kUnit - 1) / C::kUnit;
   const int64_t wave = (int64_t)sms * C::kPerSm;
-  if (row_units <= kRowUnits && rows <= wave) {
+  using R = Cfg<ES, DP, NT, true>;
+  // Rows are not cut where one block takes little longer for one than the cut, the second
+  // launch and the join do: with 8 rows of 128 channels 5.6 us against 6.3 at 5 units and
+  // 7.9 against 6.4 at 9, with 64 rows 8.5 against 9.0 at 9 and 13.1 against 9.8 at 17, with
+  // 256 rows 19.5 against 22.2 at 17 (bf16, 8 query heads a row).
+  if (row_units <= 5 + rows / 16 && rows <= (int64_t)sms * R::kPerSm) {
     auto kern = k_attend<ES, DP, NT, true>;
     cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
     if (e != cudaSuccess) return e;
-    return launch(kern, dim3((unsigned)rows), kThreads, C::kSmem, st, a, head_tiles);
+    return launch(kern, dim3((unsigned)rows), kThreads, R::kSmem, st, a, head_tiles);
   }
   auto kern = k_attend<ES, DP, NT, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
@@ -807,10 +812,11 @@ cudaError_t run(const AttendArgs &a, int head_tiles, cudaStream_t st) {
   if (grid < 1) grid = 1;
   e = launch(kern, dim3((unsigned)grid), kThreads, C::kSmem, st, a, head_tiles);
   if (e != cudaSuccess) return e;
-  // 8 warps for a row where few rows have many parts each; 2 where the rows are many, so
-  // that all blocks are resident at once when k_attend ends
+  // 8 warps for a row where few rows have many parts each (one row of 131071 tokens: 48.8
+  // us against 51.3); 2 where the rows are many, so that all blocks are resident at once
+  // when k_attend ends (128 rows of 8192 tokens: 59.6 us against 63.6)
   const int64_t joins = (int64_t)a.batch * a.q_heads;
-  const bool wide = joins <= 3 * sms;
+  const bool wide = joins <= sms;
   const dim3 jg((unsigned)joins);
   return wide ? launch(k_attend_join<ES, DP, NT, 8>, jg, 256, 0, st, a, head_tiles, (int)grid)
               : launch(k_attend_join<ES, DP, NT, 2>, jg, 64, 0, st, a, head_tiles, (int)grid);
