@@ -606,7 +606,7 @@ typedef struct {
  * sequence alone (count 1: skv_cache_reserve gives such pages and a fork never
  * shares one that is not full); otherwise it is reported (SKV_ERR_ARG) and not
  * written.  Two tokens with the same place: one of the two is kept.
- * head_dim up to 4096, up to 8192 heads and 16384 query heads. */
+ * head_dim up to 4096, q_heads + 2 * heads up to 8192. */
 int skv_cache_append(const skv_cache *cache, int32_t layer, const skv_rope *rope,
                      const skv_tokens *tokens, const int32_t *slots, const int32_t *at,
                      const int32_t *positions, int32_t n, int32_t q_heads, void *q_out,

@@ -214,8 +214,8 @@ int skv_cache_append(const skv_cache *cache, int32_t layer, const skv_rope *rope
   if ((q_heads && (tokens->q_stride % 8 || tokens->q_head_stride % 8)) || tokens->k_stride % 8 ||
       tokens->k_head_stride % 8 || tokens->v_stride % 8 || tokens->v_head_stride % 8)
     return SKV_ERR_ARG;
-  // the kernel's index arithmetic; a token's places and scales fit shared memory
-  if (c.D > 4096 || c.heads > 8192 || q_heads > 16384) return SKV_ERR_ARG;
+  // the kernel's index arithmetic; a token's rows and scales fit shared memory
+  if (c.D > 4096 || (int64_t)q_heads + 2ll * c.heads > 8192) return SKV_ERR_ARG;
   a.q = static_cast<const uint16_t *>(tokens->q);
   a.k = static_cast<const uint16_t *>(tokens->k);
   a.v = static_cast<const uint16_t *>(tokens->v);

@@ -13,8 +13,16 @@
 // A block takes a few tokens.  Their units of 16 channels (two 16-byte vectors: the two
 // halves of 8 pairs, or 16 neighbouring channels) are cut into tasks of 32 units of one
 // kind for a warp -- q or k channels that turn, q, k or v channels that pass -- so no
-// warp diverges; a task's vectors are loaded before the one before it is turned, the
-// first ones before the block forms its angles and looks up its pages.
+// warp diverges; where each (token, head) is read from and goes to lies in shared
+// memory, so a unit costs one division by multiplication and few address operations
+// (the kernel is 60% of the way to being bound by its instructions).  A task's vectors
+// are loaded before the one before it is turned, the first ones before the block forms
+// its angles and looks up its pages.
+//
+// 8190 tokens of 64 + 8 + 8 heads of 128 (336 MB): 53.3 us, 6.3 TB/s; 16001 tokens of
+// 32 + 8 + 8 heads into e4m3 (361 MB): 62.8 us, 5.7 TB/s.  Loading two or three tasks
+// ahead, or passing the tokens through shared memory by bulk copies, is slower (63 to 75
+// us and 75 to 115 us): more of the registers or of the SM's memory per warp, fewer warps.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -23,9 +31,14 @@
 namespace skv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kToks = 4;  // tokens of a block
+// Blocks per SM (bounds the registers) and units of a block, for bf16 and e4m3 caches:
+// 54.6 and 68.5 us with 9 and 8 blocks, 75.8 and 73.8 with 11 and 10 (the two calls above);
+// 55.6 and 63.6 with 1024 units, 66.2 with 2048 (e4m3).
+constexpr int kBlocks[2] = {10, 9};
+constexpr int kUnits[2] = {640, 1536};
+constexpr int kMostToks = 16;
 
 __device__ __forceinline__ void unpack(const uint4 &v, float *x) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -70,14 +83,23 @@ __device__ __forceinline__ uint32_t div_of(uint32_t x, const Div &v) {
   return v.magic ? __umulhi(x, v.magic) : x;
 }
 
-// How the work is cut (built by the host).
-struct Plan {
-  int toks;           // tokens of a block
-  int units, turned;  // 16-channel units of a head, those that turn
-  Div by_units, by_turned, by_pass, by_q, by_kv;
+// The kinds of units.  A block's rows are its tokens' q heads, then their k heads, then
+// their v heads (token-major in each).
+enum { kQTurn, kKTurn, kQPass, kKPass, kV, kKinds };
+struct Kind {
+  int task0, n;      // its first task, its units
+  int per, from;     // units of a row, the first of them
+  uint32_t magic;    // of per
+  int row0;          // its first row
+  int turns, q;
 };
 
-enum Kind { kQTurn, kKTurn, kQPass, kKPass, kV, kKinds };
+// How the work is cut (built by the host).
+struct Plan {
+  int toks;           // tokens of a block, at most 16
+  int units, turned;  // 16-channel units of a head, those that turn
+  Div by_units, by_turned, by_pass;
+};
 
 // (a, b) turned by (cos, sin).
 __device__ __forceinline__ void turn(float &a, float &b, float co, float s) {
@@ -86,57 +108,77 @@ __device__ __forceinline__ void turn(float &a, float &b, float co, float s) {
   b = x * s + y * co;
 }
 
-// One lane's unit of a task.
+// One lane's unit of a task: its vectors, row and place in the row; row < 0: none.
 struct Unit {
   uint4 v0, v1;
-  int kind, tk, h, u;  // kind < 0: none
+  int row, u, kind, tk;
 };
 
 template <bool E4M3>
-__global__ void __launch_bounds__(kThreads, 5) k_append(AppendArgs a, Plan pl) {
+__global__ void __launch_bounds__(kThreads, kBlocks[E4M3]) k_append(AppendArgs a, Plan pl) {
   extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ Kind kinds[kKinds];
   begin();
   const CacheView &c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pairs = a.rotary / 2, kv = 2 * c.heads;
-  float2 *cs = reinterpret_cast<float2 *>(smem);                            // [toks][pairs], see below
-  uint64_t *dsts = reinterpret_cast<uint64_t *>(cs + pl.toks * pairs);      // [toks][2][heads]
-  float *invs = reinterpret_cast<float *>(dsts + pl.toks * kv);             // [heads], e4m3
+  const int pairs = a.rotary / 2, kv = 2 * c.heads, heads = a.q_heads + kv;
+  float2 *cs = reinterpret_cast<float2 *>(smem);                        // [toks][pairs], see below
+  uint64_t *srcs = reinterpret_cast<uint64_t *>(cs + pl.toks * pairs);  // [rows]: address | token
+  uint64_t *dsts = srcs + pl.toks * heads;                              // [rows], 0: nowhere
+  float *invs = reinterpret_cast<float *>(dsts + pl.toks * heads);      // [heads], e4m3
   const int64_t i0 = (int64_t)blockIdx.x * pl.toks;
   const int nt = (int)min((int64_t)pl.toks, (int64_t)a.n - i0);
+  const int nq = nt * a.q_heads, nk = nt * c.heads;
   const int passing = pl.units - pl.turned;
-
-  // tasks [0, e0) are of kind 0, [e0, e1) of kind 1, ...
-  const int n0 = nt * a.q_heads * pl.turned, n1 = nt * c.heads * pl.turned;
-  const int n2 = nt * a.q_heads * passing, n3 = nt * c.heads * passing;
-  const int n4 = nt * c.heads * pl.units;
-  const int e0 = (n0 + 31) / 32, e1 = e0 + (n1 + 31) / 32, e2 = e1 + (n2 + 31) / 32;
-  const int e3 = e2 + (n3 + 31) / 32, e4 = e3 + (n4 + 31) / 32;
+  // tasks of each kind in turn, 32 units each
+  const int e0 = (nq * pl.turned + 31) / 32, e1 = e0 + (nk * pl.turned + 31) / 32;
+  const int e2 = e1 + (nq * passing + 31) / 32, e3 = e2 + (nk * passing + 31) / 32;
+  const int e4 = e3 + (nk * pl.units + 31) / 32;
+  if (threadIdx.x < kKinds) {
+    const int k = threadIdx.x;
+    Kind x;
+    x.turns = k == kQTurn || k == kKTurn;
+    x.q = k == kQTurn || k == kQPass;
+    x.per = x.turns ? pl.turned : k == kV ? pl.units : passing;
+    x.from = k == kQPass || k == kKPass ? pl.turned : 0;
+    x.magic = (x.turns ? pl.by_turned : k == kV ? pl.by_units : pl.by_pass).magic;
+    x.n = (x.q ? nq : nk) * x.per;
+    x.task0 = k == kQTurn ? 0 : k == kKTurn ? e0 : k == kQPass ? e1 : k == kKPass ? e2 : e3;
+    x.row0 = x.q ? 0 : k == kV ? nq + nk : nq;
+    kinds[k] = x;
+  }
+  for (int x = threadIdx.x; x < nt * heads; x += kThreads) {
+    const uint16_t *p;
+    int tk;
+    if (x < nq) {
+      tk = x / a.q_heads;
+      p = a.q + (i0 + tk) * a.qs + (x - tk * a.q_heads) * a.qhs;
+      dsts[x] = reinterpret_cast<uint64_t>(a.q_out + (i0 * a.q_heads + x) * c.D);
+    } else {
+      const int y = x - nq < nk ? x - nq : x - nq - nk;
+      tk = y / c.heads;
+      const int h = y - tk * c.heads;
+      p = x - nq < nk ? a.k + (i0 + tk) * a.ks + h * a.khs : a.v + (i0 + tk) * a.vs + h * a.vhs;
+    }
+    srcs[x] = reinterpret_cast<uint64_t>(p) | (uint64_t)tk;  // 16-byte aligned
+  }
+  __syncthreads();
 
   auto fetch = [&](int task) {
     Unit t;
-    t.kind = -1;
+    t.row = -1;
     if (task >= e4) return t;
-    int kind, x, n;
-    if (task < e0) kind = kQTurn, x = task, n = n0;
-    else if (task < e1) kind = kKTurn, x = task - e0, n = n1;
-    else if (task < e2) kind = kQPass, x = task - e1, n = n2;
-    else if (task < e3) kind = kKPass, x = task - e2, n = n3;
-    else kind = kV, x = task - e3, n = n4;
-    x = x * 32 + lane;
-    if (x >= n) return t;
-    const bool turns = kind <= kKTurn, q = kind == kQTurn || kind == kQPass;
-    const int th = div_of(x, turns ? pl.by_turned : kind == kV ? pl.by_units : pl.by_pass);
-    t.u = x - th * (turns ? pl.turned : kind == kV ? pl.units : passing);
-    if (kind == kQPass || kind == kKPass) t.u += pl.turned;
-    t.tk = div_of(th, q ? pl.by_q : pl.by_kv);
-    t.h = th - t.tk * (q ? a.q_heads : c.heads);
-    t.kind = kind;
-    const int64_t i = i0 + t.tk;
-    const uint16_t *src = q             ? a.q + i * a.qs + t.h * a.qhs
-                          : kind == kV  ? a.v + i * a.vs + t.h * a.vhs
-                                        : a.k + i * a.ks + t.h * a.khs;
-    const bool halves = turns && !a.interleaved;
+    t.kind = (task >= e0) + (task >= e1) + (task >= e2) + (task >= e3);
+    const Kind k = kinds[t.kind];
+    const uint32_t x = (task - k.task0) * 32 + lane;
+    if (x >= (uint32_t)k.n) return t;
+    const uint32_t r = k.magic ? __umulhi(x, k.magic) : x;
+    t.u = x - r * k.per + k.from;
+    t.row = k.row0 + r;
+    const uint64_t s = srcs[t.row];
+    t.tk = (int)(s & 15);
+    const uint16_t *src = reinterpret_cast<const uint16_t *>(s & ~15ull);
+    const bool halves = k.turns && !a.interleaved;
     const int d0 = halves ? 8 * t.u : 16 * t.u, d1 = halves ? d0 + pairs : d0 + 8;
     t.v0 = __ldcs(reinterpret_cast<const uint4 *>(src + d0));
     t.v1 = d1 < c.D ? __ldcs(reinterpret_cast<const uint4 *>(src + d1)) : make_uint4(0, 0, 0, 0);
@@ -145,15 +187,16 @@ __global__ void __launch_bounds__(kThreads, 5) k_append(AppendArgs a, Plan pl) {
 
   Unit next = fetch(warp);
 
-  // the tokens' angles, and where their keys and values go (0: nowhere)
-  for (int x = threadIdx.x; x < nt * kv; x += kThreads) {
-    const int tk = x / kv, r = x - tk * kv;
+  // where the tokens' keys and values go (0: nowhere), and the tokens' angles
+  for (int x = threadIdx.x; x < 2 * nk; x += kThreads) {
+    const int side = x >= nk, y = x - side * nk, tk = y / c.heads, h = y - tk * c.heads;
     const int32_t slot = a.slots[i0 + tk], at = a.at[i0 + tk], blk = at / c.Tb;
     uint64_t dst = 0;
     bool bad = slot >= 0;
     if (slot >= 0 && slot < c.seqs && at >= 0 && blk < c.blocks) {
       const uint32_t page =
-          c.table[((int64_t)slot * c.rows + (int64_t)a.layer * kv + r) * c.blocks + blk];
+          c.table[((int64_t)slot * c.rows + ((int64_t)a.layer * 2 + side) * c.heads + h) *
+                      c.blocks + blk];
       if (page < c.pages && c.refs[page] == 1) {
         bad = false;
         dst = reinterpret_cast<uint64_t>(c.pool + (uint64_t)page * c.page_bytes +
@@ -161,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 5) k_append(AppendArgs a, Plan pl) {
       }
     }
     if (bad) atomicOr(c.status, kCacheArg);
-    dsts[x] = dst;
+    dsts[nq + x] = dst;
   }
   if (E4M3)
     for (int h = threadIdx.x; h < c.heads; h += kThreads)
@@ -188,12 +231,10 @@ __global__ void __launch_bounds__(kThreads, 5) k_append(AppendArgs a, Plan pl) {
   for (int task = warp; task < e4; task += kWarps) {
     const Unit t = next;
     next = fetch(task + kWarps);
-    if (t.kind < 0) continue;
-    const bool turns = t.kind <= kKTurn, q = t.kind == kQTurn || t.kind == kQPass;
-    uint8_t *o = q ? reinterpret_cast<uint8_t *>(a.q_out + ((i0 + t.tk) * a.q_heads + t.h) * c.D)
-                   : reinterpret_cast<uint8_t *>(
-                         dsts[t.tk * kv + (t.kind == kV ? c.heads : 0) + t.h]);
+    if (t.row < 0) continue;
+    uint8_t *o = reinterpret_cast<uint8_t *>(dsts[t.row]);
     if (!o) continue;
+    const bool turns = t.kind <= kKTurn, q = t.kind == kQTurn || t.kind == kQPass;
     const bool halves = turns && !a.interleaved;
     const int d0 = halves ? 8 * t.u : 16 * t.u, d1 = halves ? d0 + pairs : d0 + 8;
     if (!turns && (q || !E4M3)) {
@@ -225,7 +266,8 @@ __global__ void __launch_bounds__(kThreads, 5) k_append(AppendArgs a, Plan pl) {
       }
     }
     if (E4M3 && !q) {
-      const float inv = invs[t.h];
+      const int y = t.row - nq < nk ? t.row - nq : t.row - nq - nk;
+      const float inv = invs[y - t.tk * c.heads];
       const uint2 c0 = pack_e4m3(x0, inv), c1 = pack_e4m3(x1, inv);
       if (halves) {
         __stcs(reinterpret_cast<uint2 *>(o + d0), c0);
@@ -252,16 +294,16 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t st) {
   Plan p;
   p.units = (c.D + 15) / 16;
   p.turned = a.rotary / 16;
-  // one token per block while that fills no more than a wave of blocks, and where its units
-  // are many (div_of)
+  // tokens of a block: one while these fill no more than a wave of blocks, else as many as
+  // make kUnits units
   const int64_t units = ((int64_t)a.q_heads + 2 * c.heads) * p.units;
-  p.toks = a.n <= 152 * 4 || units > 4096 ? 1 : kToks;
+  const int64_t toks = a.n <= 152 * 8 ? 1 : (kUnits[c.dtype == 1] + units / 2) / units;
+  p.toks = (int)(toks < 1 ? 1 : toks > kMostToks ? kMostToks : toks);
   p.by_units = make_div(p.units);
   p.by_turned = make_div(p.turned);
   p.by_pass = make_div(p.units - p.turned);
-  p.by_q = make_div(a.q_heads);
-  p.by_kv = make_div(c.heads);
-  const size_t smem = (size_t)p.toks * (sizeof(float2) * pairs + sizeof(uint64_t) * 2 * c.heads) +
+  const size_t heads = (size_t)a.q_heads + 2 * (size_t)c.heads;
+  const size_t smem = (size_t)p.toks * (sizeof(float2) * pairs + 2 * sizeof(uint64_t) * heads) +
                       (c.dtype == 1 ? sizeof(float) * (size_t)c.heads : 0);
   auto kern = c.dtype == 1 ? k_append<true> : k_append<false>;
   if (smem > 48 * 1024) {
