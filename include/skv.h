@@ -476,7 +476,7 @@ int skv_phi_table(uint32_t *table);
  *   table        device (16-byte aligned), u32 [max_seqs][layers][2][heads]
  *                [max_blocks]: page numbers, SKV_NO_PAGE where there is none.
  *   refs         device (16-byte aligned), u32 [num_pages]: how many table
- *                entries name the page; 0 for a free page.
+ *                entries name the page (below 2^31); 0 for a free page.
  *   status       device, one u32, gathers errors.
  *   scale        device, e4m3 only: fp32 [layers][heads], the value of a code
  *                unit (keys and values are code * scale); NULL: 1.  Must be
@@ -629,7 +629,7 @@ size_t skv_cache_attend_workspace_bytes(const skv_cache *cache, int32_t batch, i
  *                q_head_stride + channel]; strides multiples of 8, 16-byte aligned.
  *   q_heads      a multiple of heads.
  *   max_len      host: no lens[i] is larger (it sizes the launch); batch *
- *                q_heads * (max_len / 64 + 2) must be below 2^31.
+ *                q_heads * (max_len / 64 + 4) must be below 2^31.
  *   out          device bf16 [batch][q_heads][head_dim], 16-byte aligned; may be
  *                q itself when q has that layout.
  *   lse          device fp32 [batch][q_heads], or NULL.

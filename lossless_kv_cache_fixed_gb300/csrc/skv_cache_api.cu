@@ -250,11 +250,11 @@ int skv_cache_attend(const skv_cache *cache, int32_t layer, const int32_t *slots
   if (int rc = make_view(cache, &a.c)) return rc;
   const CacheView &c = a.c;
   if (layer < 0 || layer >= c.layers || batch < 0 || q_heads <= 0 || q_heads % c.heads ||
-      c.D > 256 || max_len < 0 || max_len > INT_MAX - 256)
+      c.D > 256 || max_len < 0 || max_len > INT_MAX - 1024)
     return SKV_ERR_ARG;
   // one block of the join per (entry, query head); the units of all rows are 32-bit
   if ((int64_t)batch * q_heads > INT_MAX ||
-      (int64_t)batch * q_heads * (max_len / 64 + 2) > INT_MAX)
+      (int64_t)batch * q_heads * (max_len / 64 + 4) > INT_MAX)
     return SKV_ERR_ARG;
   if (!batch) return SKV_OK;
   if (!slots || !lens || !q || !out || !aligned(slots, 4) || !aligned(lens, 4) ||

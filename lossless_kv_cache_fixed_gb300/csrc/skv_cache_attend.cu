@@ -15,7 +15,7 @@
 //     block-wide barrier; the block's 4 warps are joined once per row;
 //   - a row that lies in several blocks leaves a partial result in each (at most
 //     two per block) and is joined by k_attend_join, in block order;
-//   - a batch of few short rows is not cut: one block per row and no join.
+//   - a batch of short rows is not cut: one block per row and no join.
 // The products run on the matrix units transposed, tokens as rows and the group's
 // query heads as the 8 columns of m16n8k16: S^T = K Q^T, O^T = V^T P^T, so a
 // group of up to 8 heads wastes no row and the running maximum, the sum and O^T
@@ -35,11 +35,14 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+// A row costs a block this many units more than it has: the stages run empty and the warps
+// are joined between two rows.
+constexpr int kRowCost = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;  // x may pass m by this before the sums are rescaled (p <= 2^8)
 
-template <int ES, int DP, int NT, bool ROWS>
+template <int ES, int DP, int NT>
 struct Cfg {
   static constexpr int kRowB = DP * ES;              // bytes of a token's row in shared memory
   static constexpr int kCpr = kRowB / 16;            // 16-byte chunks of it
@@ -47,7 +50,7 @@ struct Cfg {
   static constexpr int kTile = kTok * kRowB;         // bytes of a tile of K or V
   // 2 stages leave room for 3 blocks (12 warps) per SM, which hide one another's latency:
   // 107 us against 111 with 3 stages and 2 blocks for 32 rows of up to 16384 e4m3 tokens
-  static constexpr int kStages = ROWS ? 3 : kTile <= 2048 ? 4 : DP == 256 ? 3 : 2;
+  static constexpr int kStages = kTile <= 2048 ? 4 : DP == 256 ? 3 : 2;
   static constexpr int kUnit = kWarps * kTok;        // tokens of a unit
   static constexpr int kSmem = kWarps * kStages * 2 * kTile;
   static constexpr int kPerSm = 220 * 1024 / (kSmem + 1024) < 4 ? 220 * 1024 / (kSmem + 1024) : 4;
@@ -145,7 +148,7 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 // The tokens [begin, end) of batch entry b, its first tile's start and its units.
 struct Span {
   int32_t slot, begin, end, start;
-  int32_t units;
+  int32_t units, cost;  // cost: units as they are dealt (see kRowCost)
 };
 __device__ __forceinline__ Span span_of(const AttendArgs &a, int b, int tok, int unit, bool tell) {
   Span s;
@@ -160,6 +163,7 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int b, int tok, int
   if (bad || s.slot < 0 || s.begin >= s.end) s.begin = s.end = 0;
   s.start = s.begin / tok * tok;
   s.units = (s.end - s.start + unit - 1) / unit;
+  s.cost = s.units ? s.units + kRowCost : 0;
   return s;
 }
 
@@ -179,7 +183,7 @@ __device__ __forceinline__ Sums sums_of(const AttendArgs &a, int HV, int upto, b
   const int lo = lane * r.per, hi = min(lo + r.per, a.batch);
 #pragma unroll 4
   for (int b = lo; b < hi; ++b) {
-    const uint32_t u = (uint32_t)span_of(a, b, C::kTok, C::kUnit, tell).units * HV;
+    const uint32_t u = (uint32_t)span_of(a, b, C::kTok, C::kUnit, tell).cost * HV;
     mine += u;
     if (b < upto) below += u;
   }
@@ -226,9 +230,9 @@ __device__ __forceinline__ void write_empty(const AttendArgs &a, int b, int h0, 
 
 // ROWS: block i takes row i whole (entry i / HV); otherwise the units are dealt.
 template <int ES, int DP, int NT, bool ROWS>
-__global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT, ROWS>::kPerSm)) k_attend(AttendArgs a,
+__global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(AttendArgs a,
                                                                               int head_tiles) {
-  using C = Cfg<ES, DP, NT, ROWS>;
+  using C = Cfg<ES, DP, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   // In this order: k_attend_join reads the lengths before it waits, and it is launched once
   // every block here has seen the end of the work that wrote them.
@@ -246,8 +250,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT, ROWS>::kPerSm)) k_a
     b = blockIdx.x / HV;
     const int row = blockIdx.x - b * HV;
     const Span sp = span_of(a, b, C::kTok, C::kUnit, warp == 0 && row == 0);
-    pos = row * sp.units;
-    stop = pos + sp.units;
+    pos = row * sp.cost;
+    stop = pos + sp.cost;
     if (!sp.units) {
       const int h = row / head_tiles, h0 = h * group + (row - h * head_tiles) * C::kHeads;
       write_empty(a, b, h0, min(C::kHeads, h * group + group - h0), kThreads);
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT, ROWS>::kPerSm)) k_a
     for (int b0 = b; all.per > 1; b0 += 32) {
       const int bb = b0 + lane;
       const uint32_t u =
-          bb < a.batch ? (uint32_t)span_of(a, bb, C::kTok, C::kUnit, false).units * HV : 0;
+          bb < a.batch ? (uint32_t)span_of(a, bb, C::kTok, C::kUnit, false).cost * HV : 0;
       uint32_t x = u;
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t y = __shfl_up_sync(~0u, x, o);
@@ -291,15 +295,17 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT, ROWS>::kPerSm)) k_a
 
   while (pos < stop) {
     Span sp = span_of(a, b, C::kTok, C::kUnit, false);
-    if (pos >= before + (uint32_t)sp.units * HV) {
-      before += (uint32_t)sp.units * HV;
+    if (pos >= before + (uint32_t)sp.cost * HV) {
+      before += (uint32_t)sp.cost * HV;
       ++b;
       continue;
     }
-    const int row = (pos - before) / (uint32_t)sp.units;
-    const int u0 = pos - before - (uint32_t)row * sp.units;
-    const int nu = min((uint32_t)(sp.units - u0), stop - pos);
-    pos += nu;
+    const int row = (pos - before) / (uint32_t)sp.cost;
+    const int c0 = pos - before - (uint32_t)row * sp.cost;
+    const int c1 = min((uint32_t)sp.cost, c0 + (stop - pos));
+    pos += c1 - c0;
+    const int u0 = max(c0 - kRowCost, 0), nu = c1 - kRowCost - u0;
+    if (nu <= 0) continue;  // only the row's beginning
     const int h = row / head_tiles, h0 = h * group + (row - h * head_tiles) * C::kHeads;
     const int nh = min(C::kHeads, h * group + group - h0);  // query heads of this row
     const uint32_t *tab_k =
@@ -685,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT, ROWS>::kPerSm)) k_a
 template <int ES, int DP, int NT, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32) k_attend_join(AttendArgs a, int head_tiles,
                                                             int grid) {
-  using C = Cfg<ES, DP, NT, false>;
+  using C = Cfg<ES, DP, NT>;
   constexpr int kVec = DP / 32;  // channels per lane
   constexpr int kMost = WARPS == 8 ? 8 : 4;
   constexpr int kPre = 32 / kVec > kMost ? kMost : 32 / kVec;  // parts a warp loads at first
@@ -696,15 +702,15 @@ __global__ void __launch_bounds__(WARPS * 32) k_attend_join(AttendArgs a, int he
   const int group = a.q_heads / c.heads;
   const int b = blockIdx.x / a.q_heads, hq = blockIdx.x - b * a.q_heads;
   const Sums all = sums_of<C>(a, HV, b, false);
-  const int units = span_of(a, b, C::kTok, C::kUnit, false).units;
+  const int cost = span_of(a, b, C::kTok, C::kUnit, false).cost;
   const int64_t oh = (int64_t)b * a.q_heads + hq;
   const int h = hq / group, in = hq - h * group;
   const int row = h * head_tiles + in / C::kHeads, hh = in % C::kHeads;
-  const uint32_t lo = all.below + (uint32_t)row * units, nblk = blocks_used(all.W, grid);
+  const uint32_t lo = all.below + (uint32_t)row * cost, nblk = blocks_used(all.W, grid);
   int c0 = 0, n = 0;
-  if (units) {
-    c0 = block_of(all.W, nblk, lo);
-    n = block_of(all.W, nblk, lo + units - 1) - c0 + 1;
+  if (cost) {  // the blocks of the row's first and last unit
+    c0 = block_of(all.W, nblk, lo + kRowCost);
+    n = block_of(all.W, nblk, lo + cost - 1) - c0 + 1;
   }
   // the first block's part is the one that begins the row (slot 1)
   const Part<DP, NT> *parts = reinterpret_cast<const Part<DP, NT> *>(a.ws) + c0 * 2;
@@ -785,24 +791,29 @@ int sm_count() {
 
 template <int ES, int DP, int NT>
 cudaError_t run(const AttendArgs &a, int head_tiles, cudaStream_t st) {
-  using C = Cfg<ES, DP, NT, false>;
+  using C = Cfg<ES, DP, NT>;
   const int sms = sm_count();
   if (!sms) return cudaErrorInvalidDevice;
   const int64_t rows = (int64_t)a.batch * a.c.heads * head_tiles;
   // a tile may start up to kTok - 1 tokens before the range
   const int64_t row_units = ((int64_t)a.max_len + C::kTok - 1 + C::kUnit - 1) / C::kUnit;
   const int64_t wave = (int64_t)sms * C::kPerSm;
-  using R = Cfg<ES, DP, NT, true>;
-  // Rows are not cut where one block takes little longer for one than the cut, the second
-  // launch and the join do: with 8 rows of 128 channels 5.6 us against 6.3 at 5 units and
-  // 7.9 against 6.4 at 9, with 64 rows 8.5 against 9.0 at 9 and 13.1 against 9.8 at 17, with
-  // 256 rows 19.5 against 22.2 at 17 (bf16, 8 query heads a row).
-  if (row_units <= 5 + rows / 16 && rows <= (int64_t)sms * R::kPerSm) {
+  // One block per row, and no join, where a block takes little longer for a row than the
+  // cut and the join do; with many rows the blocks that start as others end also even out
+  // what is left.  A unit takes a block that has its SM to itself 0.3 us (bf16: what the
+  // SM's shared memory takes in and out) or 0.8 us (e4m3: the conversions).  Cut / not cut,
+  // 128 channels: bf16, 8 rows of 5 units 6.3 / 5.5 us, of 9 units 6.4 / 7.9; 64 rows of 9
+  // 9.0 / 8.5, of 17 9.8 / 13.1; 512 rows of 33 61.2 / 59.4, of 65 108 / 117; 2048 rows of
+  // 9 78.4 / 57.0.  e4m3, 64 rows of 5 units 9.1 / 7.2, of 9 10.0 / 10.7; 512 rows of 9
+  // 23.8 / 23.2, of 17 35.4 / 37.4; 1024 rows of 17 61.8 / 60.0, 2048 rows of 5 51.6 / 40.3.
+  const int64_t whole = ES == 2 ? (rows < 448 ? 5 + rows / 16 : 33)
+                                : (rows < 768 ? 5 + rows / 64 : 17);
+  if (row_units <= whole) {
     auto kern = k_attend<ES, DP, NT, true>;
     cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    return launch(kern, dim3((unsigned)rows), kThreads, R::kSmem, st, a, head_tiles);
+    return launch(kern, dim3((unsigned)rows), kThreads, C::kSmem, st, a, head_tiles);
   }
   auto kern = k_attend<ES, DP, NT, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);

@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kThreads) k_free(CacheView c, const int32_t *s
     if (p == kNoPage) continue;
     if (p >= c.pages) {
       atomicOr(c.status, kCacheArg);
-    } else if (atomicSub(c.refs + p, 1u) == 0) {
+    } else if ((int32_t)atomicSub(c.refs + p, 1u) <= 0) {  // a free page, maybe named often
       atomicAdd(c.refs + p, 1u);
       atomicOr(c.status, kCacheArg);
     }

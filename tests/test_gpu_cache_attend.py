@@ -245,6 +245,26 @@ def test_many_sequences():
     run(c, 1, 0, [i % 50 for i in range(n)], lens, 4, max_len=40)
 
 
+@pytest.mark.parametrize("batch", [33, 70, 1100])
+@pytest.mark.parametrize("dtype", [0, 1], ids=["bf16", "e4m3"])
+def test_many_sequences_with_long_ones_among_them(dtype, batch):
+    """Cut rows in a batch of more entries than a warp has lanes (and than their square)."""
+    c = filled(dtype, 1, 1, 64, 32, 4, 4100)
+    g = torch.Generator().manual_seed(batch)
+    lens = torch.randint(0, 30, (batch,), generator=g)
+    long = torch.randperm(batch, generator=g)[:6]
+    lens[long] = torch.tensor([4100, 3000, 4099, 1, 2048, 777])
+    lens = lens.tolist()
+    slots = [i % 4 for i in range(batch)]
+    gq = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn(batch, 2, 64, generator=gq, device="cuda").bfloat16()
+    out, lse = c.attend(0, ints(slots), ints(lens), q, 1 << 17 if batch == 1100 else 4100, lse=True)
+    c.status()
+    sel = sorted(set(long.tolist() + [i for i in range(0, batch, 1 + batch // 40)]))
+    check_attend(c, dtype, 0, [slots[i] for i in sel], [0] * len(sel), [lens[i] for i in sel],
+                 q[sel], 64 ** -0.5, out[sel], lse[sel])
+
+
 def test_pool_offsets_past_32_bits():
     P = skv()
     tb, d = 2048, 128

@@ -158,6 +158,15 @@ def test_free_reports_bad_entries_and_a_slot_twice_counts_once():
     assert torch.all(c.table[1] == -1) and torch.all(c.refs == 0)
 
 
+def test_free_of_entries_that_name_one_free_page():
+    P, c = make()
+    c.table[1] = 7                                                            # count 0, 40 times
+    c.free(ints([1]))
+    with pytest.raises(P.SkvError):
+        c.status()
+    assert torch.all(c.table == -1) and torch.all(c.refs == 0)
+
+
 def test_compact_reports_entries_that_name_free_pages():
     P, c = make()
     c.reserve(ints([0, 1]), ints([0, 0]), ints([16, 16]))
