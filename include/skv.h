@@ -498,8 +498,7 @@ int skv_cache_init(const skv_cache *cache, skv_stream_t stream);
 
 /* The status gathered by the calls on this cache since the last
  * skv_cache_status (or skv_cache_init), which it clears: SKV_OK, SKV_ERR_ARG,
- * SKV_ERR_CAPACITY (no free pages), SKV_ERR_CUDA (a kernel's bounded wait ran
- * out).  Synchronizes `stream`. */
+ * SKV_ERR_CAPACITY (no free pages).  Synchronizes `stream`. */
 int skv_cache_status(const skv_cache *cache, skv_stream_t stream);
 
 /* Workspace bytes of skv_cache_reserve and skv_cache_fork with up to n
@@ -605,8 +604,8 @@ typedef struct {
  * encoder refuses).  A place must have a page that belongs to its
  * sequence alone (count 1: skv_cache_reserve gives such pages and a fork never
  * shares one that is not full); otherwise it is reported (SKV_ERR_ARG) and not
- * written.  Two tokens with the same place: one of the two is kept.
- * head_dim up to 4096, q_heads + 2 * heads up to 8192. */
+ * written.  Two tokens with the same place leave parts of either.  head_dim up to
+ * 4096, q_heads + 2 * heads up to 8192. */
 int skv_cache_append(const skv_cache *cache, int32_t layer, const skv_rope *rope,
                      const skv_tokens *tokens, const int32_t *slots, const int32_t *at,
                      const int32_t *positions, int32_t n, int32_t q_heads, void *q_out,

@@ -12,7 +12,6 @@ constexpr uint32_t kNoPage = 0xffffffffu;
 // bits of the cache's status word
 constexpr uint32_t kCacheArg = 1u;       // a slot, length or page out of range
 constexpr uint32_t kCacheCapacity = 2u;  // not enough free pages
-constexpr uint32_t kCacheStuck = 4u;     // a copy did not arrive within the wait's limit
 
 // The cache as the kernels see it.  Row r of a sequence is (layer*2 + kv)*heads
 // + head; its table entries are at (slot*rows + r)*blocks.
@@ -29,7 +28,7 @@ struct CacheView {
   const float *scale;
 };
 
-// Two 16-byte halves of a streaming copy: read once, written once.
+// 16 bytes of a streaming copy: read once, written once.
 __device__ __forceinline__ uint4 ld_stream(const void *p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"

@@ -58,8 +58,7 @@ int make_view(const skv_cache *k, CacheView *out) {
 }
 
 // A list of n sequences for the page operations.
-int check_list(const CacheView &c, const int32_t *p, int32_t n) {
-  (void)c;
+int check_list(const int32_t *p, int32_t n) {
   if (n < 0 || n > kMaxList || (n && !p) || !aligned(p, 4)) return SKV_ERR_ARG;
   return SKV_OK;
 }
@@ -94,7 +93,6 @@ int skv_cache_status(const skv_cache *cache, skv_stream_t stream) {
       cudaMemsetAsync(c.status, 0, sizeof(v), st) != cudaSuccess ||
       cudaStreamSynchronize(st) != cudaSuccess)
     return SKV_ERR_CUDA;
-  if (v & kCacheStuck) return SKV_ERR_CUDA;
   if (v & kCacheArg) return SKV_ERR_ARG;
   return v & kCacheCapacity ? SKV_ERR_CAPACITY : SKV_OK;
 }
@@ -110,8 +108,8 @@ int skv_cache_reserve(const skv_cache *cache, const int32_t *slots, const int32_
                       size_t workspace_bytes, skv_stream_t stream) {
   CacheView c;
   int rc = make_view(cache, &c);
-  if (rc || (rc = check_list(c, slots, n)) || (rc = check_list(c, old_len, n)) ||
-      (rc = check_list(c, new_len, n)) || (rc = check_pages_ws(c, n, workspace, workspace_bytes)))
+  if (rc || (rc = check_list(slots, n)) || (rc = check_list(old_len, n)) ||
+      (rc = check_list(new_len, n)) || (rc = check_pages_ws(c, n, workspace, workspace_bytes)))
     return rc;
   if (!n) return SKV_OK;
   return status_of(launch_reserve(c, slots, old_len, new_len, n, static_cast<uint8_t *>(workspace),
@@ -123,8 +121,8 @@ int skv_cache_fork(const skv_cache *cache, const int32_t *parents, const int32_t
                    skv_stream_t stream) {
   CacheView c;
   int rc = make_view(cache, &c);
-  if (rc || (rc = check_list(c, parents, n)) || (rc = check_list(c, children, n)) ||
-      (rc = check_list(c, lens, n)) || (rc = check_pages_ws(c, n, workspace, workspace_bytes)))
+  if (rc || (rc = check_list(parents, n)) || (rc = check_list(children, n)) ||
+      (rc = check_list(lens, n)) || (rc = check_pages_ws(c, n, workspace, workspace_bytes)))
     return rc;
   if (!n) return SKV_OK;
   if (c.rows * n > INT_MAX) return SKV_ERR_ARG;  // one block per (row, child)
@@ -135,7 +133,7 @@ int skv_cache_fork(const skv_cache *cache, const int32_t *parents, const int32_t
 int skv_cache_free(const skv_cache *cache, const int32_t *slots, int32_t n, skv_stream_t stream) {
   CacheView c;
   int rc = make_view(cache, &c);
-  if (rc || (rc = check_list(c, slots, n))) return rc;
+  if (rc || (rc = check_list(slots, n))) return rc;
   if (!n) return SKV_OK;
   return status_of(launch_free(c, slots, n, stream_of(stream)));
 }

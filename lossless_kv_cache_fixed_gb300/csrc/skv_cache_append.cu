@@ -75,21 +75,13 @@ __device__ __forceinline__ uint2 pack_e4m3(const float *x, float inv) {
   return make_uint2(w[0], w[1]);
 }
 
-// x / d where x * d is below 2^32: magic = ceil(2^32 / d), 0 for d = 1.
-struct Div {
-  uint32_t magic;
-};
-__device__ __forceinline__ uint32_t div_of(uint32_t x, const Div &v) {
-  return v.magic ? __umulhi(x, v.magic) : x;
-}
-
 // The kinds of units.  A block's rows are its tokens' q heads, then their k heads, then
 // their v heads (token-major in each).
 enum { kQTurn, kKTurn, kQPass, kKPass, kV, kKinds };
 struct Kind {
   int task0, n;      // its first task, its units
   int per, from;     // units of a row, the first of them
-  uint32_t magic;    // of per
+  uint32_t magic;    // x / per = (x * magic) >> 32, or x where it is 0 (see magic_of)
   int row0;          // its first row
   int turns, q;
 };
@@ -98,7 +90,7 @@ struct Kind {
 struct Plan {
   int toks;           // tokens of a block, at most 16
   int units, turned;  // 16-channel units of a head, those that turn
-  Div by_units, by_turned, by_pass;
+  uint32_t by_units, by_turned, by_pass;  // magics
 };
 
 // (a, b) turned by (cos, sin).
@@ -141,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks[E4M3]) k_append(AppendArgs a
     x.q = k == kQTurn || k == kQPass;
     x.per = x.turns ? pl.turned : k == kV ? pl.units : passing;
     x.from = k == kQPass || k == kKPass ? pl.turned : 0;
-    x.magic = (x.turns ? pl.by_turned : k == kV ? pl.by_units : pl.by_pass).magic;
+    x.magic = x.turns ? pl.by_turned : k == kV ? pl.by_units : pl.by_pass;
     x.n = (x.q ? nq : nk) * x.per;
     x.task0 = k == kQTurn ? 0 : k == kKTurn ? e0 : k == kQPass ? e1 : k == kKPass ? e2 : e3;
     x.row0 = x.q ? 0 : k == kV ? nq + nk : nq;
@@ -282,9 +274,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks[E4M3]) k_append(AppendArgs a
   }
 }
 
-Div make_div(int d) {
-  return Div{d > 1 ? (uint32_t)(((1ull << 32) + d - 1) / d) : 0u};
-}
+// ceil(2^32 / d), with which x / d is exact where x * d is below 2^32; 0 for d = 1.
+uint32_t magic_of(int d) { return d > 1 ? (uint32_t)(((1ull << 32) + d - 1) / d) : 0u; }
 
 }  // namespace
 
@@ -299,9 +290,9 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t st) {
   const int64_t units = ((int64_t)a.q_heads + 2 * c.heads) * p.units;
   const int64_t toks = a.n <= 152 * 8 ? 1 : (kUnits[c.dtype == 1] + units / 2) / units;
   p.toks = (int)(toks < 1 ? 1 : toks > kMostToks ? kMostToks : toks);
-  p.by_units = make_div(p.units);
-  p.by_turned = make_div(p.turned);
-  p.by_pass = make_div(p.units - p.turned);
+  p.by_units = magic_of(p.units);
+  p.by_turned = magic_of(p.turned);
+  p.by_pass = magic_of(p.units - p.turned);
   const size_t heads = (size_t)a.q_heads + 2 * (size_t)c.heads;
   const size_t smem = (size_t)p.toks * (sizeof(float2) * pairs + 2 * sizeof(uint64_t) * heads) +
                       (c.dtype == 1 ? sizeof(float) * (size_t)c.heads : 0);

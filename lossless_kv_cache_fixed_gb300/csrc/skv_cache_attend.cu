@@ -108,11 +108,11 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// two e4m3 codes (low 16 bits) to two halves
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t v) {
-  uint32_t r;
-  asm("{.reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(r) : "r"(v));
-  return r;
+// four e4m3 codes to halves: the two in the low 16 bits, the two in the high
+__device__ __forceinline__ void e4m3x4(uint32_t v, uint32_t &lo, uint32_t &hi) {
+  asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
 }
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -497,9 +497,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
             ldsm4<false>(t, sk + swz<C::kCpr>(r, k + (lane >> 4)));
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
-              const uint32_t lo = t[2 * kk], hi = t[2 * kk + 1];
-              const uint32_t a0 = e4m3x2(lo), a2 = e4m3x2(lo >> 16);
-              const uint32_t a1 = e4m3x2(hi), a3 = e4m3x2(hi >> 16);
+              uint32_t a0, a1, a2, a3;
+              e4m3x4(t[2 * kk], a0, a2);
+              e4m3x4(t[2 * kk + 1], a1, a3);
 #pragma unroll
               for (int n = 0; n < NT; ++n)
                 mma<ES>(x[mt][n], a0, a1, a2, a3, qf[n][k + kk][0], qf[n][k + kk][1]);
@@ -601,10 +601,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
 #pragma unroll
             for (int dd = 0; dd < 2; ++dd) {
               // bytes: token 2j channels (2r, 2r+1), token 2j+1 the same
-              const uint32_t lo = __byte_perm(t[2 * dd], 0, 0x3120);
-              const uint32_t hi = __byte_perm(t[2 * dd + 1], 0, 0x3120);
-              const uint32_t a0 = e4m3x2(lo), a1 = e4m3x2(lo >> 16);
-              const uint32_t a2 = e4m3x2(hi), a3 = e4m3x2(hi >> 16);
+              uint32_t a0, a1, a2, a3;
+              e4m3x4(__byte_perm(t[2 * dd], 0, 0x3120), a0, a1);
+              e4m3x4(__byte_perm(t[2 * dd + 1], 0, 0x3120), a2, a3);
 #pragma unroll
               for (int n = 0; n < NT; ++n)
                 mma<ES>(o[d + dd][n], a0, a1, a2, a3, pf[mt][n][0], pf[mt][n][1]);
@@ -802,10 +801,11 @@ cudaError_t run(const AttendArgs &a, int head_tiles, cudaStream_t st) {
   // cut and the join do; with many rows the blocks that start as others end also even out
   // what is left.  A unit takes a block that has its SM to itself 0.3 us (bf16: what the
   // SM's shared memory takes in and out) or 0.8 us (e4m3: the conversions).  Cut / not cut,
-  // 128 channels: bf16, 8 rows of 5 units 6.3 / 5.5 us, of 9 units 6.4 / 7.9; 64 rows of 9
-  // 9.0 / 8.5, of 17 9.8 / 13.1; 512 rows of 33 61.2 / 59.4, of 65 108 / 117; 2048 rows of
-  // 9 78.4 / 57.0.  e4m3, 64 rows of 5 units 9.1 / 7.2, of 9 10.0 / 10.7; 512 rows of 9
-  // 23.8 / 23.2, of 17 35.4 / 37.4; 1024 rows of 17 61.8 / 60.0, 2048 rows of 5 51.6 / 40.3.
+  // 128 channels, us: bf16, 8 rows of 9 units 7.1 / 7.8; 64 rows of 9 8.1 / 8.4, of 17 9.3 /
+  // 12.9; 256 rows of 17 22.0 / 21.1, of 33 33.6 / 36.7; 512 rows of 33 61.2 / 59.2, of 65
+  // 108 / 117; 2048 rows of 9 78.8 / 56.8.  e4m3, 64 rows of 5 units 8.6 / 7.2, of 9 8.9 /
+  // 10.2; 256 rows of 9 16.2 / 14.7, of 17 22.3 / 23.5; 1024 rows of 17 61.2 / 58.3; 2048
+  // rows of 5 49.3 / 38.6.
   const int64_t whole = ES == 2 ? (rows < 448 ? 5 + rows / 16 : 33)
                                 : (rows < 768 ? 5 + rows / 64 : 17);
   if (row_units <= whole) {
