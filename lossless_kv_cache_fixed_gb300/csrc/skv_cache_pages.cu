@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(kThreads) k_free_list(CacheView c, Request q, 
 constexpr int kSmallThreads = 1024;
 constexpr uint64_t kSmallPages = (uint64_t)kSmallThreads * kPer;
 constexpr int64_t kSmallEntries = 1 << 14;
+constexpr int64_t kSmallRows = 2 * kSmallThreads;
 __global__ void __launch_bounds__(kSmallThreads) k_small_list(CacheView c, Request q, Go go,
                                                               uint32_t *list) {
   __shared__ uint32_t s[2][32];
@@ -306,6 +307,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_small_list(CacheView c, Reque
       const uint32_t i = x / rows, r = x - i * rows;
       const Item t = item_of(c, q, i);
       const uint32_t *own = c.table + (int64_t)t.slot * entries + r * blocks + t.b0;
+#pragma unroll 4
       for (int b = 0; b < t.nb; ++b) wrong |= own[b] != kNoPage;  // nb is 0 where not ok
     }
   } else {
@@ -636,8 +638,12 @@ cudaError_t run_request(const CacheView &c, const Request &q, uint8_t *ws, cudaS
   const Go go{at(w.go), at(w.base)};
   uint32_t *list = at(w.list);
   cudaError_t e;
-  // one block where it has little to read
-  if (c.pages <= kSmallPages && q.n <= kSmallThreads && c.rows * c.blocks * q.n <= kSmallEntries) {
+  // one block where it has little to read: all entries of the slots for a fork; for reserve
+  // only those that it fills, mostly few
+  const int64_t entries = c.rows * c.blocks * q.n;
+  const bool little = q.parents ? entries <= kSmallEntries
+                                : c.rows * q.n <= kSmallRows && entries <= 4 * kSmallEntries;
+  if (c.pages <= kSmallPages && q.n <= kSmallThreads && little) {
     e = launch(k_small_list, dim3(1), kSmallThreads, 0, st, c, q, go, list);
   } else {
     Found f{at(w.need), at(w.bad), at(w.counts), 1, chunks_of(c)};
