@@ -15,7 +15,7 @@
 // kind for a warp -- q or k channels that turn, q, k or v channels that pass -- so no
 // warp diverges; where each (token, head) is read from and goes to lies in shared
 // memory, so a unit costs one division by multiplication and few address operations
-// (the kernel is 60% of the way to being bound by its instructions).  A task's vectors
+// (53% of the issue slots are busy for e4m3, 63% for bf16).  A task's vectors
 // are loaded before the one before it is turned, the first ones before the block forms
 // its angles and looks up its pages.
 //

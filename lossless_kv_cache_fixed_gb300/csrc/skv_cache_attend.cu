@@ -50,7 +50,8 @@ struct Cfg {
   static constexpr int kTile = kTok * kRowB;         // bytes of a tile of K or V
   // 2 stages leave room for 3 blocks (12 warps) per SM, which hide one another's latency:
   // 107 us against 111 with 3 stages and 2 blocks for 32 rows of up to 16384 e4m3 tokens
-  static constexpr int kStages = kTile <= 2048 ? 4 : DP == 256 ? 3 : 2;
+  // (64-channel e4m3 tiles are half as large: 3 stages, 4 blocks)
+  static constexpr int kStages = kTile <= 2048 ? 3 : DP == 256 ? 3 : 2;
   static constexpr int kUnit = kWarps * kTok;        // tokens of a unit
   static constexpr int kSmem = kWarps * kStages * 2 * kTile;
   static constexpr int kPerSm = 220 * 1024 / (kSmem + 1024) < 4 ? 220 * 1024 / (kSmem + 1024) : 4;

@@ -225,7 +225,7 @@ class PagedCache:
         """`call` with `stream` current: what it allocates belongs to that stream, and the
         tensors given stay allocated until the stream is past it."""
         with self.torch.cuda.stream(stream):
-            for t in tensors:
+            for t in (*tensors, self.pool, self.table, self.refs, self._status, self.scale):
                 if t is not None:
                     t.record_stream(stream)
             return call()

@@ -140,6 +140,22 @@ def test_special_values_inside_the_range():
     assert torch.all(torch.isnan(out)) and math.isnan(float(lse))
 
 
+def test_nan_codes_inside_the_range():
+    c = filled(1, 1, 2, 64, 16, 1, 40)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = torch.randn(1, 4, 64, generator=g, device="cuda").bfloat16()
+    want, wl = c.attend(0, ints([0]), ints([40]), q, 40, lse=True)
+    c.pool[int(c.table[0, 0, 1, 0, 1]), 3, 7] = 0x7F          # a value of kv head 0
+    out, lse = c.attend(0, ints([0]), ints([40]), q, 40, lse=True)
+    assert torch.all(torch.isnan(out[0, :2, 7])) and torch.equal(lse, wl)
+    rest = [d for d in range(64) if d != 7]
+    assert torch.equal(out[0, :2, rest], want[0, :2, rest]) and torch.equal(out[0, 2:], want[0, 2:])
+    c.pool[int(c.table[0, 0, 0, 1, 2]), 1, 0] = 0xFF          # a key of kv head 1
+    out, lse = c.attend(0, ints([0]), ints([40]), q, 40, lse=True)
+    assert torch.all(torch.isnan(out[0, 2:])) and torch.all(torch.isnan(lse[0, 2:]))
+    assert torch.equal(lse[0, :2], wl[0, :2])
+
+
 def test_infinite_values_inside_the_range():
     c = filled(0, 1, 1, 64, 16, 1, 40)
     g = torch.Generator(device="cuda").manual_seed(2)
