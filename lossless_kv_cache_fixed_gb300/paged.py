@@ -118,6 +118,18 @@ def _bad(what):
     return SkvError(SKV_ERR_ARG, what)
 
 
+def _allocator(device):
+    """empty(shape, strides, dtype) on the current device, which is `device`: torch's own
+    short cut where it has it (1 us a call in place of 3), else torch.empty_strided."""
+    import torch
+    try:
+        from torch._C._dynamo.guards import _empty_strided_cuda
+        return _empty_strided_cuda
+    except ImportError:
+        return lambda shape, strides, dtype: torch.empty_strided(shape, strides, dtype=dtype,
+                                                                 device=device)
+
+
 class Rope:
     """Rotary positions: pair p of a head's first 2 * freqs.numel() channels turns by
     position[axis_of_pair[p]] * freqs[p].
@@ -205,7 +217,10 @@ class PagedCache:
         self._ref = C.byref(self.struct)
         self._index = self.device.index
         self._raw_stream = torch._C._cuda_getCurrentRawStream
-        self._int32, self._bf16, self._empty = torch.int32, torch.bfloat16, torch.empty
+        self._current_device = torch._C._cuda_getDevice
+        self._capturing = torch._C._cuda_isCurrentStreamCapturing
+        self._int32, self._bf16, self._f32 = torch.int32, torch.bfloat16, torch.float32
+        self._empty = _allocator(self.device)
         self._attend_bytes = {}    # workspace bytes by q_heads
         self._pages_bytes = {}     # and of the page operations by n
         self._default_scale = head_dim ** -0.5
@@ -219,6 +234,8 @@ class PagedCache:
     # -- helpers --
 
     def _stream(self):
+        if self._current_device() != self._index:
+            raise _bad("PagedCache: its device must be the current one")
         return self._raw_stream(self._index)
 
     def _on(self, stream, tensors, call):
@@ -231,13 +248,15 @@ class PagedCache:
             return call()
 
     def _workspace(self, kind, stream, nbytes):
-        capturing = self.torch.cuda.is_current_stream_capturing()
-        ws = None if capturing else self._ws.get((kind, stream))
-        if ws is None or ws.numel() < nbytes:
+        """This stream's workspace of at least nbytes: (address, bytes, tensor)."""
+        capturing = self._capturing()
+        have = None if capturing else self._ws.get((kind, stream))
+        if have is None or have[1] < nbytes:
             ws = self.torch.empty(nbytes, dtype=self.torch.uint8, device=self.device)
+            have = ws.data_ptr(), nbytes, ws
             if not capturing:       # a captured one belongs to its graph
-                self._ws[kind, stream] = ws
-        return ws
+                self._ws[kind, stream] = have
+        return have
 
     def _ints(self, what, n, *tensors):
         i32 = self._int32
@@ -294,8 +313,7 @@ class PagedCache:
         st = self._stream()
         ws = self._pages_ws(n, st)
         self._check(self._lib.skv_cache_reserve(self._ref, slots.data_ptr(), old_len.data_ptr(),
-                                                new_len.data_ptr(), n, ws.data_ptr(), ws.numel(),
-                                                st), "skv_cache_reserve")
+                                                new_len.data_ptr(), n, ws[0], ws[1], st), "skv_cache_reserve")
 
     def fork(self, parents, children, lens, stream=None):
         """Each child becomes a copy of the first tokens of its parent."""
@@ -307,7 +325,7 @@ class PagedCache:
         st = self._stream()
         ws = self._pages_ws(n, st)
         self._check(self._lib.skv_cache_fork(self._ref, parents.data_ptr(), children.data_ptr(),
-                                             lens.data_ptr(), n, ws.data_ptr(), ws.numel(), st),
+                                             lens.data_ptr(), n, ws[0], ws[1], st),
                     "skv_cache_fork")
 
     def free(self, slots, stream=None):
@@ -335,7 +353,7 @@ class PagedCache:
         ws = self._pages_ws(0, st)
         self._check(self._lib.skv_cache_compact(
             self._ref, None if table_out is None else table_out.data_ptr(),
-            None if refs_out is None else refs_out.data_ptr(), ws.data_ptr(), ws.numel(), st),
+            None if refs_out is None else refs_out.data_ptr(), ws[0], ws[1], st),
             "skv_cache_compact")
 
     def copy_pages(self, src, dst, src_pool=None, dst_pool=None, stream=None):
@@ -376,11 +394,13 @@ class PagedCache:
         ks = self._heads("append: k", k, n, self.heads)
         vs = self._heads("append: v", v, n, self.heads)
         qs, q_heads, q_ptr, out_ptr = (0, 0), 0, None, None
+        st = self._stream()
         if q is not None:
             qs = self._heads("append: q", q, n)
             q_heads = q.shape[1]
             if q_out is None:
-                q_out = self._empty((n, q_heads, self.head_dim), dtype=self._bf16, device=self.device)
+                d = self.head_dim
+                q_out = self._empty((n, q_heads, d), (q_heads * d, d, 1), self._bf16)
             else:
                 self._heads("append: q_out", q_out, n, q_heads)
                 if not q_out.is_contiguous():
@@ -397,7 +417,7 @@ class PagedCache:
         t = SkvTokens(q_ptr, k.data_ptr(), v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1])
         self._check(self._lib.skv_cache_append(
             self._ref, layer, rope_ref, C.byref(t), slots.data_ptr(), at.data_ptr(), pos_ptr, n,
-            q_heads, out_ptr, self._stream()), "skv_cache_append")
+            q_heads, out_ptr, st), "skv_cache_append")
         return q_out
 
     def attend(self, layer, slots, lens, q, max_len, begins=None, scale=None, out=None, lse=False,
@@ -415,16 +435,7 @@ class PagedCache:
         if begins is not None:
             self._ints("attend", n, begins)
         qs = self._heads("attend: q", q, n)
-        q_heads = q.shape[1]
-        if out is None:
-            out = self._empty((n, q_heads, self.head_dim), dtype=self._bf16, device=self.device)
-        else:
-            self._heads("attend: out", out, n, q_heads)
-            if not out.is_contiguous():
-                raise _bad("attend: out must be contiguous")
-        s = None
-        if lse:
-            s = self._empty((n, q_heads), dtype=self.torch.float32, device=self.device)
+        q_heads, d = q.shape[1], self.head_dim
         nb = self._attend_bytes.get(q_heads)
         if nb is None:
             nb = skv_cache_attend_workspace_bytes(self.struct, n, q_heads)
@@ -433,9 +444,16 @@ class PagedCache:
             self._attend_bytes[q_heads] = nb
         st = self._stream()
         ws = self._workspace("attend", st, nb)
+        if out is None:
+            out = self._empty((n, q_heads, d), (q_heads * d, d, 1), self._bf16)
+        else:
+            self._heads("attend: out", out, n, q_heads)
+            if not out.is_contiguous():
+                raise _bad("attend: out must be contiguous")
+        s = self._empty((n, q_heads), (q_heads, 1), self._f32) if lse else None
         self._check(self._lib.skv_cache_attend(
             self._ref, layer, slots.data_ptr(), lens.data_ptr(),
             None if begins is None else begins.data_ptr(), n, q.data_ptr(), qs[0], qs[1], q_heads,
             self._default_scale if scale is None else scale, max_len, out.data_ptr(),
-            None if s is None else s.data_ptr(), ws.data_ptr(), nb, st), "skv_cache_attend")
+            None if s is None else s.data_ptr(), ws[0], ws[1], st), "skv_cache_attend")
         return (out, s) if lse else out
