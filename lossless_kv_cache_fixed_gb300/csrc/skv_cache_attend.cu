@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
     const int owner = __ffs(__ballot_sync(~0u, pos < all.before + all.mine)) - 1;
     before = __shfl_sync(~0u, all.before, owner);
     b = owner * all.per;
-    for (int b0 = b; all.per > 1; b0 += 32) {
+    for (int b0 = b; all.per > 1 && b0 < a.batch; b0 += 32) {
       const int bb = b0 + lane;
       const uint32_t u =
           bb < a.batch ? (uint32_t)span_of(a, bb, C::kTok, C::kUnit, false).cost * HV : 0;
@@ -294,7 +294,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
   const bool whole = c.Tb % C::kTok == 0;  // a tile lies in one page
   const bool plain = whole && c.row_bytes == C::kRowB;  // and is one run of bytes
 
-  while (pos < stop) {
+  // (the bound on b: lengths that are overwritten meanwhile must not lead out of the arrays)
+  while (pos < stop && b < a.batch) {
     Span sp = span_of(a, b, C::kTok, C::kUnit, false);
     if (pos >= before + (uint32_t)sp.cost * HV) {
       before += (uint32_t)sp.cost * HV;
@@ -710,7 +711,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_attend_join(AttendArgs a, int he
   int c0 = 0, n = 0;
   if (cost) {  // the blocks of the row's first and last unit
     c0 = block_of(all.W, nblk, lo + kRowCost);
-    n = block_of(all.W, nblk, lo + cost - 1) - c0 + 1;
+    n = min(block_of(all.W, nblk, lo + cost - 1), (int)nblk - 1) - c0 + 1;
   }
   // the first block's part is the one that begins the row (slot 1)
   const Part<DP, NT> *parts = reinterpret_cast<const Part<DP, NT> *>(a.ws) + c0 * 2;

@@ -390,10 +390,12 @@ __global__ void __launch_bounds__(kThreads) k_fork(CacheView c, Request q, Go go
   const uint32_t r = blockIdx.x / (uint32_t)q.n;
   const int i = (int)(blockIdx.x - r * (uint32_t)q.n);
   const Item t = item_of(c, q, i);
+  if (!t.ok) return;
   const uint32_t *par = c.table + ((int64_t)t.parent * c.rows + r) * c.blocks;
   uint32_t *own = c.table + ((int64_t)t.slot * c.rows + r) * c.blocks;
   for (int b = threadIdx.x; b < t.full; b += kThreads) {
     const uint32_t p = par[b];
+    if (p >= c.pages) continue;  // checked, unless the table is being overwritten
     own[b] = p;
     atomicAdd(c.refs + p, 1u);
   }
@@ -403,7 +405,9 @@ __global__ void __launch_bounds__(kThreads) k_fork(CacheView c, Request q, Go go
     own[t.full] = p;
     c.refs[p] = 1;
   }
-  const uint8_t *src = c.pool + (uint64_t)par[t.full] * c.page_bytes;
+  const uint32_t from = par[t.full];
+  if (from >= c.pages) return;
+  const uint8_t *src = c.pool + (uint64_t)from * c.page_bytes;
   uint8_t *dst = c.pool + (uint64_t)p * c.page_bytes;
   const uint32_t bytes = (uint32_t)t.tail * c.row_bytes;
   constexpr uint32_t kRow = kThreads * 16;
