@@ -14,7 +14,8 @@
 //     outside the range filled with zeros) and computes on them without any
 //     block-wide barrier; the block's 4 warps are joined once per row;
 //   - a row that lies in several blocks leaves a partial result in each (at most
-//     two per block) and is joined by k_attend_join, in block order;
+//     two per block) and is joined by k_attend_join or, where few rows lie in many
+//     blocks, k_attend_join_wide, in a fixed order;
 //   - a batch of short rows is not cut: one block per row and no join.
 // The products run on the matrix units transposed, tokens as rows and the group's
 // query heads as the 8 columns of m16n8k16: S^T = K Q^T, O^T = V^T P^T, so a
@@ -684,49 +685,62 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
   }
 }
 
-// One block per (batch entry, query head): joins the parts of a row that lies in
-// several blocks and writes rows without tokens.  The warps take every WARPS-th part
-// each and are added up in warp order.  It is launched while k_attend still runs and
-// finds its parts before it waits, so only the reading of the parts (one round of
-// loads for up to kPre * WARPS of them) comes after k_attend's end.
-template <int ES, int DP, int NT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32) k_attend_join(AttendArgs a, int head_tiles,
-                                                            int grid) {
+// A row as the joins see it: the blocks that share it and where its parts lie.
+struct Row {
+  int b, hq, hh;  // batch entry, query head, the head's place in the parts
+  int c0, n;      // the first block, how many; n = 0: no tokens
+};
+template <typename C>
+__device__ __forceinline__ Row row_of(const AttendArgs &a, int head_tiles, int grid, int x) {
+  Row r;
+  r.b = x / a.q_heads;
+  r.hq = x - r.b * a.q_heads;
+  const int HV = a.c.heads * head_tiles, group = a.q_heads / a.c.heads;
+  const Sums all = sums_of<C>(a, HV, r.b, false);
+  const int cost = span_of(a, r.b, C::kTok, C::kUnit, false).cost;
+  const int h = r.hq / group, in = r.hq - h * group;
+  r.hh = in % C::kHeads;
+  const uint32_t lo = all.below + (uint32_t)(h * head_tiles + in / C::kHeads) * cost;
+  const uint32_t nblk = blocks_used(all.W, grid);
+  r.c0 = r.n = 0;
+  if (cost) {  // the blocks of the row's first and last unit
+    r.c0 = block_of(all.W, nblk, lo + kRowCost);
+    r.n = min(block_of(all.W, nblk, lo + cost - 1), (int)nblk - 1) - r.c0 + 1;
+  }
+  return r;
+}
+
+// The joins add up the parts of a row that lies in several blocks (the first block's part is
+// the one that begins the row, slot 1) and write rows without tokens.  They are launched
+// while k_attend still runs and find their parts before they wait, so that only the reading
+// of the parts comes after k_attend's end.  Every block waits, also one whose row is
+// complete: what follows in the stream waits for the join alone, so it must not end before
+// k_attend.  (It does not let its successor start early: the next call's blocks would take
+// the places of its own.)
+
+// Many rows: one block of two warps per (batch entry, query head); each warp takes every
+// second part, the first kPre of them in one round of loads.
+template <int ES, int DP, int NT>
+__global__ void __launch_bounds__(64) k_attend_join(AttendArgs a, int head_tiles, int grid) {
   using C = Cfg<ES, DP, NT>;
   constexpr int kVec = DP / 32;  // channels per lane
-  constexpr int kMost = WARPS == 8 ? 8 : 4;
-  constexpr int kPre = 32 / kVec > kMost ? kMost : 32 / kVec;  // parts a warp loads at first
-  __shared__ float s_o[WARPS][DP];
+  constexpr int kPre = 4;
+  __shared__ float s_o[2][DP];
   const CacheView &c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int HV = c.heads * head_tiles;
-  const int group = a.q_heads / c.heads;
-  const int b = blockIdx.x / a.q_heads, hq = blockIdx.x - b * a.q_heads;
-  const Sums all = sums_of<C>(a, HV, b, false);
-  const int cost = span_of(a, b, C::kTok, C::kUnit, false).cost;
-  const int64_t oh = (int64_t)b * a.q_heads + hq;
-  const int h = hq / group, in = hq - h * group;
-  const int row = h * head_tiles + in / C::kHeads, hh = in % C::kHeads;
-  const uint32_t lo = all.below + (uint32_t)row * cost, nblk = blocks_used(all.W, grid);
-  int c0 = 0, n = 0;
-  if (cost) {  // the blocks of the row's first and last unit
-    c0 = block_of(all.W, nblk, lo + kRowCost);
-    n = min(block_of(all.W, nblk, lo + cost - 1), (int)nblk - 1) - c0 + 1;
-  }
-  // the first block's part is the one that begins the row (slot 1)
-  const Part<DP, NT> *parts = reinterpret_cast<const Part<DP, NT> *>(a.ws) + c0 * 2;
+  const Row r = row_of<C>(a, head_tiles, grid, blockIdx.x);
+  const int64_t oh = (int64_t)r.b * a.q_heads + r.hq;
+  const int n = r.n, hh = r.hh;
+  const Part<DP, NT> *parts = reinterpret_cast<const Part<DP, NT> *>(a.ws) + r.c0 * 2;
   float osc = 1.f;
-  if (ES == 1 && c.scale) osc = c.scale[a.layer * c.heads + h];
-  // Every block waits, also one whose row is complete: what follows this grid in the
-  // stream waits for it alone, so it must not end before k_attend.  (It does not let its
-  // successor start early: the next call's blocks would take the places of its own.)
+  if (ES == 1 && c.scale) osc = c.scale[a.layer * c.heads + r.hq / (a.q_heads / c.heads)];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (n == 0) write_empty(a, b, hq, 1, WARPS * 32);
+  if (n == 0) write_empty(a, r.b, r.hq, 1, 64);
   if (n <= 1) return;
   float pm[kPre], po[kPre][kVec];
 #pragma unroll
   for (int i = 0; i < kPre; ++i) {
-    const int k = warp + i * WARPS;
+    const int k = warp + i * 2;
     pm[i] = -INFINITY;
     if (k < n) {
       const Part<DP, NT> &p = parts[2 * k + (k == 0)];
@@ -753,13 +767,13 @@ __global__ void __launch_bounds__(WARPS * 32) k_attend_join(AttendArgs a, int he
   for (int v = 0; v < kVec; ++v) acc[v] = 0.f;
 #pragma unroll
   for (int i = 0; i < kPre; ++i)
-    if (warp + i * WARPS < n) {
+    if (warp + i * 2 < n) {
       const float w = ex2(pm[i] - m0);
 #pragma unroll
       for (int v = 0; v < kVec; ++v) acc[v] += w * po[i][v];
     }
 #pragma unroll 4
-  for (int i = warp + kPre * WARPS; i < n; i += WARPS) {
+  for (int i = warp + kPre * 2; i < n; i += 2) {
     const Part<DP, NT> &p = parts[2 * i];
     const float w = ex2(p.m[hh] - m0);
 #pragma unroll
@@ -770,14 +784,85 @@ __global__ void __launch_bounds__(WARPS * 32) k_attend_join(AttendArgs a, int he
 #pragma unroll
   for (int v = 0; v < kVec; ++v) s_o[warp][v * 32 + lane] = acc[v];
   __syncthreads();
-  for (int d = threadIdx.x; d < c.D; d += WARPS * 32) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) v += s_o[w][d];
-    const __nv_bfloat16 r = __float2bfloat16_rn(L == 0.f ? 0.f : v / L * osc);
-    a.out[oh * c.D + d] = *reinterpret_cast<const uint16_t *>(&r);
+  for (int d = threadIdx.x; d < c.D; d += 64) {
+    const __nv_bfloat16 v =
+        __float2bfloat16_rn(L == 0.f ? 0.f : (s_o[0][d] + s_o[1][d]) / L * osc);
+    a.out[oh * c.D + d] = *reinterpret_cast<const uint16_t *>(&v);
   }
   if (threadIdx.x == 0 && a.lse) a.lse[oh] = (m0 + log2f(L)) * kLn2;
+}
+
+// Few rows with many parts each: one block of 8 warps per (batch entry, query head) and 32
+// channels; each warp takes every 8th part, 32 of them in one round of loads.
+constexpr int kWide = 8;
+constexpr int kMostParts = 4 * 160;  // blocks that can share a row
+template <int ES, int DP, int NT>
+__global__ void __launch_bounds__(kWide * 32) k_attend_join_wide(AttendArgs a, int head_tiles,
+                                                                 int grid) {
+  using C = Cfg<ES, DP, NT>;
+  constexpr int kPre = 32, kCols = DP / 32;
+  __shared__ float s_w[kMostParts], s_o[kWide][32], s_m[kWide], s_l[kWide];
+  const CacheView &c = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int x = blockIdx.x / kCols, col = blockIdx.x - x * kCols;
+  const Row r = row_of<C>(a, head_tiles, grid, x);
+  const int64_t oh = (int64_t)r.b * a.q_heads + r.hq;
+  const int n = min(r.n, kMostParts), hh = r.hh, d = col * 32 + lane;
+  const Part<DP, NT> *parts = reinterpret_cast<const Part<DP, NT> *>(a.ws) + r.c0 * 2;
+  float osc = 1.f;
+  if (ES == 1 && c.scale) osc = c.scale[a.layer * c.heads + r.hq / (a.q_heads / c.heads)];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (n == 0 && col == 0) write_empty(a, r.b, r.hq, 1, kWide * 32);
+  if (n <= 1) return;
+  float po[kPre];
+#pragma unroll
+  for (int i = 0; i < kPre; ++i) {
+    const int k = warp + i * kWide;
+    po[i] = k < n ? parts[2 * k + (k == 0)].o[hh][d] : 0.f;
+  }
+  float M = -INFINITY;
+  for (int k = threadIdx.x; k < n; k += kWide * 32) {
+    const float m = parts[2 * k + (k == 0)].m[hh];
+    s_w[k] = m;
+    M = fmaxf(M, m);
+  }
+#pragma unroll
+  for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
+  if (lane == 0) s_m[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWide; ++w) M = fmaxf(M, s_m[w]);
+  const float m0 = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  for (int k = threadIdx.x; k < n; k += kWide * 32) {
+    const float w = ex2(s_w[k] - m0);
+    s_w[k] = w;
+    L += w * parts[2 * k + (k == 0)].l[hh];
+  }
+#pragma unroll
+  for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(~0u, L, s);
+  if (lane == 0) s_l[warp] = L;
+  __syncthreads();
+  float acc = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPre; ++i)
+    if (warp + i * kWide < n) acc += s_w[warp + i * kWide] * po[i];
+#pragma unroll 8
+  for (int k = warp + kPre * kWide; k < n; k += kWide) acc += s_w[k] * parts[2 * k].o[hh][d];
+  s_o[warp][lane] = acc;
+  __syncthreads();
+  if (warp) return;
+  acc = L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWide; ++w) {
+    acc += s_o[w][lane];
+    L += s_l[w];
+  }
+  if (d < c.D) {
+    const __nv_bfloat16 v = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L * osc);
+    a.out[oh * c.D + d] = *reinterpret_cast<const uint16_t *>(&v);
+  }
+  if (col == 0 && lane == 0 && a.lse) a.lse[oh] = (m0 + log2f(L)) * kLn2;
 }
 
 int sm_count() {
@@ -786,6 +871,7 @@ int sm_count() {
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed))) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (n > kMostParts / 4) n = kMostParts / 4;
   if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
@@ -825,14 +911,15 @@ cudaError_t run(const AttendArgs &a, int head_tiles, cudaStream_t st) {
   if (grid < 1) grid = 1;
   e = launch(kern, dim3((unsigned)grid), kThreads, C::kSmem, st, a, head_tiles);
   if (e != cudaSuccess) return e;
-  // 8 warps for a row where few rows have many parts each (one row of 131071 tokens: 48.8
-  // us against 51.3); 2 where the rows are many, so that all blocks are resident at once
-  // when k_attend ends (128 rows of 8192 tokens: 59.6 us against 63.6)
   const int64_t joins = (int64_t)a.batch * a.q_heads;
-  const bool wide = joins <= sms;
-  const dim3 jg((unsigned)joins);
-  return wide ? launch(k_attend_join<ES, DP, NT, 8>, jg, 256, 0, st, a, head_tiles, (int)grid)
-              : launch(k_attend_join<ES, DP, NT, 2>, jg, 64, 0, st, a, head_tiles, (int)grid);
+  // Few rows with many parts each: one row of 31394 tokens 8.7 us against 21.1, 8 of 131071
+  // 47.1 against 50.9; but 8 of 2048 (17 parts) 8.5 against 8.0, and 16 of 8192 with 8 query
+  // heads (512 blocks) 19.9 against 19.0.
+  if (grid / rows >= 24 && joins * (DP / 32) <= 2 * sms)
+    return launch(k_attend_join_wide<ES, DP, NT>, dim3((unsigned)(joins * (DP / 32))), kWide * 32,
+                  0, st, a, head_tiles, (int)grid);
+  return launch(k_attend_join<ES, DP, NT>, dim3((unsigned)joins), 64, 0, st, a, head_tiles,
+                (int)grid);
 }
 
 template <int ES, int DP>
