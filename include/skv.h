@@ -461,7 +461,10 @@ int skv_phi_table(uint32_t *table);
  * data (a slot, length or page out of range, no free page) are gathered in
  * *status and reported by skv_cache_status, and what they concern is left out.
  * Calls that change the table or the counts, and calls that read what those
- * wrote, must be ordered one after the other (one stream, or events).        */
+ * wrote, must be ordered one after the other (one stream, or events).  A call
+ * that takes a workspace may be several kernels, which hand data on in it and in
+ * the cache: host threads that share a stream and a workspace, or a stream and a
+ * cache that they change, must not enter such calls at the same time.        */
 
 #define SKV_NO_PAGE 0xffffffffu /* a table entry without a page */
 

@@ -7,6 +7,7 @@ Nothing here synchronizes but ``PagedCache.status``.
 from __future__ import annotations
 
 import ctypes as C
+import threading
 
 from . import (SKV_BF16, SKV_E4M3, SKV_ERR_ARG, SkvError, lib)
 
@@ -167,7 +168,9 @@ class PagedCache:
 
     Slots, lengths, places and positions are int32 tensors on the device.  Calls
     run on ``stream`` (a torch stream; default: the current one), outputs are
-    allocated there; errors in the data show in ``status()``."""
+    allocated there; errors in the data show in ``status()``.  Several threads may
+    call at once: each call's kernels are enqueued together (which of two calls comes
+    first is theirs to order)."""
 
     def __init__(self, dtype, layers, heads, head_dim, page_tokens, num_pages=None, max_seqs=None,
                  max_blocks=None, scale=None, device="cuda", pool=None, table=None, refs=None):
@@ -226,6 +229,9 @@ class PagedCache:
         self._default_scale = head_dim ** -0.5
         self._lib = lib()
         self._ws = {}
+        # held from the look-up of a workspace until its call has enqueued all of its kernels:
+        # they hand data on in it, and the library's calls let other threads run
+        self._enqueue = threading.Lock()
         if skv_cache_workspace_bytes(self.struct, 0) == 0:
             raise _bad("PagedCache: shape (head_dim a multiple of 8, or 16 for e4m3)")
         if empty:
@@ -283,7 +289,10 @@ class PagedCache:
 
     def clear(self):
         """Empty the cache: no sequence has pages."""
-        self._check(self._lib.skv_cache_init(self._ref, self._stream()), "skv_cache_init")
+        st = self._stream()
+        with self._enqueue:
+            rc = self._lib.skv_cache_init(self._ref, st)
+        self._check(rc, "skv_cache_init")
 
     def status(self):
         """Raises the error gathered since the last call, if any.  Synchronizes."""
@@ -311,9 +320,11 @@ class PagedCache:
         n = slots.numel()
         self._ints("reserve", n, slots, old_len, new_len)
         st = self._stream()
-        ws = self._pages_ws(n, st)
-        self._check(self._lib.skv_cache_reserve(self._ref, slots.data_ptr(), old_len.data_ptr(),
-                                                new_len.data_ptr(), n, ws[0], ws[1], st), "skv_cache_reserve")
+        with self._enqueue:
+            ws = self._pages_ws(n, st)
+            rc = self._lib.skv_cache_reserve(self._ref, slots.data_ptr(), old_len.data_ptr(),
+                                             new_len.data_ptr(), n, ws[0], ws[1], st)
+        self._check(rc, "skv_cache_reserve")
 
     def fork(self, parents, children, lens, stream=None):
         """Each child becomes a copy of the first tokens of its parent."""
@@ -323,10 +334,11 @@ class PagedCache:
         n = parents.numel()
         self._ints("fork", n, parents, children, lens)
         st = self._stream()
-        ws = self._pages_ws(n, st)
-        self._check(self._lib.skv_cache_fork(self._ref, parents.data_ptr(), children.data_ptr(),
-                                             lens.data_ptr(), n, ws[0], ws[1], st),
-                    "skv_cache_fork")
+        with self._enqueue:
+            ws = self._pages_ws(n, st)
+            rc = self._lib.skv_cache_fork(self._ref, parents.data_ptr(), children.data_ptr(),
+                                          lens.data_ptr(), n, ws[0], ws[1], st)
+        self._check(rc, "skv_cache_fork")
 
     def free(self, slots, stream=None):
         """Give back the pages of these sequences."""
@@ -334,8 +346,10 @@ class PagedCache:
             return self._on(stream, (slots,), lambda: self.free(slots))
         n = slots.numel()
         self._ints("free", n, slots)
-        self._check(self._lib.skv_cache_free(self._ref, slots.data_ptr(), n, self._stream()),
-                    "skv_cache_free")
+        st = self._stream()
+        with self._enqueue:     # not between a fork's check of its parents and their sharing
+            rc = self._lib.skv_cache_free(self._ref, slots.data_ptr(), n, st)
+        self._check(rc, "skv_cache_free")
 
     def compact(self, table_out=None, refs_out=None, stream=None):
         """Move the pages in use to the lowest numbers; in place, or with the new table
@@ -350,11 +364,12 @@ class PagedCache:
                                   t.device != own.device or not t.is_contiguous()):
                 raise _bad("compact: outputs shaped like the cache's table and refs")
         st = self._stream()
-        ws = self._pages_ws(0, st)
-        self._check(self._lib.skv_cache_compact(
-            self._ref, None if table_out is None else table_out.data_ptr(),
-            None if refs_out is None else refs_out.data_ptr(), ws[0], ws[1], st),
-            "skv_cache_compact")
+        with self._enqueue:
+            ws = self._pages_ws(0, st)
+            rc = self._lib.skv_cache_compact(
+                self._ref, None if table_out is None else table_out.data_ptr(),
+                None if refs_out is None else refs_out.data_ptr(), ws[0], ws[1], st)
+        self._check(rc, "skv_cache_compact")
 
     def copy_pages(self, src, dst, src_pool=None, dst_pool=None, stream=None):
         """Page dst[i] of dst_pool = page src[i] of src_pool (None: the cache's pool; a
@@ -443,7 +458,6 @@ class PagedCache:
                 raise _bad("attend: q_heads a multiple of the cache's heads, head_dim up to 256")
             self._attend_bytes[q_heads] = nb
         st = self._stream()
-        ws = self._workspace("attend", st, nb)
         if out is None:
             out = self._empty((n, q_heads, d), (q_heads * d, d, 1), self._bf16)
         else:
@@ -451,9 +465,12 @@ class PagedCache:
             if not out.is_contiguous():
                 raise _bad("attend: out must be contiguous")
         s = self._empty((n, q_heads), (q_heads, 1), self._f32) if lse else None
-        self._check(self._lib.skv_cache_attend(
-            self._ref, layer, slots.data_ptr(), lens.data_ptr(),
-            None if begins is None else begins.data_ptr(), n, q.data_ptr(), qs[0], qs[1], q_heads,
-            self._default_scale if scale is None else scale, max_len, out.data_ptr(),
-            None if s is None else s.data_ptr(), ws[0], ws[1], st), "skv_cache_attend")
+        with self._enqueue:
+            ws = self._workspace("attend", st, nb)
+            rc = self._lib.skv_cache_attend(
+                self._ref, layer, slots.data_ptr(), lens.data_ptr(),
+                None if begins is None else begins.data_ptr(), n, q.data_ptr(), qs[0], qs[1],
+                q_heads, self._default_scale if scale is None else scale, max_len, out.data_ptr(),
+                None if s is None else s.data_ptr(), ws[0], ws[1], st)
+        self._check(rc, "skv_cache_attend")
         return (out, s) if lse else out

@@ -1,0 +1,81 @@
+"""What PagedCache does on the host around the calls of the library, without a GPU: its
+tensors lie in host memory and the library is a stand-in that records its calls."""
+import threading
+import time
+
+import pytest
+import torch
+
+D, TB, HEADS = 64, 16, 2
+
+
+@pytest.fixture(scope="module")
+def P():
+    import lossless_kv_cache_fixed_gb300 as P
+    P.build()
+    return P
+
+
+class Device(torch.Tensor):
+    """A host tensor that PagedCache takes for one on its device."""
+    is_cuda = property(lambda self: True)
+
+
+class Library:
+    """Stands in for the library: records the arguments of each call and how many calls are
+    inside at once; every call takes a while, as one with several launches does."""
+
+    def __init__(self, seconds=0.0):
+        self.seconds, self.calls = seconds, []
+        self.inside = self.most = 0
+        self.guard = threading.Lock()
+
+    def __getattr__(self, name):
+        def call(*args):
+            with self.guard:
+                self.inside += 1
+                self.most = max(self.most, self.inside)
+                self.calls.append((name, args))
+            time.sleep(self.seconds)
+            with self.guard:
+                self.inside -= 1
+            return 0
+        return call
+
+
+def host_cache(P, library, pages=8):
+    pool = torch.zeros(pages, TB, D, dtype=torch.int16).as_subclass(Device)
+    table = torch.full((2, 1, 2, HEADS, 2), -1, dtype=torch.int32)
+    c = P.PagedCache(P.SKV_BF16, 1, HEADS, D, TB, pool=pool, table=table,
+                     refs=torch.zeros(pages, dtype=torch.int32))
+    c._lib = library
+    c._index = -1                                   # what get_device() says of host tensors
+    c._current_device, c._raw_stream = (lambda: -1), (lambda index: 5)
+    c._capturing = lambda: False
+    c._empty = lambda shape, strides, dtype: torch.empty_strided(shape, strides, dtype=dtype)
+    c._attend_bytes = {4: 4096}
+    return c
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+def test_threads_on_one_stream_do_not_mix_their_launches(P):
+    """A call of several launches hands data from one to the next in the stream's workspace,
+    so no other call on it may be enqueued in between, from whichever thread."""
+    library = Library(0.02)
+    c = host_cache(P, library)
+    q = torch.zeros(1, 4, D, dtype=torch.bfloat16)
+    calls = [lambda: c.attend(0, ints(0), ints(1), q, 8), lambda: c.attend(0, ints(1), ints(3), q, 8),
+             lambda: c.reserve(ints(0), ints(0), ints(4)), lambda: c.fork(ints(0), ints(1), ints(4)),
+             lambda: c.compact(), lambda: c.free(ints(1)), lambda: c.clear()]
+    threads = [threading.Thread(target=f) for f in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert sorted(n for n, _ in library.calls) == sorted(
+        ["skv_cache_attend"] * 2 + ["skv_cache_" + n for n in ("reserve", "fork", "compact", "free",
+                                                              "init")])
+    assert library.most == 1
