@@ -337,7 +337,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
         // byte offsets in the pool of row 0 (the tile lies in one page) or of row lane % kTok
         int blk = ld_blk, tin = ld_off;
         if (!whole) {
-          const int t = min(t0 + lane % C::kTok, sp.end - 1);
+          // (only pages of the range are looked up: there may be none outside)
+          const int t = min(max(t0 + lane % C::kTok, sp.begin), sp.end - 1);
           blk = t / c.Tb;
           tin = t - blk * c.Tb;
         }
