@@ -637,7 +637,8 @@ size_t skv_cache_attend_workspace_bytes(const skv_cache *cache, int32_t batch, i
  *   lse          device fp32 [batch][q_heads], or NULL.
  * head_dim up to 256.  Products and sums are fp32 (the matrix unit's); before they
  * meet the values the weights are kept to 2^-16 (bf16 caches, two bf16 parts) or
- * 2^-11 (e4m3 caches, fp16).  The result does not depend on what else runs: a row is split and
+ * 2^-11 (e4m3 caches, fp16; a weight below 2^-25 of the row's largest to 2^-36 of
+ * that one).  The result does not depend on what else runs: a row is split and
  * joined in a fixed order for given lens, max_len and device.  A slot, length or page
  * out of range is reported (SKV_ERR_ARG); that row is empty, or that page's
  * tokens are left out. */

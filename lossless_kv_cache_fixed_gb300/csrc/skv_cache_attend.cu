@@ -2,8 +2,8 @@
 // KV cache.
 //
 // o_h = sum_t p_t v_t / sum_t p_t with p_t = 2^(x_t - m), x_t = log2(e) * scale *
-// q_h.k_t, m a running maximum (softmax in one pass: when m grows to m', the
-// sums so far are multiplied by 2^(m - m')).  Every key and value byte is used
+// q_h.k_t, m at a distance from the running maximum (softmax in one pass: when m grows
+// to m', the sums so far are multiplied by 2^(m - m')).  Every key and value byte is used
 // for 2 * group (bf16) or 4 * group (e4m3) operations, far below what the matrix
 // units need per byte of HBM, so HBM bounds the call and the design is about
 // keeping loads in flight:
@@ -22,8 +22,8 @@
 // group of up to 8 heads wastes no row and the running maximum, the sum and O^T
 // share one column layout (no exchange to rescale).  P goes from the accumulator
 // to the operand layout by movmatrix.  e4m3 codes become fp16 (exact); q becomes
-// fp16 after a power-of-two scale per head, which loses nothing above 2^-24 of
-// the head's largest channel.
+// fp16 after a power-of-two scale per head: the largest channel lies in [1, 2), so
+// channels down to 2^-17 of it are exact and smaller ones are off by 2^-25 of it at most.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -41,7 +41,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kRowCost = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.f;  // x may pass m by this before the sums are rescaled (p <= 2^8)
 
 template <int ES, int DP, int NT>
 struct Cfg {
@@ -57,6 +56,13 @@ struct Cfg {
   static constexpr int kSmem = kWarps * kStages * 2 * kTile;
   static constexpr int kPerSm = 220 * 1024 / (kSmem + 1024) < 4 ? 220 * 1024 / (kSmem + 1024) : 4;
   static constexpr int kHeads = 8 * NT;
+  // m is set kLift below the running maximum when x - m passes kMost, so p <= 2^kMost.  For
+  // e4m3 p meets the values as fp16, which ends at 2^16 above, holds 11 bits down to 2^-14
+  // and nothing below 2^-25: with the largest weight at 2^11 to 2^15, weights keep 11 bits
+  // down to 2^-25 of it and the others are off by 2^-36 of it at most (105 us for 32 rows of
+  // up to 16384 tokens and 39.2 for 256 of up to 512, as without).  bf16 has a float's
+  // exponent.
+  static constexpr float kLift = ES == 1 ? 11.f : 0.f, kMost = ES == 1 ? 15.f : 8.f;
   // floats of a head's row where the warps are joined: the 4 padding floats put what a
   // warp stores at once (8 channels of 4 heads) in different banks
   static constexpr int kPad = DP + 4;
@@ -532,7 +538,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
             x[mt][n][i] = v;
             top[n][i & 1] = fmaxf(top[n][i & 1], v);
           }
-        grow = grow || top[n][0] > m[n][0] + kSlack || top[n][1] > m[n][1] + kSlack;
+        // (the difference that the weights are made of: no rounding can pass kMost)
+        grow = grow || top[n][0] - m[n][0] > C::kMost || top[n][1] - m[n][1] > C::kMost;
       }
       if (__any_sync(~0u, grow)) {
 #pragma unroll
@@ -543,7 +550,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
             t = fmaxf(t, __shfl_xor_sync(~0u, t, 4));
             t = fmaxf(t, __shfl_xor_sync(~0u, t, 8));
             t = fmaxf(t, __shfl_xor_sync(~0u, t, 16));
-            const float mn = fmaxf(m[n][i], t);
+            // (beyond 2^23 a float has no room for kLift)
+            const float mn = fmaxf(m[n][i], fabsf(t) < 0x1p23f ? t - C::kLift : t);
             const float s = mn == -INFINITY ? 1.f : ex2(m[n][i] - mn);
             m[n][i] = mn;
             l[n][i] *= s;
