@@ -297,9 +297,12 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t st) {
   const size_t smem = (size_t)p.toks * (sizeof(float2) * pairs + 2 * sizeof(uint64_t) * heads) +
                       (c.dtype == 1 ? sizeof(float) * (size_t)c.heads : 0);
   auto kern = c.dtype == 1 ? k_append<true> : k_append<false>;
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+  // A launch has 48 KB, the kernel's own variables among them.  What is asked for is the most
+  // that any call takes (one token of 8192 heads, 512 pairs, 4096 scales), so that threads
+  // that launch at the same time do not lower it for one another.
+  constexpr int kFree = 47 * 1024, kMost = 148 * 1024;
+  if (smem > (size_t)kFree) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
   }
   return launch(kern, dim3((unsigned)((a.n + p.toks - 1) / p.toks)), kThreads, smem, st, a, p);
