@@ -100,11 +100,14 @@ __device__ __forceinline__ Item item_of(const CacheView &c, const Request &q, in
   return t;
 }
 
-// What k_free_list found: *go != 0 where the request goes through, and the first list
-// index of each item (base).
+// What k_free_list found: *go != 0 where the request goes through, the first list index of
+// each item (base) and how many pages it was counted for (need).  The kernel that hands
+// them out reads the items again, so it keeps to that many: lengths that are overwritten
+// meanwhile must not lead out of the list.
 struct Go {
   uint32_t *go;
   uint32_t *base;
+  uint32_t *need;
 };
 
 // Where k_check leaves what it found: need[i] pages for item i, bad[i*parts + part], free
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_small_list(CacheView c, Reque
       }
     }
   }
-  // prefixes of need (at most kSmallEntries) and of the free pages
+  // prefixes of need (at most 4 kSmallEntries) and of the free pages
   const uint32_t mine = __popc(free_mask);
   const uint32_t upto_need = warp_prefix(need), upto_free = warp_prefix(mine);
   if (lane == 31) {
@@ -355,7 +358,10 @@ __global__ void __launch_bounds__(kSmallThreads) k_small_list(CacheView c, Reque
     if (verdict) atomicOr(c.status, verdict);
   }
   if (verdict) return;
-  if ((int)threadIdx.x < q.n) go.base[threadIdx.x] = need0 + upto_need - need;
+  if ((int)threadIdx.x < q.n) {
+    go.base[threadIdx.x] = need0 + upto_need - need;
+    go.need[threadIdx.x] = need;
+  }
   uint32_t k = free0 + upto_free - mine;
   for (uint32_t m = free_mask; m && k < want; m &= m - 1)
     list[k++] = threadIdx.x * kPer + (__ffs(m) - 1);
@@ -371,7 +377,7 @@ __global__ void __launch_bounds__(kThreads) k_reserve(CacheView c, Request q, Go
   if (!t.nb) return;
   const uint32_t *mine = list + go.base[i];
   uint32_t *own = c.table + (int64_t)t.slot * c.rows * c.blocks;
-  const uint32_t total = (uint32_t)c.rows * (uint32_t)t.nb;
+  const uint32_t total = min((uint32_t)c.rows * (uint32_t)t.nb, go.need[i]);
   for (uint32_t k = blockIdx.x * kThreads + threadIdx.x; k < total; k += gridDim.x * kThreads) {
     const uint32_t r = k / (uint32_t)t.nb;
     const uint32_t p = mine[k];
@@ -399,7 +405,7 @@ __global__ void __launch_bounds__(kThreads) k_fork(CacheView c, Request q, Go go
     own[b] = p;
     atomicAdd(c.refs + p, 1u);
   }
-  if (!t.tail) return;
+  if (!t.tail || r >= go.need[i]) return;
   const uint32_t p = list[go.base[i] + r];
   if (threadIdx.x == 0) {
     own[t.full] = p;
@@ -639,7 +645,7 @@ namespace {
 cudaError_t run_request(const CacheView &c, const Request &q, uint8_t *ws, cudaStream_t st) {
   const PagesWs w = pages_ws(c.pages, q.n);
   auto at = [&](size_t o) { return reinterpret_cast<uint32_t *>(ws + o); };
-  const Go go{at(w.go), at(w.base)};
+  const Go go{at(w.go), at(w.base), at(w.need)};
   uint32_t *list = at(w.list);
   cudaError_t e;
   // one block where it has little to read: all entries of the slots for a fork; for reserve
