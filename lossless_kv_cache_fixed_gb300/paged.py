@@ -382,7 +382,7 @@ class PagedCache:
         self._ints("copy_pages", n, src, dst)
         for t in (src_pool, dst_pool):
             if t is not None and (t.dtype != self.pool.dtype or t.shape[1:] != self.pool.shape[1:]
-                                  or not t.is_contiguous() or
+                                  or not t.is_contiguous() or not t.numel() or
                                   not (t.device == self.device or t.is_pinned())):
                 raise _bad("copy_pages: pools with pages like the cache's, on its device or pinned")
         self._check(self._lib.skv_cache_copy_pages(

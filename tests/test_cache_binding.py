@@ -79,3 +79,16 @@ def test_threads_on_one_stream_do_not_mix_their_launches(P):
         ["skv_cache_attend"] * 2 + ["skv_cache_" + n for n in ("reserve", "fork", "compact", "free",
                                                               "init")])
     assert library.most == 1
+
+
+@pytest.mark.parametrize("side", ["src_pool", "dst_pool"])
+def test_a_pool_without_pages_is_not_the_caches_own(P, side):
+    """The library takes a null pool for the cache's own, and an empty tensor's address is
+    null: such a pool is refused, not written to or read from in another's place."""
+    library = Library()
+    c = host_cache(P, library)
+    none = torch.empty(0, TB, D, dtype=torch.int16)
+    assert none.data_ptr() == 0
+    with pytest.raises(P.SkvError):
+        c.copy_pages(ints(1), ints(2), **{side: none})
+    assert not library.calls
