@@ -119,6 +119,21 @@ def _bad(what):
     return SkvError(SKV_ERR_ARG, what)
 
 
+# The pinned pools of copies that may still run, each with an event behind its copy: torch
+# knows which stream a device tensor is used on, but of pinned memory that a kernel reads or
+# writes it knows nothing, and would give a dropped pool to the next who asks.
+_in_flight = []
+_in_flight_lock = threading.Lock()
+
+
+def _keep(event, pools):
+    """Hold these pools until the event has passed (None: only let go of what has)."""
+    with _in_flight_lock:
+        _in_flight[:] = [x for x in _in_flight if not x[0].query()]
+        if event is not None:
+            _in_flight.append((event, pools))
+
+
 def _allocator(device):
     """empty(shape, strides, dtype) on the current device, which is `device`: torch's own
     short cut where it has it (1 us a call in place of 3), else torch.empty_strided."""
@@ -246,7 +261,7 @@ class PagedCache:
 
     def _on(self, stream, tensors, call):
         """`call` with `stream` current: what it allocates belongs to that stream, and the
-        tensors given stay allocated until the stream is past it."""
+        device tensors given stay allocated until the stream is past it."""
         with self.torch.cuda.stream(stream):
             for t in (*tensors, self.pool, self.table, self.refs, self._status, self.scale):
                 if t is not None:
@@ -296,7 +311,10 @@ class PagedCache:
 
     def status(self):
         """Raises the error gathered since the last call, if any.  Synchronizes."""
-        self._check(self._lib.skv_cache_status(self._ref, self._stream()), "paged cache")
+        rc = self._lib.skv_cache_status(self._ref, self._stream())
+        if _in_flight:
+            _keep(None, ())
+        self._check(rc, "paged cache")
 
     def page_of_chunk(self, slot, tokens):
         """The sequence's pages as Codec.decode_range wants them (a container of this
@@ -373,7 +391,9 @@ class PagedCache:
 
     def copy_pages(self, src, dst, src_pool=None, dst_pool=None, stream=None):
         """Page dst[i] of dst_pool = page src[i] of src_pool (None: the cache's pool; a
-        pool may be in pinned host memory)."""
+        pool may be in pinned host memory, and stays allocated until the copy is done.  The
+        pools of a copy that is captured into a graph are the caller's to keep, like
+        all that a graph uses)."""
         if stream is not None:
             return self._on(stream, [t for t in (src, dst, src_pool, dst_pool)
                                      if t is not None and t.is_cuda],
@@ -391,6 +411,11 @@ class PagedCache:
             None if dst_pool is None else dst_pool.data_ptr(),
             0 if dst_pool is None else dst_pool.shape[0], dst.data_ptr(), n, self._stream()),
             "skv_cache_copy_pages")
+        pinned = [t for t in (src_pool, dst_pool) if t is not None and not t.is_cuda]
+        if pinned and not self._capturing():
+            event = self.torch.cuda.Event()
+            event.record()
+            _keep(event, pinned)
 
     # -- tokens --
 

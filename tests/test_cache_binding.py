@@ -2,6 +2,7 @@
 tensors lie in host memory and the library is a stand-in that records its calls."""
 import threading
 import time
+import weakref
 
 import pytest
 import torch
@@ -92,3 +93,46 @@ def test_a_pool_without_pages_is_not_the_caches_own(P, side):
     with pytest.raises(P.SkvError):
         c.copy_pages(ints(1), ints(2), **{side: none})
     assert not library.calls
+
+
+class Event:
+    """Stands in for torch.cuda.Event: passed when the test says so."""
+    made = []
+
+    def __init__(self):
+        self.recorded = self.passed = False
+        self.made.append(self)
+
+    def record(self):
+        self.recorded = True
+
+    def query(self):
+        assert self.recorded
+        return self.passed
+
+
+@pytest.mark.parametrize("side", ["src_pool", "dst_pool"])
+def test_a_pinned_pool_lives_until_its_copy_is_done(P, side, monkeypatch):
+    """A kernel reads or writes the pool after the call has returned, and the caller may have
+    dropped it by then."""
+    monkeypatch.setattr(torch.cuda, "Event", Event)
+    Event.made = []
+    c = host_cache(P, Library())
+    pools = [torch.zeros(4, TB, D, dtype=torch.int16) for _ in range(2)]
+    alive = [weakref.ref(p) for p in pools]
+    while pools:
+        c.copy_pages(ints(1), ints(2), **{side: pools.pop(0)})
+    assert [e.recorded for e in Event.made] == [True, True]
+    assert alive[0]() is not None and alive[1]() is not None
+    Event.made[0].passed = True
+    c.status()                                          # lets go of what is done
+    assert alive[0]() is None and alive[1]() is not None
+    Event.made[1].passed = True
+    c.copy_pages(ints(1), ints(2))
+    c.status()
+    assert alive[1]() is None
+    # nothing is recorded for device pools, nor while a graph is captured
+    c.copy_pages(ints(1), ints(2), src_pool=torch.zeros(4, TB, D, dtype=torch.int16).as_subclass(Device))
+    c._capturing = lambda: True
+    c.copy_pages(ints(1), ints(2), **{side: torch.zeros(4, TB, D, dtype=torch.int16)})
+    assert len(Event.made) == 2
