@@ -287,14 +287,15 @@ class PagedCache:
                 raise _bad("%s: int32 vectors of one length on the cache's device" % what)
 
     def _heads(self, what, t, n, heads=None):
-        """Strides of a [tokens, heads, head_dim] tensor."""
+        """Token and head strides of a [tokens, heads, head_dim] tensor; 0 for a dimension of
+        one, where torch keeps any number and the library asks for multiples of 8."""
         shape = t.shape
         st = t.stride()
         if (t.dtype is not self._bf16 or len(shape) != 3 or shape[0] != n or
                 shape[2] != self.head_dim or t.get_device() != self._index or
                 (heads is not None and shape[1] != heads) or (st[2] != 1 and t.numel())):
             raise _bad("%s: bf16 [tokens, heads, head_dim], channels contiguous" % what)
-        return st
+        return st[0] if n > 1 else 0, st[1] if shape[1] > 1 else 0
 
     def _check(self, rc, what):
         if rc:

@@ -136,3 +136,24 @@ def test_a_pinned_pool_lives_until_its_copy_is_done(P, side, monkeypatch):
     c._capturing = lambda: True
     c.copy_pages(ints(1), ints(2), **{side: torch.zeros(4, TB, D, dtype=torch.int16)})
     assert len(Event.made) == 2
+
+
+def test_strides_of_dimensions_of_one_do_not_matter(P):
+    """One token, or one head: torch keeps any stride there, and no address depends on it."""
+    library = Library()
+    c = host_cache(P, library)
+    q = torch.zeros(4, D, 1, dtype=torch.bfloat16).permute(2, 0, 1)      # one token
+    assert q.is_contiguous() and q.stride(0) == 1
+    c.attend(0, ints(0), ints(1), q, 8)
+    (name, args), = library.calls
+    assert name == "skv_cache_attend" and args[7] % 8 == 0 and args[8] == D
+    kv = torch.zeros(HEADS, D, 1, dtype=torch.bfloat16).permute(2, 0, 1)
+    c.append(0, ints(0), ints(0), q, kv, kv)
+    wide = torch.zeros(3, D, 5, dtype=torch.bfloat16)
+    one = torch.as_strided(wide, (3, 1, D), (D, 3, 1))                   # one query head of three tokens
+    kv = torch.zeros(3, HEADS, D, dtype=torch.bfloat16)
+    c.append(0, ints(0, 0, 0), ints(0, 1, 2), one, kv, kv)
+    for _, args in library.calls[1:]:
+        t = args[3]._obj
+        assert all(getattr(t, f) % 8 == 0 for f, _ in P.SkvTokens._fields_ if "stride" in f)
+    assert library.calls[2][1][3]._obj.q_stride == D
