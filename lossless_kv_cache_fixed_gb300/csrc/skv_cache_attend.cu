@@ -50,8 +50,12 @@ struct Cfg {
   static constexpr int kTile = kTok * kRowB;         // bytes of a tile of K or V
   // 2 stages leave room for 3 blocks (12 warps) per SM, which hide one another's latency:
   // 107 us against 111 with 3 stages and 2 blocks for 32 rows of up to 16384 e4m3 tokens
-  // (64-channel e4m3 tiles are half as large: 3 stages, 4 blocks)
-  static constexpr int kStages = kTile <= 2048 ? 3 : DP == 256 ? 3 : 2;
+  // (64 channels of e4m3, half as many bytes: 59.7 with 2, 61.8 with 3, 62.7 with 4; 25.9, 26.8
+  // and 31.1 for 256 rows of up to 512).  256 channels: bf16 leaves one block of 4 warps per
+  // SM either way, and 3 stages are better (197 us against 204 for 32 rows of up to 8192);
+  // e4m3 has the room that the join of 16 heads takes (67 KB), though 2 would do for 8
+  // heads (107 us against 110).
+  static constexpr int kStages = DP == 256 ? 3 : 2;
   static constexpr int kUnit = kWarps * kTok;        // tokens of a unit
   static constexpr int kSmem = kWarps * kStages * 2 * kTile;
   static constexpr int kPerSm = 220 * 1024 / (kSmem + 1024) < 4 ? 220 * 1024 / (kSmem + 1024) : 4;
