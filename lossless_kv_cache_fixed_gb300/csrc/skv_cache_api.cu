@@ -15,7 +15,13 @@ constexpr size_t kAlign = 256;
 constexpr int32_t kMaxList = 4096;  // sequences of one page operation
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 cudaStream_t stream_of(skv_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
-int status_of(cudaError_t e) { return e == cudaSuccess ? SKV_OK : SKV_ERR_CUDA; }
+// An error is reported here, once: left with the runtime, the coder's next launch would
+// report it as its own.
+int status_of(cudaError_t e) {
+  if (e == cudaSuccess) return SKV_OK;
+  cudaGetLastError();
+  return SKV_ERR_CUDA;
+}
 
 int make_view(const skv_cache *k, CacheView *out) {
   if (!k || k->flags) return SKV_ERR_ARG;
@@ -77,11 +83,10 @@ int skv_cache_init(const skv_cache *cache, skv_stream_t stream) {
   if (int rc = make_view(cache, &c)) return rc;
   cudaStream_t st = stream_of(stream);
   const size_t entries = (size_t)c.seqs * (size_t)c.rows * (size_t)c.blocks;
-  if (cudaMemsetAsync(c.table, 0xff, sizeof(uint32_t) * entries, st) != cudaSuccess ||
-      cudaMemsetAsync(c.refs, 0, sizeof(uint32_t) * (size_t)c.pages, st) != cudaSuccess ||
-      cudaMemsetAsync(c.status, 0, sizeof(uint32_t), st) != cudaSuccess)
-    return SKV_ERR_CUDA;
-  return SKV_OK;
+  cudaError_t e = cudaMemsetAsync(c.table, 0xff, sizeof(uint32_t) * entries, st);
+  if (e == cudaSuccess) e = cudaMemsetAsync(c.refs, 0, sizeof(uint32_t) * (size_t)c.pages, st);
+  if (e == cudaSuccess) e = cudaMemsetAsync(c.status, 0, sizeof(uint32_t), st);
+  return status_of(e);
 }
 
 int skv_cache_status(const skv_cache *cache, skv_stream_t stream) {
@@ -89,10 +94,10 @@ int skv_cache_status(const skv_cache *cache, skv_stream_t stream) {
   if (int rc = make_view(cache, &c)) return rc;
   cudaStream_t st = stream_of(stream);
   uint32_t v = 0;
-  if (cudaMemcpyAsync(&v, c.status, sizeof(v), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
-      cudaMemsetAsync(c.status, 0, sizeof(v), st) != cudaSuccess ||
-      cudaStreamSynchronize(st) != cudaSuccess)
-    return SKV_ERR_CUDA;
+  cudaError_t e = cudaMemcpyAsync(&v, c.status, sizeof(v), cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaMemsetAsync(c.status, 0, sizeof(v), st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (int rc = status_of(e)) return rc;
   if (v & kCacheArg) return SKV_ERR_ARG;
   return v & kCacheCapacity ? SKV_ERR_CAPACITY : SKV_OK;
 }
@@ -236,7 +241,9 @@ int skv_cache_append(const skv_cache *cache, int32_t layer, const skv_rope *rope
 size_t skv_cache_attend_workspace_bytes(const skv_cache *cache, int32_t batch, int32_t q_heads) {
   CacheView c;
   if (make_view(cache, &c) || batch < 0 || q_heads <= 0 || q_heads % c.heads || c.D > 256) return 0;
-  return attend_ws_bytes(c, q_heads);
+  const size_t need = attend_ws_bytes(c, q_heads);
+  if (!need) cudaGetLastError();  // no device
+  return need;
 }
 
 int skv_cache_attend(const skv_cache *cache, int32_t layer, const int32_t *slots,
@@ -261,7 +268,7 @@ int skv_cache_attend(const skv_cache *cache, int32_t layer, const int32_t *slots
   if (q_stride % 8 || q_head_stride % 8) return SKV_ERR_ARG;
   if (!workspace || !aligned(workspace, kAlign)) return SKV_ERR_ARG;
   const size_t need = attend_ws_bytes(c, q_heads);
-  if (!need) return SKV_ERR_CUDA;  // no device
+  if (!need) return status_of(cudaErrorInvalidDevice);
   if (workspace_bytes < need) return SKV_ERR_CAPACITY;
   a.slots = slots;
   a.lens = lens;
