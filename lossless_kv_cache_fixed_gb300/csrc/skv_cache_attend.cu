@@ -907,6 +907,16 @@ cudaError_t run(const AttendArgs &a, int head_tiles, cudaStream_t st) {
   // 108 / 117; 2048 rows of 9 78.8 / 56.8.  e4m3, 64 rows of 5 units 8.6 / 7.2, of 9 8.9 /
   // 10.2; 256 rows of 9 16.2 / 14.7, of 17 22.3 / 23.5; 1024 rows of 17 61.2 / 58.3; 2048
   // rows of 5 49.3 / 38.6.
+  // A unit is 64 or 128 tokens: 32 KB of keys and values as at 128 channels for bf16 of 64
+  // and e4m3 of 256 channels, half of that for e4m3 of 64, twice that for bf16 of 256.  The
+  // same rule, rows of one length, cut / not cut, us: bf16 of 64, 8 rows of 9 units 7.7 /
+  // 10.2, 256 of 17 29.8 / 26.9, of 33 47.8 / 46.6, 512 of 33 87 / 100 (the last blocks
+  // run alone), 2048 of 33 325 / 313; e4m3 of 64, 64 of 9 9.3 / 9.9, 256 of 17 19.6 / 18.0,
+  // 512 of 33 51.4 / 48.7, 2048 of 9 64 / 55, of 33 187 / 172; bf16 of 256, 8 of 9 9.0 /
+  // 11.8, 64 of 9 15.4 / 13.1, of 17 19.5 / 20.4, 256 of 17 50.2 / 49.1, 512 of 33 163 /
+  // 171; e4m3 of 256, 64 of 9 12.8 / 11.8, 256 of 17 31.9 / 28.1, of 33 51.7 / 47.4, 2048 of
+  // 33 339 / 319.  It is within 9% of the better side but for rows in two or three waves
+  // (512 of 33 units, bf16) and many rows of 17 to 33 units of e4m3 (up to 12%).
   const int64_t whole = ES == 2 ? (rows < 448 ? 5 + rows / 16 : 33)
                                 : (rows < 768 ? 5 + rows / 64 : 17);
   if (row_units <= whole) {
