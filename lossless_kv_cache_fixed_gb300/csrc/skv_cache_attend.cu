@@ -915,8 +915,9 @@ cudaError_t run(const AttendArgs &a, int head_tiles, cudaStream_t st) {
   // 512 of 33 51.4 / 48.7, 2048 of 9 64 / 55, of 33 187 / 172; bf16 of 256, 8 of 9 9.0 /
   // 11.8, 64 of 9 15.4 / 13.1, of 17 19.5 / 20.4, 256 of 17 50.2 / 49.1, 512 of 33 163 /
   // 171; e4m3 of 256, 64 of 9 12.8 / 11.8, 256 of 17 31.9 / 28.1, of 33 51.7 / 47.4, 2048 of
-  // 33 339 / 319.  It is within 9% of the better side but for rows in two or three waves
-  // (512 of 33 units, bf16) and many rows of 17 to 33 units of e4m3 (up to 12%).
+  // 33 339 / 319.  The rule's side is the slower one, by up to 15%, for rows in two waves
+  // (512 of 17 to 33 units, bf16) and by up to 14% for 256 and more rows of 17 to 33 units of
+  // e4m3, by 10% for 64 rows of 9 (bf16), elsewhere by less than 9% or not at all.
   const int64_t whole = ES == 2 ? (rows < 448 ? 5 + rows / 16 : 33)
                                 : (rows < 768 ? 5 + rows / 64 : 17);
   if (row_units <= whole) {
