@@ -185,7 +185,7 @@ class PagedCache:
     run on ``stream`` (a torch stream; default: the current one), outputs are
     allocated there; errors in the data show in ``status()``.  Several threads may
     call at once: each call's kernels are enqueued together (which of two calls comes
-    first is theirs to order)."""
+    first is theirs to order).  Results carry no gradient, whatever the inputs require."""
 
     def __init__(self, dtype, layers, heads, head_dim, page_tokens, num_pages=None, max_seqs=None,
                  max_blocks=None, scale=None, device="cuda", pool=None, table=None, refs=None):
