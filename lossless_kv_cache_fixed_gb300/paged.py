@@ -119,21 +119,6 @@ def _bad(what):
     return SkvError(SKV_ERR_ARG, what)
 
 
-# The pinned pools of copies that may still run, each with an event behind its copy: torch
-# knows which stream a device tensor is used on, but of pinned memory that a kernel reads or
-# writes it knows nothing, and would give a dropped pool to the next who asks.
-_in_flight = []
-_in_flight_lock = threading.Lock()
-
-
-def _keep(event, pools):
-    """Hold these pools until the event has passed (None: only let go of what has)."""
-    with _in_flight_lock:
-        _in_flight[:] = [x for x in _in_flight if not x[0].query()]
-        if event is not None:
-            _in_flight.append((event, pools))
-
-
 def _allocator(device):
     """empty(shape, strides, dtype) on the current device, which is `device`: torch's own
     short cut where it has it (1 us a call in place of 3), else torch.empty_strided."""
@@ -312,10 +297,7 @@ class PagedCache:
 
     def status(self):
         """Raises the error gathered since the last call, if any.  Synchronizes."""
-        rc = self._lib.skv_cache_status(self._ref, self._stream())
-        if _in_flight:
-            _keep(None, ())
-        self._check(rc, "paged cache")
+        self._check(self._lib.skv_cache_status(self._ref, self._stream()), "paged cache")
 
     def page_of_chunk(self, slot, tokens):
         """The sequence's pages as Codec.decode_range wants them (a container of this
@@ -392,9 +374,9 @@ class PagedCache:
 
     def copy_pages(self, src, dst, src_pool=None, dst_pool=None, stream=None):
         """Page dst[i] of dst_pool = page src[i] of src_pool (None: the cache's pool; a
-        pool may be in pinned host memory, and stays allocated until the copy is done.  The
-        pools of a copy that is captured into a graph are the caller's to keep, like
-        all that a graph uses)."""
+        pool may be in pinned host memory, which torch, if it pinned it, keeps until the
+        copy is done.  The pools of a copy that is captured into a graph are the caller's to
+        keep, like all that a graph uses)."""
         if stream is not None:
             return self._on(stream, [t for t in (src, dst, src_pool, dst_pool)
                                      if t is not None and t.is_cuda],
@@ -406,17 +388,25 @@ class PagedCache:
                                   or not t.is_contiguous() or not t.numel() or
                                   not (t.device == self.device or t.is_pinned())):
                 raise _bad("copy_pages: pools with pages like the cache's, on its device or pinned")
+        st = self._stream()
         self._check(self._lib.skv_cache_copy_pages(
             self._ref, None if src_pool is None else src_pool.data_ptr(),
             0 if src_pool is None else src_pool.shape[0], src.data_ptr(),
             None if dst_pool is None else dst_pool.data_ptr(),
-            0 if dst_pool is None else dst_pool.shape[0], dst.data_ptr(), n, self._stream()),
+            0 if dst_pool is None else dst_pool.shape[0], dst.data_ptr(), n, st),
             "skv_cache_copy_pages")
-        pinned = [t for t in (src_pool, dst_pool) if t is not None and not t.is_cuda]
-        if pinned and not self._capturing():
-            event = self.torch.cuda.Event()
-            event.record()
-            _keep(event, pinned)
+        if not self._capturing():
+            for t in (src_pool, dst_pool):
+                if t is not None and not t.is_cuda:
+                    self._used(t, st)
+
+    def _used(self, pool, stream):
+        """Tell torch's pinned allocator that this stream uses the pool up to here.  Of a
+        kernel's accesses it knows nothing, and would give a dropped pool to the next who
+        asks; a copy of its own out of it makes it wait.  (An event of our own would have to
+        be asked for, which breaks a capture that another thread is at.)"""
+        last = self._workspace("last", stream, 16)[2][:pool.element_size()].view(pool.dtype)
+        last.copy_(pool.view(-1)[:1], non_blocking=True)
 
     # -- tokens --
 

@@ -2,7 +2,6 @@
 tensors lie in host memory and the library is a stand-in that records its calls."""
 import threading
 import time
-import weakref
 
 import pytest
 import torch
@@ -95,47 +94,37 @@ def test_a_pool_without_pages_is_not_the_caches_own(P, side):
     assert not library.calls
 
 
-class Event:
-    """Stands in for torch.cuda.Event: passed when the test says so."""
-    made = []
+class Copies(torch.utils._python_dispatch.TorchDispatchMode):
+    """Records torch's own copies: where from, and how many calls the library had had by then."""
 
-    def __init__(self):
-        self.recorded = self.passed = False
-        self.made.append(self)
+    def __init__(self, library):
+        super().__init__()
+        self.library, self.seen = library, []
 
-    def record(self):
-        self.recorded = True
-
-    def query(self):
-        assert self.recorded
-        return self.passed
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        if func is torch.ops.aten.copy_.default:
+            last = (args + ((kwargs or {}).get("non_blocking", False),))[2]
+            self.seen.append((args[1].untyped_storage().data_ptr(), last, len(self.library.calls)))
+        return func(*args, **(kwargs or {}))
 
 
 @pytest.mark.parametrize("side", ["src_pool", "dst_pool"])
-def test_a_pinned_pool_lives_until_its_copy_is_done(P, side, monkeypatch):
+def test_a_pinned_pool_lives_until_its_copy_is_done(P, side):
     """A kernel reads or writes the pool after the call has returned, and the caller may have
-    dropped it by then."""
-    monkeypatch.setattr(torch.cuda, "Event", Event)
-    Event.made = []
-    c = host_cache(P, Library())
-    pools = [torch.zeros(4, TB, D, dtype=torch.int16) for _ in range(2)]
-    alive = [weakref.ref(p) for p in pools]
-    while pools:
-        c.copy_pages(ints(1), ints(2), **{side: pools.pop(0)})
-    assert [e.recorded for e in Event.made] == [True, True]
-    assert alive[0]() is not None and alive[1]() is not None
-    Event.made[0].passed = True
-    c.status()                                          # lets go of what is done
-    assert alive[0]() is None and alive[1]() is not None
-    Event.made[1].passed = True
-    c.copy_pages(ints(1), ints(2))
-    c.status()
-    assert alive[1]() is None
-    # nothing is recorded for device pools, nor while a graph is captured
-    c.copy_pages(ints(1), ints(2), src_pool=torch.zeros(4, TB, D, dtype=torch.int16).as_subclass(Device))
-    c._capturing = lambda: True
-    c.copy_pages(ints(1), ints(2), **{side: torch.zeros(4, TB, D, dtype=torch.int16)})
-    assert len(Event.made) == 2
+    dropped it by then: torch's allocator learns of it from a copy behind the kernel."""
+    library = Library()
+    c = host_cache(P, library)
+    pool = torch.zeros(4, TB, D, dtype=torch.int16)
+    with Copies(library) as copies:
+        c.copy_pages(ints(1), ints(2), **{side: pool})
+        assert copies.seen == [(pool.data_ptr(), True, 1)]
+        # not for device pools, nor while a graph is captured
+        c.copy_pages(ints(1), ints(2))
+        c.copy_pages(ints(1), ints(2), **{side: pool.clone().as_subclass(Device)})
+        c._capturing = lambda: True
+        copies.seen.clear()
+        c.copy_pages(ints(1), ints(2), **{side: pool})
+        assert not copies.seen
 
 
 def test_strides_of_dimensions_of_one_do_not_matter(P):

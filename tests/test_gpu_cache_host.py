@@ -66,3 +66,54 @@ def test_a_dropped_pinned_pool(other):
         c.status()
         assert torch.equal(c.pool[4:].cpu(), data)
         assert all(not t.any() for t in after)
+
+
+# One thread captures a graph (in torch's default mode, which forbids calls that wait or ask
+# for events in every thread), another copies pages to host memory meanwhile.
+CAPTURE = """
+import sys, threading
+sys.path[:0] = [%r]
+import torch
+import lossless_kv_cache_fixed_gb300 as P
+c = P.PagedCache(P.SKV_BF16, 1, 1, 64, 16, num_pages=8, max_seqs=1, max_blocks=1)
+c.pool.copy_(torch.arange(c.pool.numel(), device="cuda").view_as(c.pool) %% 30000)
+ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+src, dst = ints(3, 4), ints(0, 1)
+hosts = [torch.zeros(2, 16, 64, dtype=torch.int16).pin_memory() for _ in range(5)]
+side, stream = torch.cuda.Stream(), torch.cuda.Stream()
+c.copy_pages(src, dst, dst_pool=hosts[0], stream=side)
+x = torch.ones(1000, device="cuda")
+torch.cuda.synchronize()
+go, done, errors = threading.Event(), threading.Event(), []
+def work():
+    go.wait()
+    try:
+        for h in hosts[1:]:
+            c.copy_pages(src, dst, dst_pool=h, stream=side)
+    except Exception as e:
+        errors.append(e)
+    done.set()
+t = threading.Thread(target=work); t.start()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.stream(stream):
+    graph.capture_begin()
+    x.add_(1)
+    go.set(); done.wait()
+    x.add_(1)
+    graph.capture_end()
+t.join()
+graph.replay()
+torch.cuda.synchronize()
+print("captured", float(x[0]) == 3.0, errors, all(torch.equal(h, c.pool[3:5].cpu()) for h in hosts),
+      flush=True)
+"""
+
+
+def test_host_copies_while_another_thread_captures():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CAPTURE % root], capture_output=True, text=True,
+                       timeout=120)
+    assert "captured True [] True" in r.stdout, (r.stdout, r.stderr[-2000:])
