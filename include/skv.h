@@ -648,6 +648,80 @@ int skv_cache_attend(const skv_cache *cache, int32_t layer, const int32_t *slots
                      float softmax_scale, int32_t max_len, void *out, float *lse,
                      void *workspace, size_t workspace_bytes, skv_stream_t stream);
 
+/* The new tokens of a batch of sequences, and what they see.  The new tokens of
+ * sequence slots[i] are rows starts[i] .. starts[i + 1] - 1 of q and the last ones of its
+ * lens[i] tokens (their keys and values are in the pages already: skv_cache_append).
+ * A token at place p sees the tokens t with begins[i] <= t, t <= p and, with a window,
+ * t > p - window; with SKV_CHUNK_FULL all those begins[i] <= t < lens[i] above p - window.
+ *   batch        sequences.
+ *   tokens       rows of q and out; rows that no sequence names are left as they are.
+ *   max_len      host: no lens[i] is larger (it sizes the launch); heads * (tokens *
+ *                q_heads / heads / 64 + batch) * (max_len / 64 + 4) must be below 2^31.
+ *   window       tokens that a token sees, itself included; 0: no window.
+ *   flags        SKV_CHUNK_FULL or 0.
+ *   reserved     0.
+ *   slots, lens  device, i32 [batch]; a negative slot is padding.
+ *   begins       device, i32 [batch], or NULL: 0.
+ *   starts       device, i32 [batch + 1], not decreasing, 0 .. tokens; NULL: every
+ *                sequence has one new token, row i (tokens equals batch). */
+#define SKV_CHUNK_FULL 1
+typedef struct {
+  int32_t batch, tokens, max_len, window, flags, reserved;
+  const int32_t *slots, *lens, *begins, *starts;
+} skv_chunk;
+
+/* Workspace bytes of skv_cache_attend_chunk and skv_cache_attend_diff (any chunk and
+ * lengths); 0 if invalid.  The workspace (256-byte aligned) holds nothing between calls. */
+size_t skv_cache_attend_chunk_workspace_bytes(const skv_cache *cache, int32_t q_heads);
+
+/* Attention of the new tokens of each sequence over the pages of one layer: for row i
+ * of q, with head h reading the keys and values of kv head h / (q_heads / heads),
+ *   out[i][h] = sum_t w_t v_t,  w = softmax_t(softmax_scale * q[i][h] . k_t),
+ *   lse[i][h] = log sum_t exp(softmax_scale * q[i][h] . k_t),
+ * over the tokens t that the row sees.  A row that sees none (also one of padding, or
+ * with a place below 0) gives zeros and -infinity.  What a row does not see, NaN and
+ * infinities included, has no effect on it.
+ *   q            device bf16, (i, head, channel) at q[i * q_stride + head *
+ *                q_head_stride + channel]; strides multiples of 8, 16-byte aligned.
+ *   q_heads      a multiple of heads.
+ *   out          device bf16 [tokens][q_heads][head_dim], 16-byte aligned; may be q
+ *                itself when q has that layout.
+ *   lse          device fp32 [tokens][q_heads], or NULL.
+ * head_dim up to 256.  Products and sums are fp32; results do not depend on what else
+ * runs.  A slot, length or page out of range is reported (SKV_ERR_ARG); that
+ * sequence's rows are empty, or that page's tokens are left out.  Starts that decrease or
+ * leave 0 .. tokens are reported, and that sequence's rows left as they are. */
+int skv_cache_attend_chunk(const skv_cache *cache, int32_t layer, const skv_chunk *chunk,
+                           const void *q, int64_t q_stride, int64_t q_head_stride,
+                           int32_t q_heads, float softmax_scale, void *out, float *lse,
+                           void *workspace, size_t workspace_bytes, skv_stream_t stream);
+
+/* Differential attention.  A head's channels are two halves of head_dim / 2 in keys and
+ * queries, q = (q1, q2) and k = (k1, k2); its values have head_dim channels:
+ *   out[i][h] = sum_t (w1_t - lambda[h] * w2_t) v_t,
+ *   w1 = softmax_t(softmax_scale * q1 . k1_t),  w2 = softmax_t(softmax_scale * q2 . k2_t),
+ *   lse[i][h][m] = the log of the sum of exponentials of map m, m < 2,
+ * and, with a norm, out[i][h] times norm / sqrt(mean of its squares + eps).
+ *   lambda       device fp32 [q_heads].
+ *   norm         device fp32 [head_dim], or NULL.
+ *   eps          not negative.
+ *   reserved     0. */
+typedef struct {
+  const float *lambda, *norm;
+  float eps;
+  int32_t reserved;
+} skv_diff;
+
+/* Differential attention of the new tokens of each sequence (starts NULL: one each) over
+ * the pages of one layer; arguments, rows that see nothing and errors as
+ * skv_cache_attend_chunk, but head_dim a multiple of 16 and
+ *   lse          device fp32 [tokens][q_heads][2], or NULL. */
+int skv_cache_attend_diff(const skv_cache *cache, int32_t layer, const skv_chunk *chunk,
+                          const skv_diff *diff, const void *q, int64_t q_stride,
+                          int64_t q_head_stride, int32_t q_heads, float softmax_scale,
+                          void *out, float *lse, void *workspace, size_t workspace_bytes,
+                          skv_stream_t stream);
+
 /* Static description of a status code. */
 const char *skv_strerror(int status);
 

@@ -38,7 +38,8 @@ EXPORTS = ("skv_max_encoded_bytes", "skv_workspace_bytes", "skv_encode", "skv_en
            "skv_cache_init", "skv_cache_status", "skv_cache_workspace_bytes",
            "skv_cache_reserve", "skv_cache_fork", "skv_cache_free", "skv_cache_compact",
            "skv_cache_copy_pages", "skv_cache_append", "skv_cache_attend_workspace_bytes",
-           "skv_cache_attend")
+           "skv_cache_attend", "skv_cache_attend_chunk_workspace_bytes", "skv_cache_attend_chunk",
+           "skv_cache_attend_diff")
 
 
 class SkvParams(C.Structure):
@@ -464,8 +465,10 @@ class Codec:
 
 # ---- the paged cache (pages, append, attention) ----
 
-from .paged import (SIGNATURES, SKV_NO_PAGE, SKV_ROPE_INTERLEAVED, PagedCache,  # noqa: E402,F401
-                    Rope, SkvCache, SkvRope, SkvTokens, skv_cache_append, skv_cache_attend,
+from .paged import (SIGNATURES, SKV_CHUNK_FULL, SKV_NO_PAGE, SKV_ROPE_INTERLEAVED,  # noqa: E402,F401
+                    PagedCache, Rope, SkvCache, SkvChunk, SkvDiff, SkvRope, SkvTokens,
+                    skv_cache_append, skv_cache_attend, skv_cache_attend_chunk,
+                    skv_cache_attend_chunk_workspace_bytes, skv_cache_attend_diff,
                     skv_cache_attend_workspace_bytes, skv_cache_compact, skv_cache_copy_pages,
                     skv_cache_fork, skv_cache_free, skv_cache_init, skv_cache_reserve,
                     skv_cache_status, skv_cache_workspace_bytes)

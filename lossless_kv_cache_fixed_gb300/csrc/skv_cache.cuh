@@ -1,6 +1,6 @@
 // skv_cache.cuh -- what the paged-cache kernels (skv_cache_pages.cu,
-// skv_cache_append.cu, skv_cache_attend.cu) and their C ABI (skv_cache_api.cu)
-// share.  Not installed; not part of the ABI.
+// skv_cache_append.cu, skv_cache_attend.cu, skv_cache_chunk.cu) and their C ABI
+// (skv_cache_api.cu) share.  Not installed; not part of the ABI.
 #pragma once
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -111,5 +111,20 @@ struct AttendArgs {
 };
 size_t attend_ws_bytes(const CacheView &c, int32_t q_heads);
 cudaError_t launch_attend(const AttendArgs &a, cudaStream_t st);
+
+struct ChunkArgs {
+  CacheView c;
+  const int32_t *slots, *lens, *begins, *starts;
+  const uint16_t *q;
+  int64_t qs, qhs;
+  uint16_t *out;
+  float *lse;
+  const float *lambda, *norm;  // differential attention: lambda is not null
+  uint8_t *ws;
+  float scale, eps;
+  int32_t batch, tokens, q_heads, layer, max_len, window, full;
+};
+size_t chunk_ws_bytes(const CacheView &c, int32_t q_heads);
+cudaError_t launch_chunk(const ChunkArgs &a, cudaStream_t st);
 
 }  // namespace skv

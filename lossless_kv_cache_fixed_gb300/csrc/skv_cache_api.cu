@@ -74,6 +74,66 @@ int check_pages_ws(const CacheView &c, int32_t n, const void *ws, size_t bytes) 
   return bytes < pages_ws(c.pages, n).total ? SKV_ERR_CAPACITY : SKV_OK;
 }
 
+// What skv_cache_attend_chunk and skv_cache_attend_diff share; diff is null for the former.
+int attend_chunk(const skv_cache *cache, int32_t layer, const skv_chunk *k, const skv_diff *diff,
+                 const void *q, int64_t q_stride, int64_t q_head_stride, int32_t q_heads,
+                 float softmax_scale, void *out, float *lse, void *workspace,
+                 size_t workspace_bytes, skv_stream_t stream) {
+  ChunkArgs a;
+  if (int rc = make_view(cache, &a.c)) return rc;
+  const CacheView &c = a.c;
+  if (!k || layer < 0 || layer >= c.layers || q_heads <= 0 || q_heads % c.heads || c.D > 256 ||
+      (k->flags & ~SKV_CHUNK_FULL) || k->reserved || k->batch < 0 || k->tokens < 0 ||
+      k->window < 0 || k->max_len < 0 || k->max_len > INT_MAX - 1024)
+    return SKV_ERR_ARG;
+  if (!k->starts && k->tokens != k->batch) return SKV_ERR_ARG;
+  // the units of all rows, and the rows of all heads, are 32-bit
+  const int64_t group = q_heads / c.heads;
+  const int64_t items = (k->tokens * group / 64 + k->batch) * c.heads;
+  if (k->tokens * (int64_t)q_heads > INT_MAX || items > INT_MAX ||
+      items * (k->max_len / 64 + 4) > INT_MAX)
+    return SKV_ERR_ARG;
+  a.lambda = a.norm = nullptr;
+  a.eps = 0.f;
+  if (diff) {
+    if (!diff->lambda || !aligned(diff->lambda, 4) || !aligned(diff->norm, 4) || diff->reserved ||
+        !(diff->eps >= 0.f) || c.D % 16)
+      return SKV_ERR_ARG;
+    a.lambda = diff->lambda;
+    a.norm = diff->norm;
+    a.eps = diff->eps;
+  }
+  if (!k->batch || !k->tokens) return SKV_OK;
+  if (!k->slots || !k->lens || !q || !out || !aligned(k->slots, 4) || !aligned(k->lens, 4) ||
+      !aligned(k->begins, 4) || !aligned(k->starts, 4) || !aligned(q, 16) || !aligned(out, 16) ||
+      !aligned(lse, 4))
+    return SKV_ERR_ARG;
+  if (q_stride % 8 || q_head_stride % 8) return SKV_ERR_ARG;
+  if (!workspace || !aligned(workspace, kAlign)) return SKV_ERR_ARG;
+  const size_t need = chunk_ws_bytes(c, q_heads);
+  if (!need) return status_of(cudaErrorInvalidDevice);
+  if (workspace_bytes < need) return SKV_ERR_CAPACITY;
+  a.slots = k->slots;
+  a.lens = k->lens;
+  a.begins = k->begins;
+  a.starts = k->starts;
+  a.q = static_cast<const uint16_t *>(q);
+  a.qs = q_stride;
+  a.qhs = q_head_stride;
+  a.out = static_cast<uint16_t *>(out);
+  a.lse = lse;
+  a.ws = static_cast<uint8_t *>(workspace);
+  a.scale = softmax_scale;
+  a.batch = k->batch;
+  a.tokens = k->tokens;
+  a.q_heads = q_heads;
+  a.layer = layer;
+  a.max_len = k->max_len;
+  a.window = k->window;
+  a.full = (k->flags & SKV_CHUNK_FULL) ? 1 : 0;
+  return status_of(launch_chunk(a, stream_of(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -285,6 +345,32 @@ int skv_cache_attend(const skv_cache *cache, int32_t layer, const int32_t *slots
   a.layer = layer;
   a.max_len = max_len;
   return status_of(launch_attend(a, stream_of(stream)));
+}
+
+size_t skv_cache_attend_chunk_workspace_bytes(const skv_cache *cache, int32_t q_heads) {
+  CacheView c;
+  if (make_view(cache, &c) || q_heads <= 0 || q_heads % c.heads || c.D > 256) return 0;
+  const size_t need = chunk_ws_bytes(c, q_heads);
+  if (!need) cudaGetLastError();  // no device
+  return need;
+}
+
+int skv_cache_attend_chunk(const skv_cache *cache, int32_t layer, const skv_chunk *chunk,
+                           const void *q, int64_t q_stride, int64_t q_head_stride,
+                           int32_t q_heads, float softmax_scale, void *out, float *lse,
+                           void *workspace, size_t workspace_bytes, skv_stream_t stream) {
+  return attend_chunk(cache, layer, chunk, nullptr, q, q_stride, q_head_stride, q_heads,
+                      softmax_scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+int skv_cache_attend_diff(const skv_cache *cache, int32_t layer, const skv_chunk *chunk,
+                          const skv_diff *diff, const void *q, int64_t q_stride,
+                          int64_t q_head_stride, int32_t q_heads, float softmax_scale,
+                          void *out, float *lse, void *workspace, size_t workspace_bytes,
+                          skv_stream_t stream) {
+  if (!diff) return SKV_ERR_ARG;
+  return attend_chunk(cache, layer, chunk, diff, q, q_stride, q_head_stride, q_heads,
+                      softmax_scale, out, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

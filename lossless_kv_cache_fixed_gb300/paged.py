@@ -1,4 +1,5 @@
-"""A paged KV cache: its pages, the append of new tokens and attention over them.
+"""A paged KV cache: its pages, the append of new tokens and attention over them (of one new
+token per sequence, of chunks of them, differential).
 
 ``skv_cache_*`` mirror the C ABI in ``include/skv.h`` one to one; ``PagedCache``
 owns the buffers as torch tensors and ``Rope`` the tables of rotary positions.
@@ -13,6 +14,7 @@ from . import (SKV_BF16, SKV_E4M3, SKV_ERR_ARG, SkvError, lib)
 
 SKV_NO_PAGE = 0xFFFFFFFF
 SKV_ROPE_INTERLEAVED = 1
+SKV_CHUNK_FULL = 1
 
 
 class SkvCache(C.Structure):
@@ -35,6 +37,18 @@ class SkvTokens(C.Structure):
                 ("v_stride", C.c_int64), ("v_head_stride", C.c_int64)]
 
 
+class SkvChunk(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("tokens", C.c_int32), ("max_len", C.c_int32),
+                ("window", C.c_int32), ("flags", C.c_int32), ("reserved", C.c_int32),
+                ("slots", C.c_void_p), ("lens", C.c_void_p), ("begins", C.c_void_p),
+                ("starts", C.c_void_p)]
+
+
+class SkvDiff(C.Structure):
+    _fields_ = [("lambda_", C.c_void_p), ("norm", C.c_void_p), ("eps", C.c_float),
+                ("reserved", C.c_int32)]
+
+
 _vp, _i32, _i64, _u64, _sz = C.c_void_p, C.c_int32, C.c_int64, C.c_uint64, C.c_size_t
 _K = C.POINTER(SkvCache)
 SIGNATURES = {
@@ -51,6 +65,11 @@ SIGNATURES = {
     "skv_cache_attend_workspace_bytes": (_sz, [_K, _i32, _i32]),
     "skv_cache_attend": (C.c_int, [_K, _i32, _vp, _vp, _vp, _i32, _vp, _i64, _i64, _i32, C.c_float,
                                    _i32, _vp, _vp, _vp, _sz, _vp]),
+    "skv_cache_attend_chunk_workspace_bytes": (_sz, [_K, _i32]),
+    "skv_cache_attend_chunk": (C.c_int, [_K, _i32, C.POINTER(SkvChunk), _vp, _i64, _i64, _i32,
+                                         C.c_float, _vp, _vp, _vp, _sz, _vp]),
+    "skv_cache_attend_diff": (C.c_int, [_K, _i32, C.POINTER(SkvChunk), C.POINTER(SkvDiff), _vp,
+                                        _i64, _i64, _i32, C.c_float, _vp, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -111,6 +130,26 @@ def skv_cache_attend(cache, layer, slots_ptr, lens_ptr, begins_ptr, batch, q_ptr
     return lib().skv_cache_attend(C.byref(cache), layer, slots_ptr, lens_ptr, begins_ptr, batch,
                                   q_ptr, q_stride, q_head_stride, q_heads, softmax_scale, max_len,
                                   out_ptr, lse_ptr, ws_ptr, ws_bytes, stream)
+
+
+def skv_cache_attend_chunk_workspace_bytes(cache, q_heads):
+    return int(lib().skv_cache_attend_chunk_workspace_bytes(C.byref(cache), q_heads))
+
+
+def skv_cache_attend_chunk(cache, layer, chunk, q_ptr, q_stride, q_head_stride, q_heads,
+                           softmax_scale, out_ptr, lse_ptr, ws_ptr, ws_bytes, stream):
+    """chunk: an SkvChunk."""
+    return lib().skv_cache_attend_chunk(C.byref(cache), layer, C.byref(chunk), q_ptr, q_stride,
+                                        q_head_stride, q_heads, softmax_scale, out_ptr, lse_ptr,
+                                        ws_ptr, ws_bytes, stream)
+
+
+def skv_cache_attend_diff(cache, layer, chunk, diff, q_ptr, q_stride, q_head_stride, q_heads,
+                          softmax_scale, out_ptr, lse_ptr, ws_ptr, ws_bytes, stream):
+    """chunk: an SkvChunk; diff: an SkvDiff."""
+    return lib().skv_cache_attend_diff(C.byref(cache), layer, C.byref(chunk), C.byref(diff), q_ptr,
+                                       q_stride, q_head_stride, q_heads, softmax_scale, out_ptr,
+                                       lse_ptr, ws_ptr, ws_bytes, stream)
 
 
 # ---- torch convenience wrappers ----
@@ -225,6 +264,7 @@ class PagedCache:
         self._int32, self._bf16, self._f32 = torch.int32, torch.bfloat16, torch.float32
         self._empty = _allocator(self.device)
         self._attend_bytes = {}    # workspace bytes by q_heads
+        self._chunk_bytes = {}     # of attend_chunk and attend_diff
         self._pages_bytes = {}     # and of the page operations by n
         self._default_scale = head_dim ** -0.5
         self._lib = lib()
@@ -490,3 +530,96 @@ class PagedCache:
                 None if s is None else s.data_ptr(), ws[0], ws[1], st)
         self._check(rc, "skv_cache_attend")
         return (out, s) if lse else out
+
+    def _floats(self, what, t, n):
+        if (t.dtype is not self._f32 or t.dim() != 1 or t.numel() != n or
+                t.get_device() != self._index or not t.is_contiguous()):
+            raise _bad("%s: a float32 vector of %d on the cache's device" % (what, n))
+
+    def _chunk(self, what, layer, slots, lens, starts, begins, q, max_len, window, causal, scale,
+               out, lse, maps, diff):
+        """The call that attend_chunk (diff None) and attend_diff share; maps: sums of
+        exponentials per row and head."""
+        batch, d = slots.numel(), self.head_dim
+        self._ints(what, batch, slots, lens)
+        if begins is not None:
+            self._ints(what, batch, begins)
+        if starts is not None:
+            self._ints(what, batch + 1, starts)
+        n = q.shape[0] if starts is not None and q.dim() else batch
+        qs = self._heads(what + ": q", q, n)
+        q_heads = q.shape[1]
+        nb = self._chunk_bytes.get(q_heads)
+        if nb is None:
+            nb = skv_cache_attend_chunk_workspace_bytes(self.struct, q_heads)
+            if nb == 0:
+                raise _bad("%s: q_heads a multiple of the cache's heads, head_dim up to 256" % what)
+            self._chunk_bytes[q_heads] = nb
+        st = self._stream()
+        if out is None:
+            out = self._empty((n, q_heads, d), (q_heads * d, d, 1), self._bf16)
+        else:
+            self._heads(what + ": out", out, n, q_heads)
+            if not out.is_contiguous():
+                raise _bad("%s: out must be contiguous" % what)
+        s = None
+        if lse:
+            s = self._empty((n, q_heads), (q_heads, 1), self._f32) if maps == 1 else \
+                self._empty((n, q_heads, 2), (2 * q_heads, 2, 1), self._f32)
+        k = SkvChunk(batch, n, max_len, window, 0 if causal else SKV_CHUNK_FULL, 0,
+                     slots.data_ptr(), lens.data_ptr(),
+                     None if begins is None else begins.data_ptr(),
+                     None if starts is None else starts.data_ptr())
+        if scale is None:
+            scale = (d / maps) ** -0.5
+        more = () if diff is None else (C.byref(diff),)
+        call = self._lib.skv_cache_attend_chunk if diff is None else self._lib.skv_cache_attend_diff
+        with self._enqueue:
+            ws = self._workspace("chunk", st, nb)
+            rc = call(self._ref, layer, C.byref(k), *more, q.data_ptr(), qs[0], qs[1], q_heads,
+                      scale, out.data_ptr(), None if s is None else s.data_ptr(), ws[0], ws[1], st)
+        self._check(rc, what)
+        return (out, s) if lse else out
+
+    def attend_chunk(self, layer, slots, lens, starts, q, max_len, begins=None, window=0,
+                     causal=True, scale=None, out=None, lse=False, stream=None):
+        """Attention of the new tokens of each sequence, q [tokens, q_heads, D] bf16: rows
+        starts[i] .. starts[i + 1] - 1 are the last ones of the lens[i] tokens of sequence
+        slots[i] (max_len: no length is larger), whose keys and values are in the pages
+        already.  A token at place p sees the tokens begins[i] .. p (causal=False: to the
+        sequence's end), with a window those above p - window.  scale: default 1 /
+        sqrt(head_dim).  Returns out [tokens, q_heads, D], with lse=True also the log of the
+        sum of exponentials [tokens, q_heads]; rows that no sequence names are not
+        written."""
+        if starts is None:
+            raise _bad("attend_chunk: starts")
+        if stream is not None:
+            return self._on(stream, (slots, lens, starts, begins, q, out),
+                            lambda: self.attend_chunk(layer, slots, lens, starts, q, max_len,
+                                                      begins, window, causal, scale, out, lse))
+        return self._chunk("attend_chunk", layer, slots, lens, starts, begins, q, max_len, window,
+                           causal, scale, out, lse, 1, None)
+
+    def attend_diff(self, layer, slots, lens, q, lam, max_len, starts=None, norm=None, eps=1e-5,
+                    begins=None, window=0, causal=True, scale=None, out=None, lse=False,
+                    stream=None):
+        """Differential attention: with q = (q1, q2) and k = (k1, k2) in halves of a head's
+        channels, (softmax(q1 k1) - lam[head] softmax(q2 k2)) v of the new tokens of each
+        sequence, q [tokens, q_heads, D] bf16.  starts None: one new token per sequence
+        (row i); else as in attend_chunk, like the other arguments.  lam: float32
+        [q_heads]; norm: float32 [D] or None, with it each head's result is divided by
+        the root of its mean square + eps and multiplied by norm.  scale: default 1 /
+        sqrt(D / 2).  Returns out [tokens, q_heads, D], with lse=True also the logs of both
+        sums of exponentials [tokens, q_heads, 2]."""
+        if stream is not None:
+            return self._on(stream, (slots, lens, q, lam, starts, norm, begins, out),
+                            lambda: self.attend_diff(layer, slots, lens, q, lam, max_len, starts,
+                                                     norm, eps, begins, window, causal, scale, out,
+                                                     lse))
+        if q.dim() == 3:
+            self._floats("attend_diff: lam", lam, q.shape[1])
+        if norm is not None:
+            self._floats("attend_diff: norm", norm, self.head_dim)
+        diff = SkvDiff(lam.data_ptr(), None if norm is None else norm.data_ptr(), eps, 0)
+        return self._chunk("attend_diff", layer, slots, lens, starts, begins, q, max_len, window,
+                           causal, scale, out, lse, 2, diff)
