@@ -12,6 +12,7 @@ constexpr uint32_t kNoPage = 0xffffffffu;
 // bits of the cache's status word
 constexpr uint32_t kCacheArg = 1u;       // a slot, length or page out of range
 constexpr uint32_t kCacheCapacity = 2u;  // not enough free pages
+constexpr uint32_t kCacheStuck = 4u;     // a kernel gave up waiting for a part of itself
 
 // The cache as the kernels see it.  Row r of a sequence is (layer*2 + kv)*heads
 // + head; its table entries are at (slot*rows + r)*blocks.

@@ -158,6 +158,7 @@ int skv_cache_status(const skv_cache *cache, skv_stream_t stream) {
   if (e == cudaSuccess) e = cudaMemsetAsync(c.status, 0, sizeof(v), st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (int rc = status_of(e)) return rc;
+  if (v & kCacheStuck) return SKV_ERR_CUDA;
   if (v & kCacheArg) return SKV_ERR_ARG;
   return v & kCacheCapacity ? SKV_ERR_CAPACITY : SKV_OK;
 }
