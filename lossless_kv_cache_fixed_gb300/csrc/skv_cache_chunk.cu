@@ -25,6 +25,7 @@
 // What a row does not see must not touch it, and 0 * infinity is not 0: rows outside an item's
 // range are zeros in shared memory, and in blocks that some rows see only in part the values
 // that are not finite become 0, a flag is set, and the rows that see them get them in the end.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -42,7 +43,9 @@ constexpr int kItemCost = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kHoles = 16;       // blocks whose missing tokens are remembered
-constexpr uint64_t kPatience = 2000000000;  // ns that a barrier may take before a block gives up
+constexpr long long kPatience = 4000000000;  // clocks that a barrier may take before a block gives up
+
+constexpr uint32_t kDescHigh = 1024 >> 4 | 1u << 14 | 2u << 29;  // see desc_of
 
 template <int ES, int DP, bool DIFF>
 struct Cfg {
@@ -84,6 +87,7 @@ struct Seg {
 template <typename C>
 struct Misc {
   uint64_t q_full, q_empty, kv_full[C::kSlots], kv_empty[C::kSlots];
+  uint64_t raw_full[4], raw_empty[4];
   uint64_t s_full[2], p_full[2], o_full[2], seg_full[2], seg_empty[2], pair, last;
   uint32_t tmem, dead;
   Seg seg[2];
@@ -120,17 +124,24 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// an arrival that also waits for this many bytes of bulk copies
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// a box of the pool: x (channel), y (token of the page), z (page)
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y,
+                                         uint32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];" ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"((int)z)
+      : "memory");
+}
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{.reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p;}"
       : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok;
-}
-__device__ __forceinline__ uint64_t now() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
 }
 // writes to shared memory become visible to the matrix unit
 __device__ __forceinline__ void fence_async() {
@@ -142,23 +153,30 @@ __device__ __forceinline__ void fence_before() {
 __device__ __forceinline__ void fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
+// One lane of a warp, always the same.  What a matrix instruction takes lies in registers of the
+// whole warp: all lanes go through the same code with the same values, and one issues.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{.reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p;}" : "=r"(p));
+  return p;
+}
 // the barrier gets an arrival when all matrix instructions so far of this thread are done
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{.reg .pred p; setp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-      "r"((uint32_t)add)
+      "{.reg .pred p; .reg .b64 a, b; setp.ne.b32 p, %4, 0; mov.b64 a, {%1, %5}; mov.b64 b, {%2, %5};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;}" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+      "r"((uint32_t)add), "r"(kDescHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{.reg .pred p; setp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-      "r"((uint32_t)add)
+      "{.reg .pred p; .reg .b64 b; setp.ne.b32 p, %4, 0; mov.b64 b, {%2, %5};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;}" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+      "r"((uint32_t)add), "r"(kDescHigh)
       : "memory");
 }
 // 32 columns of this thread's row of tensor memory
@@ -209,6 +227,24 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// two floats at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long &>(d))
+      : "l"(reinterpret_cast<const unsigned long long &>(a)),
+        "l"(reinterpret_cast<const unsigned long long &>(b)),
+        "l"(reinterpret_cast<const unsigned long long &>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long &>(d))
+      : "l"(reinterpret_cast<const unsigned long long &>(a)),
+        "l"(reinterpret_cast<const unsigned long long &>(b)));
+  return d;
+}
 template <int ES>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   if (ES == 2) {
@@ -231,9 +267,10 @@ __device__ __forceinline__ void e4m3x4(uint32_t v, uint32_t &lo, uint32_t &hi) {
 __device__ __forceinline__ uint32_t swz(int rows, int row, int ch) {
   return (uint32_t)((ch >> 3) * rows * 128 + row * 128 + (((ch ^ row) & 7) << 4));
 }
-__device__ __forceinline__ uint64_t desc_of(uint32_t addr, uint32_t lbo) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(lbo >> 4) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// The low half of an operand's descriptor: address and lbo, both in 16 bytes; the high half is
+// the same for all.  Steps along an operand are added to the low half.
+__device__ __forceinline__ uint32_t desc_of(uint32_t addr, uint32_t lbo) {
+  return (addr & 0x3ffff) >> 4 | (lbo >> 4) << 16;
 }
 
 // A sequence of the batch.
@@ -242,7 +279,7 @@ struct Entry {
   int32_t rows, items;  // packed rows, items per kv head
 };
 template <typename C>
-__device__ __forceinline__ Entry entry_of(const ChunkArgs &a, int group, int b, bool tell) {
+__device__ __noinline__ Entry entry_of(const ChunkArgs &a, int group, int b, bool tell) {
   Entry e;
   e.slot = a.slots[b];
   e.len = a.lens[b];
@@ -264,7 +301,7 @@ struct Span {
   int32_t lo, hi, start, units;
 };
 template <typename C>
-__device__ __forceinline__ Span span_of(const ChunkArgs &a, int group, const Entry &e, int i) {
+__device__ __noinline__ Span span_of(const ChunkArgs &a, int group, const Entry &e, int i) {
   Span s;
   const int p0 = i * C::kItem, p1 = min(p0 + C::kItem, e.rows);
   const int base = e.len - e.n;
@@ -303,7 +340,8 @@ __device__ __forceinline__ void store8(float *p, const float *v) {
 }
 
 template <int ES, int DP, bool DIFF>
-__global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(ChunkArgs a, int cut) {
+__global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
+    ChunkArgs a, int cut, int box, const __grid_constant__ CUtensorMap map) {
   using C = Cfg<ES, DP, DIFF>;
   constexpr int kTiles = C::kTiles, kN = C::kN;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -318,11 +356,11 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
   auto wait1 = [&](uint64_t &bar, uint32_t parity) -> bool {
     const uint32_t b = smem_addr(&bar);
     if (bar_try(b, parity)) return true;
-    const uint64_t from = now();
+    const long long from = clock64();
     do {
       if (bar_try(b, parity)) return true;
       if (*reinterpret_cast<volatile uint32_t *>(&sh.dead)) return false;
-    } while (now() - from < kPatience);
+    } while (clock64() - from < kPatience);
     *reinterpret_cast<volatile uint32_t *>(&sh.dead) = 1;
     atomicOr(c.status, kCacheStuck);
     return false;
@@ -354,6 +392,10 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
       bar_init(smem_addr(&sh.seg_full[i]), 1);
       bar_init(smem_addr(&sh.seg_empty[i]), C::kSoftmax + 5);
     }
+    for (int i = 0; i < C::kRaws; ++i) {
+      bar_init(smem_addr(&sh.raw_full[i]), 1);
+      bar_init(smem_addr(&sh.raw_empty[i]), 4);
+    }
     bar_init(smem_addr(&sh.pair), 8);
     bar_init(smem_addr(&sh.last), 1);
     sh.dead = 0;
@@ -383,6 +425,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
       arrive(sh.pair);
       return wait(sh.pair, pairs++ & 1);
     };
+#pragma unroll 1
     for (uint32_t sidx = 0;; ++sidx) {
       Seg &s = sh.seg[sidx & 1];
       if (!wait(sh.seg_full[sidx & 1], (sidx >> 1) & 1)) break;
@@ -399,107 +442,127 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
         hi = place < 0 ? 0 : a.full ? s.len : min(s.len, place + 1);
       }
       const bool rows = DIFF || s.p0 + tile * 128 < s.p1;  // the tile has some
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY;
+      float2 l = make_float2(0.f, 0.f);  // two sums of the weights
+      bool far = false, some_far = false;  // |m| > 2^20; of a row of the warp
       float unit = 1.f;
       if (ES == 1 && c.scale) unit = c.scale[a.layer * c.heads + s.h];
       if (nu > 0 && rows) {
         float f = a.scale * kLog2e * unit;
+        // blocks from wlo to whi are seen by all rows of the warp
+        const int wlo = __reduce_max_sync(~0u, lo), whi = __reduce_min_sync(~0u, hi), first = s.t0;
+#pragma unroll 1
         for (int u = 0; u < nu; ++u) {
           const int buf = kTiles == 2 ? tile : (int)(mine & 1);
           const uint32_t phase = kTiles == 2 ? mine & 1 : (mine >> 1) & 1;
           if (!wait(sh.s_full[buf], phase)) break;
           fence_after();
-          if (u == 0) {
-            if (ES == 1) f *= __uint_as_float((uint32_t)sh.qe[sidx & 1][tile][r] << 23);
-            if (f == 0.f) f = 1.17549435e-38f;  // 0 * -infinity is not -infinity
-          }
+          if (ES == 1 && u == 0) f *= __uint_as_float((uint32_t)sh.qe[sidx & 1][tile][r] << 23);
           const uint32_t tm_s = lanes + buf * C::kS;
-          float x[kN];
-#pragma unroll
-          for (int i = 0; i < kN; i += 32) tm_ld32(x + i, tm_s + i);
-          tm_wait_ld();
-          const int t0 = s.t0 + u * kN;
+          const int t0 = first + u * kN;
           const uint4 hole = sh.holes[(blocks + u) % kHoles];
           const bool holes = hole.x | hole.y | hole.z | hole.w;
-          const float none = f < 0.f ? INFINITY : -INFINITY;
-          if (__any_sync(~0u, lo > t0 || hi < t0 + kN) || holes) {
-            const int from = lo - t0, to = hi - t0;
+          const bool edge = t0 < wlo || t0 + kN > whi || holes;
+          float fx = f;  // x = fx * what is in S
+          // The rare cases put x itself in S: masks, a negative f, and scores beyond 2^20, whose
+          // differences from m are exact only when they are rounded before, as m was.
+          auto settle = [&]() {
+            const bool mul = edge || f < 0.f || far;
+#pragma unroll 1
+            for (int i = 0; i < kN; i += 32) {
+              float x[32];
+              tm_ld32(x, tm_s + i);
+              tm_wait_ld();
+              uint32_t out = 0;  // tokens that this row does not see
+              if (edge) {
+                const int from = min(max(lo - t0 - i, 0), 32), to = min(max(hi - t0 - i, 0), 32);
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(&sh.holes[(blocks + u) % kHoles]);
+                out = kN == 128 ? w[i / 32] : (w[i / 16] & 0xffffu) | w[i / 16 + 1] << 16;
+                out |= ~(uint32_t)(((1ull << to) - 1) & ~((1ull << from) - 1));
+              }
 #pragma unroll
-            for (int i = 0; i < kN; ++i)
-              if (i < from || i >= to) x[i] = none;
-            if (holes) {
-              const uint32_t w[4] = {hole.x, hole.y, hole.z, hole.w};
-#pragma unroll
-              for (int i = 0; i < kN; ++i)
-                if (w[i / (kN / 4)] >> (i % (kN / 4)) & 1) x[i] = none;
+              for (int k = 0; k < 32; ++k) {
+                x[k] = mul ? __fmul_rn(x[k], f) : x[k];
+                if (out >> k & 1) x[k] = -INFINITY;
+              }
+              tm_st32(tm_s + i, x);
             }
-          }
-          float top;
-          {
-            float t[4];
-            if (f > 0.f) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) t[i] = x[i];
-#pragma unroll
-              for (int i = 4; i < kN; ++i) t[i & 3] = fmaxf(t[i & 3], x[i]);
-              top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * f;
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) t[i] = x[i];
-#pragma unroll
-              for (int i = 4; i < kN; ++i) t[i & 3] = fminf(t[i & 3], x[i]);
-              top = fminf(fminf(t[0], t[1]), fminf(t[2], t[3])) * f;
-            }
-          }
-          if (__any_sync(~0u, top - m > C::kMost)) {
-            // only rows that pass it change, so that no row's bits depend on another's
-            // (beyond 2^23 a float has no room for kLift)
-            const float mn = top - m > C::kMost ? (fabsf(top) < 0x1p23f ? top - C::kLift : top) : m;
-            const float by = mn == -INFINITY ? 1.f : ex2(m - mn);
-            m = mn;
-            l *= by;
-            if (u > 0) {
-              // With two buffers S may be there before the last product with the values is done
-              // (but not before the one before that, so the barrier is one phase ahead at most).
-              if (kTiles == 1 && !wait(sh.o_full[0], (mine - 1) & 1)) break;
-              fence_after();
-#pragma unroll
-              for (int d = 0; d < DP; d += 32) {
-                float o[32];
-                tm_ld32(o, tm_o + d);
+            tm_wait_st();
+            fx = mul ? 1.f : f;
+          };
+          bool settled = edge || f < 0.f || some_far;
+          if (settled) settle();
+          uint32_t w[kN / 2];
+          float2 sum[2];
+          // A guess: the weights with the m so far.  Where that lets one pass kMost, m grows and
+          // they are made again: S is there until the weights are written over it.
+          bool ok = true;
+#pragma unroll 1
+          for (int guess = u > 0 ? 0 : 1; guess < 2; ++guess) {
+            if (guess) {
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int i = 0; i < kN; i += 32) {
+                float x[32];
+                tm_ld32(x, tm_s + i);
                 tm_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= by;
-                tm_st32(tm_o + d, o);
+                for (int k = 0; k < 32; ++k) top = fmaxf(top, __fmul_rn(x[k], fx));
+              }
+              // only rows that pass it change, so that no row's bits depend on another's
+              // (beyond 2^23 a float has no room for kLift)
+              const float mn = top - m > C::kMost ? (fabsf(top) < 0x1p23f ? top - C::kLift : top) : m;
+              const float by = mn == -INFINITY ? 1.f : ex2(m - mn);
+              m = mn;
+              far = fabsf(m) > 0x1p20f && m != -INFINITY;
+              some_far = __any_sync(~0u, far);
+              l.x *= by;
+              l.y *= by;
+              if (u > 0) {
+                // With two buffers S may be there before the last product with the values is done
+                // (but not before the one before that, so the barrier is one phase ahead at most).
+                if (kTiles == 1 && !(ok = wait(sh.o_full[0], (mine - 1) & 1))) break;
+                fence_after();
+#pragma unroll 1
+                for (int d = 0; d < DP; d += 32) {
+                  float o[32];
+                  tm_ld32(o, tm_o + d);
+                  tm_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] *= by;
+                  tm_st32(tm_o + d, o);
+                }
+              }
+              if (some_far && !settled) settle();
+            }
+            const float m0 = m == -INFINITY ? 0.f : m;
+            const float2 f2 = make_float2(fx, fx), m2 = make_float2(-m0, -m0);
+            float t[2] = {-INFINITY, -INFINITY};
+            sum[0] = sum[1] = make_float2(0.f, 0.f);
+            float x[2][32];
+            tm_ld32(x[0], tm_s);
+#pragma unroll
+            for (int i = 0; i < kN; i += 32) {
+              float *y = x[(i >> 5) & 1];
+              tm_wait_ld();
+              if (i + 32 < kN) tm_ld32(x[((i >> 5) & 1) ^ 1], tm_s + i + 32);
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const float2 z = fma2(make_float2(y[k], y[k + 1]), f2, m2);
+                t[(k >> 1) & 1] = fmaxf(fmaxf(t[(k >> 1) & 1], z.x), z.y);
+                const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], e);
+                w[(i + k) / 2] = pack2<ES>(e.x, e.y);
               }
             }
+            if (guess == 0 &&
+                !__any_sync(~0u, fmaxf(t[0], t[1]) > (m == -INFINITY ? -INFINITY : C::kMost)))
+              break;
           }
-          const float m0 = m == -INFINITY ? 0.f : m;
-          // One rounding of the difference where that is exact enough; scores beyond 2^20 are
-          // rounded first, as m was, so that their differences are exact.
-          const bool far = fabsf(m0) > 0x1p20f;
-          if (__any_sync(~0u, far)) {
+          if (!ok) break;
 #pragma unroll
-            for (int i = 0; i < kN; ++i)
-              x[i] = far ? __fsub_rn(__fmul_rn(x[i], f), m0) : fmaf(x[i], f, -m0);
-          } else {
-#pragma unroll
-            for (int i = 0; i < kN; ++i) x[i] = fmaf(x[i], f, -m0);
-          }
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int i = 0; i < kN; i += 32) {
-            uint32_t w[16];
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              const float p0 = ex2(x[i + k]), p1 = ex2(x[i + k + 1]);
-              sum[k & 2] += p0;
-              sum[(k & 2) + 1] += p1;
-              w[k / 2] = pack2<ES>(p0, p1);
-            }
-            tm_st16(tm_s + i / 2, w);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          for (int i = 0; i < kN / 2; i += 16) tm_st16(tm_s + i, w + i);
+          l = add2(l, add2(sum[0], sum[1]));
           tm_wait_st();
           fence_before();
           arrive(sh.p_full[buf]);
@@ -513,143 +576,152 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
       } else if (nu > 0) {
         blocks += nu;
       }
-      const float m0 = m == -INFINITY ? 0.f : m;
+      const float m0 = m == -INFINITY ? 0.f : m, L = l.x + l.y;
       const int64_t oh = ((int64_t)s.q0 + j) * a.q_heads + head;
-      // values that are not finite, of partly masked blocks: those that this row sees
-      auto mend = [&](float *o, int d0) {
-        if (!s.fix || !on) return;
+      if (nu > 0 && rows && s.fix) {
+        // values that are not finite, of partly masked blocks: those that this row sees
         const int jl = (min(s.p0 + C::kItem, s.p1) - 1) / group;
         const int most = a.window ? (int)max((int64_t)s.begin, (int64_t)s.base + jl - a.window + 1) : s.begin;
         const int least = a.full ? s.len : min(s.len, s.base + s.p0 / group + 1);
-        const uint32_t *tab = c.table + ((int64_t)s.slot * c.rows +
-                                         ((int64_t)a.layer * 2) * c.heads + s.h) * c.blocks;
-        for (int u = 0; u < nu; ++u) {
-          const int t0 = s.t0 + u * kN;
-          if (t0 >= most && t0 + kN <= least) continue;
-          for (int t = max(t0, lo); t < min(t0 + kN, hi); ++t) {
-            const uint32_t pk = tab[t / c.Tb], pv = tab[(int64_t)c.heads * c.blocks + t / c.Tb];
-            if (pk >= c.pages || pv >= c.pages) continue;
-            const uint8_t *row = c.pool + (uint64_t)pv * c.page_bytes + (uint32_t)(t % c.Tb) * c.row_bytes;
+        const uint32_t *tab =
+            c.table + ((int64_t)s.slot * c.rows + ((int64_t)a.layer * 2) * c.heads + s.h) * c.blocks;
+#pragma unroll 1
+        for (int d = 0; d < c.D; d += 32) {
+          float o[32];
+          tm_ld32(o, tm_o + d);
+          tm_wait_ld();
+#pragma unroll 1
+          for (int u = 0; u < nu; ++u) {
+            const int t0 = s.t0 + u * kN;
+            if (!on || (t0 >= most && t0 + kN <= least)) continue;
+#pragma unroll 1
+            for (int t = max(t0, lo); t < min(t0 + kN, hi); ++t) {
+              const uint32_t pk = tab[t / c.Tb], pv = tab[(int64_t)c.heads * c.blocks + t / c.Tb];
+              if (pk >= c.pages || pv >= c.pages) continue;
+              const uint8_t *row = c.pool + (uint64_t)pv * c.page_bytes + (uint32_t)(t % c.Tb) * c.row_bytes;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (d0 + i >= c.D) continue;
-              if (ES == 2) {
-                const uint16_t w = reinterpret_cast<const uint16_t *>(row)[d0 + i];
-                if ((w & 0x7f80) == 0x7f80) o[i] += __uint_as_float((uint32_t)w << 16);
-              } else if ((row[d0 + i] & 0x7f) == 0x7f) {
-                o[i] = NAN;
+              for (int i = 0; i < 32; ++i) {
+                if (d + i >= c.D) continue;
+                if (ES == 2) {
+                  const uint16_t w = reinterpret_cast<const uint16_t *>(row)[d + i];
+                  if ((w & 0x7f80) == 0x7f80) o[i] += __uint_as_float((uint32_t)w << 16);
+                } else if ((row[d + i] & 0x7f) == 0x7f) {
+                  o[i] = NAN;
+                }
               }
             }
           }
+          __syncwarp();
+          tm_st32(tm_o + d, o);
         }
+        tm_wait_st();
+      }
+      // 8 channels of a result
+      auto write8 = [&](int d, const float *o, float by) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          float x0 = o[i] * by, x1 = o[i + 1] * by;
+          if (DIFF && a.norm) {
+            x0 *= a.norm[d + i];
+            x1 *= a.norm[d + i + 1];
+          }
+          w[i / 2] = pack2<2>(x0, x1);
+        }
+        *reinterpret_cast<uint4 *>(a.out + oh * c.D + d) = make_uint4(w[0], w[1], w[2], w[3]);
       };
       if (nu == 0) {
         if (on && (!DIFF || map == 0)) {
+#pragma unroll 1
           for (int d = 0; d < c.D; d += 8)
             *reinterpret_cast<uint4 *>(a.out + oh * c.D + d) = make_uint4(0, 0, 0, 0);
           if (a.lse)
             for (int i = 0; i < maps; ++i) a.lse[oh * maps + i] = -INFINITY;
         }
-      } else if (s.part && rows) {
+      } else if (rows && (s.part || !DIFF)) {
         Part<C, DP> &part =
-            reinterpret_cast<Part<C, DP> *>(a.ws + kCutBytes)[blockIdx.x * 2 + s.part - 1];
-#pragma unroll
-        for (int d = 0; d < DP; d += 32) {
-          if (d >= c.D) break;
+            reinterpret_cast<Part<C, DP> *>(a.ws + kCutBytes)[blockIdx.x * 2 + max(s.part - 1, 0)];
+        const float by = L == 0.f ? 0.f : unit / L;
+#pragma unroll 1
+        for (int d = 0; d < c.D; d += 32) {
           float o[32];
           tm_ld32(o, tm_o + d);
           tm_wait_ld();
-          mend(o, d);
-          if (on)
+          if (on && s.part) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8) store8(&part.o[tile * 128 + r][d + i], o + i);
-        }
-        if (on) {
-          part.m[tile * 128 + r] = m;
-          part.l[tile * 128 + r] = l;
-        }
-      } else if (!DIFF && rows) {
-        const float by = l == 0.f ? 0.f : unit / l;
-#pragma unroll
-        for (int d = 0; d < DP; d += 32) {
-          if (d >= c.D) break;
-          float o[32];
-          tm_ld32(o, tm_o + d);
-          tm_wait_ld();
-          mend(o, d);
-          if (on)
+          } else if (on) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8)
-              if (d + i < c.D)
-                *reinterpret_cast<uint4 *>(a.out + oh * c.D + d + i) =
-                    make_uint4(pack2<2>(o[i] * by, o[i + 1] * by), pack2<2>(o[i + 2] * by, o[i + 3] * by),
-                               pack2<2>(o[i + 4] * by, o[i + 5] * by), pack2<2>(o[i + 6] * by, o[i + 7] * by));
+              if (d + i < c.D) write8(d + i, o + i, by);
+          }
         }
-        if (on && a.lse) a.lse[oh] = (m0 + log2f(l)) * kLn2;
+        if (on && s.part) {
+          part.m[tile * 128 + r] = m;
+          part.l[tile * 128 + r] = L;
+        } else if (on && a.lse) {
+          a.lse[oh] = (m0 + log2f(L)) * kLn2;
+        }
       } else if (DIFF) {
-        if (on && a.lse) a.lse[oh * 2 + map] = (m0 + log2f(l)) * kLn2;
-        float by = l == 0.f ? 0.f : unit / l;
+        if (on && a.lse) a.lse[oh * 2 + map] = (m0 + log2f(L)) * kLn2;
+        float by = L == 0.f ? 0.f : unit / L;
         if (map && on) by *= a.lambda[head];
+        float n = 1.f, q = 0.f;
         if constexpr (kTiles == 2) {
           // each of the two threads of a row takes half of the channels of both maps
-          constexpr int kHalf = DP / 2;
           sh.l[map][r] = by;
+          fence_before();
           if (!both()) break;
           const float f0 = sh.l[0][r], f1 = sh.l[1][r];
           fence_after();
-          float o[kHalf], q = 0.f;
-          const int d0 = map * kHalf;
-#pragma unroll
-          for (int d = 0; d < kHalf; d += 32) {
-            float o1[32];
-            tm_ld32(o + d, lanes + C::kO + d0 + d);
-            tm_ld32(o1, lanes + C::kO + DP + d0 + d);
+#pragma unroll 1
+          for (int d = map * (DP / 2); d < min(c.D, (map + 1) * (DP / 2)); d += 32) {
+            float o[32], o1[32];
+            tm_ld32(o, lanes + C::kO + d);
+            tm_ld32(o1, lanes + C::kO + DP + d);
             tm_wait_ld();
-            mend(o + d, d0 + d);
-            mend(o1, d0 + d);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              o[d + i] = o[d + i] * f0 - o1[i] * f1;
-              if (d0 + d + i < c.D) q = fmaf(o[d + i], o[d + i], q);
+              o[i] = o[i] * f0 - o1[i] * f1;
+              if (d + i < c.D) q = fmaf(o[i], o[i], q);
+            }
+            if (a.norm) {
+              tm_st32(lanes + C::kO + d, o);
+            } else if (on) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+                if (d + i < c.D) write8(d + i, o + i, 1.f);
             }
           }
-          fence_before();
-          if (!both()) break;  // (neither tile's sums are overwritten before both are read)
-          float n = 1.f;
           if (a.norm) {
+            tm_wait_st();
+            if (!both()) break;  // (both have read the factors)
             sh.l[map][r] = q;
             if (!both()) break;
             q = sh.l[0][r] + sh.l[1][r];
             n = q == 0.f ? 0.f : rsqrtf(q / c.D + a.eps);
-            if (!both()) break;
-          }
-          if (on)
+#pragma unroll 1
+            for (int d = map * (DP / 2); d < min(c.D, (map + 1) * (DP / 2)); d += 32) {
+              float o[32];
+              tm_ld32(o, lanes + C::kO + d);
+              tm_wait_ld();
+              if (on)
 #pragma unroll
-            for (int d = 0; d < kHalf; d += 8) {
-              if (d0 + d >= c.D) break;
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 8; i += 2) {
-                float x0 = o[d + i] * n, x1 = o[d + i + 1] * n;
-                if (a.norm) {
-                  x0 *= a.norm[d0 + d + i];
-                  x1 *= a.norm[d0 + d + i + 1];
-                }
-                w[i / 2] = pack2<2>(x0, x1);
-              }
-              *reinterpret_cast<uint4 *>(a.out + oh * c.D + d0 + d) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int i = 0; i < 32; i += 8)
+                  if (d + i < c.D) write8(d + i, o + i, n);
             }
+          }
+          fence_before();
+          if (!both()) break;  // (neither tile's sums are overwritten before both are read)
         } else {
           // lanes i and i + 16 have a row's two maps
-          float n = 1.f, q = 0.f;
+#pragma unroll 1
           for (int pass = a.norm ? 0 : 1; pass < 2; ++pass) {
-#pragma unroll
-            for (int d = 0; d < DP; d += 32) {
-              if (d >= c.D) break;
+#pragma unroll 1
+            for (int d = 0; d < c.D; d += 32) {
               float o[32];
               tm_ld32(o, tm_o + d);
               tm_wait_ld();
-              mend(o, d);
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float x = o[i] * by, y = __shfl_xor_sync(~0u, x, 16);
@@ -658,20 +730,8 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
               }
               if (pass == 1 && on)
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                  if (d + i >= c.D || (i >> 4) != map) continue;
-                  uint32_t w[4];
-#pragma unroll
-                  for (int k = 0; k < 8; k += 2) {
-                    float x0 = o[i + k] * n, x1 = o[i + k + 1] * n;
-                    if (a.norm) {
-                      x0 *= a.norm[d + i + k];
-                      x1 *= a.norm[d + i + k + 1];
-                    }
-                    w[k / 2] = pack2<2>(x0, x1);
-                  }
-                  *reinterpret_cast<uint4 *>(a.out + oh * c.D + d + i) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
+                for (int i = 0; i < 32; i += 8)
+                  if (d + i < c.D && (i >> 4) == map) write8(d + i, o + i, n);
             }
             if (pass == 0) n = q == 0.f ? 0.f : rsqrtf(q / c.D + a.eps);
           }
@@ -690,6 +750,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
     uint32_t tiles = 0, blocks = 0;                  // K and V blocks so far; blocks
     bool alive = true;
     constexpr int kLag = 2;  // copies under way whose arrival is not told yet (bf16)
+#pragma unroll 1
     for (uint32_t sidx = 0; alive; ++sidx) {
       Seg &s = sh.seg[sidx & 1];
       if (!wait(sh.seg_full[sidx & 1], (sidx >> 1) & 1)) break;
@@ -705,86 +766,14 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
       arrive(sh.seg_empty[sidx & 1]);
       if (nu < 0) break;
       if (nu == 0) continue;
-      // ---- queries
-      if (!wait(sh.q_empty, (sidx & 1) ^ 1)) break;
-#pragma unroll 1
-      for (int t = 0; t < kTiles; ++t) {
-        const uint32_t dst = sm + t * C::kQ;
-        if (ES == 2) {
-          // packed row -> (token, head), step by step
-          int row = w * 32 + sub;
-          const int step = DIFF && kTiles == 1 ? 0 : kRpi;
-          int p = p0 + (!DIFF ? t * 128 + row : row);
-          int j = p / group, g = p - j * group;
-          const int dj = step / group, dg = step - dj * group;
-#pragma unroll 1
-          for (int i = 0; i < 32 / kRpi; ++i, row += kRpi) {
-            int map = t;
-            if (DIFF && kTiles == 1) {
-              p = p0 + (row >> 5) * 16 + (row & 15);
-              map = (row >> 4) & 1;
-              j = p / group;
-              g = p - j * group;
-            }
-            bool on = p < p1 && ch * 8 < c.D;
-            if (DIFF) {
-              // halves end at a multiple of 8 channels
-              const int half = c.D / 2;
-              if (map == 0 ? ch * 8 >= half : ch * 8 < half) on = false;
-            }
-            const uint16_t *src = a.q + ((int64_t)q0 + j) * a.qs + (int64_t)(h * group + g) * a.qhs + ch * 8;
-            cp_async16(dst + swz(128, row, ch), on ? src : a.q, on);
-            p += step;
-            j += dj;
-            g += dg;
-            if (g >= group) {
-              g -= group;
-              ++j;
-            }
-          }
-        } else {
-          // a thread per row: fp16 after a power of two, the largest channel in [1, 2)
-          const int row = w * 32 + lane;
-          int rr = !DIFF ? t * 128 + row : row, map = t;
-          if (DIFF && kTiles == 1) {
-            rr = (row >> 5) * 16 + (row & 15);
-            map = (row >> 4) & 1;
-          }
-          const int p = p0 + rr, j = p / group, g = p - j * group;
-          const uint16_t *src = a.q + ((int64_t)q0 + j) * a.qs + (int64_t)(h * group + g) * a.qhs;
-          int from = 0, to = c.D / 8;
-          if (DIFF) (map ? from : to) = c.D / 16;
-          if (p >= p1) to = from;
-          float mx = 0.f;
-          for (int k = from; k < to; ++k) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(src + k * 8);
-            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[i] << 16)),
-                                   fabsf(__uint_as_float(x[i] & 0xffff0000u))));
-          }
-          uint32_t ex = __float_as_uint(mx) >> 23;
-          if (ex < 1 || ex >= 253) ex = 127;  // kept where 1 / 2^(ex - 127) is normal
-          const float r = __uint_as_float((254 - ex) << 23);
-          for (int k = 0; k < kCpr; ++k) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (k >= from && k < to) {
-              v = *reinterpret_cast<const uint4 *>(src + k * 8);
-              uint32_t *x = &v.x;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                x[i] = pack2<1>(__uint_as_float(x[i] << 16) * r, __uint_as_float(x[i] & 0xffff0000u) * r);
-            }
-            sts128(dst + swz(128, row, k), v);
-          }
-          sh.qe[sidx & 1][t][row] = (uint8_t)ex;
-        }
-      }
       const uint32_t *tab_k =
           c.table + ((int64_t)slot * c.rows + ((int64_t)a.layer * 2) * c.heads + h) * c.blocks;
       const uint32_t *tab_v = tab_k + (int64_t)c.heads * c.blocks;
-      // byte offsets in the pool of this lane's row of a block, ~0 where it has none
+      auto masked = [&](int u) {
+        const int t0 = first + u * kN;
+        return t0 < most || t0 + kN > least;
+      };
+      // Byte offsets in the pool of this lane's row of a block, ~0 where it has none.
       uint64_t bk = ~0ull, bv = ~0ull;
       auto find = [&](int u) {
         const int t = first + u * kN + w * kRpw + lane % kRpw;
@@ -805,15 +794,109 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
           if (gone) atomicOr(c.status, kCacheArg);
         }
       };
-      auto masked = [&](int u) {
-        const int t0 = first + u * kN;
-        return t0 < most || t0 + kN > least;
+      // A block that all rows see, in whole boxes of existing pages, is copied by the TMA: lane i
+      // has box i.  Other blocks are copied row by row (zeros where there is nothing).
+      uint32_t pk = 0, pv = 0;
+      int off = 0;
+      auto boxes = [&](int u) -> bool {
+        if (!box || masked(u) || first + u * kN < lo || first + (u + 1) * kN > hi) return false;
+        const int t = first + u * kN + lane * box;
+        bool ok = true;
+        if (lane * box < kN) {
+          const int blk = t / c.Tb;
+          off = t - blk * c.Tb;
+          pk = tab_k[blk];
+          pv = tab_v[blk];
+          ok = pk < c.pages && pv < c.pages;
+        }
+        return __all_sync(~0u, ok);
+      };
+      auto no_holes = [&](int u) {
+        if (lane == 0) reinterpret_cast<uint32_t *>(&sh.holes[(blocks + u) % kHoles])[w] = 0;
+      };
+      auto queries = [&]() {
+#pragma unroll 1
+        for (int t = 0; t < kTiles; ++t) {
+          const uint32_t dst = sm + t * C::kQ;
+          if (ES == 2) {
+            // packed row -> (token, head), step by step
+            int row = w * 32 + sub;
+            const int step = DIFF && kTiles == 1 ? 0 : kRpi;
+            int p = p0 + (!DIFF ? t * 128 + row : row);
+            int j = p / group, g = p - j * group;
+            const int dj = step / group, dg = step - dj * group;
+#pragma unroll 1
+            for (int i = 0; i < 32 / kRpi; ++i, row += kRpi) {
+              int of = t;
+              if (DIFF && kTiles == 1) {
+                p = p0 + (row >> 5) * 16 + (row & 15);
+                of = (row >> 4) & 1;
+                j = p / group;
+                g = p - j * group;
+              }
+              bool on = p < p1 && ch * 8 < c.D;
+              if (DIFF) {
+                // halves end at a multiple of 8 channels
+                const int half = c.D / 2;
+                if (of == 0 ? ch * 8 >= half : ch * 8 < half) on = false;
+              }
+              const uint16_t *src = a.q + ((int64_t)q0 + j) * a.qs + (int64_t)(h * group + g) * a.qhs + ch * 8;
+              cp_async16(dst + swz(128, row, ch), on ? src : a.q, on);
+              p += step;
+              j += dj;
+              g += dg;
+              if (g >= group) {
+                g -= group;
+                ++j;
+              }
+            }
+          } else {
+            // a thread per row: fp16 after a power of two, the largest channel in [1, 2)
+            const int row = w * 32 + lane;
+            int rr = !DIFF ? t * 128 + row : row, of = t;
+            if (DIFF && kTiles == 1) {
+              rr = (row >> 5) * 16 + (row & 15);
+              of = (row >> 4) & 1;
+            }
+            const int p = p0 + rr, j = p / group, g = p - j * group;
+            const uint16_t *src = a.q + ((int64_t)q0 + j) * a.qs + (int64_t)(h * group + g) * a.qhs;
+            int from = 0, to = c.D / 8;
+            if (DIFF) (of ? from : to) = c.D / 16;
+            if (p >= p1) to = from;
+            float mx = 0.f;
+  #pragma unroll 1
+          for (int k = from; k < to; ++k) {
+              const uint4 v = *reinterpret_cast<const uint4 *>(src + k * 8);
+              const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[i] << 16)),
+                                     fabsf(__uint_as_float(x[i] & 0xffff0000u))));
+            }
+            uint32_t ex = __float_as_uint(mx) >> 23;
+            if (ex < 1 || ex >= 253) ex = 127;  // kept where 1 / 2^(ex - 127) is normal
+            const float r = __uint_as_float((254 - ex) << 23);
+#pragma unroll 2
+            for (int k = 0; k < kCpr; ++k) {
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (k >= from && k < to) {
+                v = *reinterpret_cast<const uint4 *>(src + k * 8);
+                uint32_t *x = &v.x;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  x[i] = pack2<1>(__uint_as_float(x[i] << 16) * r, __uint_as_float(x[i] & 0xffff0000u) * r);
+              }
+              sts128(dst + swz(128, row, k), v);
+            }
+            sh.qe[sidx & 1][t][row] = (uint8_t)ex;
+          }
+        }
       };
       if constexpr (ES == 2) {
-        cp_commit();
         // values that are not finite in this thread's chunks of a partly masked block
         auto clean = [&](uint32_t dst) {
           bool any = false;
+#pragma unroll 1
           for (int i = 0; i < kRpw / kRpi; ++i) {
             const int row = w * kRpw + i * kRpi + sub;
             uint4 v = lds128(dst + swz(kN, row, ch));
@@ -831,38 +914,76 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
           }
           if (any) s.fix = 1;
         };
-        auto tell = [&](int n) {  // n: 0 the queries, 1 + 2u K, 2 + 2u V of block u
-          if (n > 0 && !(n & 1) && masked(n / 2 - 1))
-            clean(sm + C::kOffSlots + (tiles + n - 1) % C::kSlots * C::kSlot);
+        // Copies of this item: K0, V0, K1, ...  Those of single rows are told kLag copies later.
+        bool bulk = false, bulk_before = true;
+        auto tell = [&](int n) {
+          const uint32_t i = tiles + n;
+          if ((n & 1) && masked(n / 2)) clean(sm + C::kOffSlots + i % C::kSlots * C::kSlot);
           fence_async();
-          arrive(n == 0 ? sh.q_full : sh.kv_full[(tiles + n - 1) % C::kSlots]);
+          arrive(sh.kv_full[i % C::kSlots]);
         };
-        const int copies = 1 + 2 * nu;
-        for (int n = 1; n < copies && alive; ++n) {
-          const uint32_t i = tiles + n - 1;
-          const int u = (n - 1) / 2;
-          const bool is_k = n & 1;
-          if (is_k) find(u);
+        const int copies = 2 * nu;
+#pragma unroll 1
+        for (int n = 0; n < copies; ++n) {
+          const uint32_t i = tiles + n;
+          const int u = n / 2;
+          const bool is_v = n & 1;
+          if (!is_v) {
+            bulk_before = n == 0 || bulk;
+            bulk = boxes(u);
+            if (bulk) no_holes(u);
+            else find(u);
+          }
           if (!wait(sh.kv_empty[i % C::kSlots], ((i / C::kSlots) & 1) ^ 1)) {
             alive = false;
             break;
           }
           const uint32_t dst = sm + C::kOffSlots + i % C::kSlots * C::kSlot;
-          const uint64_t from = is_k ? bk : bv;
+          if (bulk) {
+            const uint32_t bar = smem_addr(&sh.kv_full[i % C::kSlots]);
+            const int wide = (c.D + 63) / 64;
+            if (w == 0) {
+              if (lane == 0) bar_expect(bar, wide * kN * 128);
+              __syncwarp();
+              if (lane * box < kN)
+                for (int x = 0; x < wide; ++x)
+                  copy_box(dst + x * kN * 128 + lane * box * 128, &map, bar, x * 64, off, is_v ? pv : pk);
+            } else {
+              arrive(sh.kv_full[i % C::kSlots]);
+            }
+          } else {
+            const uint64_t from = is_v ? bv : bk;
 #pragma unroll 4
-          for (int x = 0; x < kRpw / kRpi; ++x) {
-            const int row = x * kRpi + sub;
-            const uint64_t b = __shfl_sync(~0u, from, row);
-            const bool on = b != ~0ull && ch * 8 < c.D;
-            cp_async16(dst + swz(kN, w * kRpw + row, ch), c.pool + (on ? b + ch * 16 : 0), on);
+            for (int x = 0; x < kRpw / kRpi; ++x) {
+              const int row = x * kRpi + sub;
+              const uint64_t b = __shfl_sync(~0u, from, row);
+              const bool on = b != ~0ull && ch * 8 < c.D;
+              cp_async16(dst + swz(kN, w * kRpw + row, ch), c.pool + (on ? b + ch * 16 : 0), on);
+            }
           }
           cp_commit();
-          if (n >= kLag) {
+          if (n == 1) {
+            // the queries, which wait for the end of the item before, after the first block
+            if (!wait(sh.q_empty, (sidx & 1) ^ 1)) {
+              alive = false;
+              break;
+            }
+            queries();
+            cp_commit();
+            cp_wait<0>();
+            fence_async();
+            arrive(sh.q_full);
+            if (!bulk) {
+              tell(0);
+              tell(1);
+            }
+            bulk = true;  // told
+          } else if (n >= kLag + 2 && !bulk_before) {
             cp_wait<kLag>();
             tell(n - kLag);
           }
         }
-        if (alive) {
+        if (alive && !bulk) {
           // (the next item's queries wait for this item's last block)
           cp_wait<1>();
           tell(copies - 2);
@@ -870,62 +991,107 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
           tell(copies - 1);
         }
       } else {
-        fence_async();
-        arrive(sh.q_full);
-        constexpr int kCprRaw = DP / 16, kRpiRaw = 32 / kCprRaw > 0 ? 32 / kCprRaw : 1;
+        constexpr int kCprRaw = DP / 16, kRpiRaw = 32 / kCprRaw;
         constexpr int kCopies = kRpw * kCprRaw / 32;  // chunks of 16 codes of a thread per block
         const int chr = lane % kCprRaw, subr = lane / kCprRaw;
-        const uint32_t raw = sm + C::kOffRaw + threadIdx.x % 128 * 16;
+        const uint32_t raw = sm + C::kOffRaw + (w * kRpw + subr) * DP + chr * 16;
         const int copies = 2 * nu;
-        auto fetch = [&](int n) {
+        bool bulk = false;
+        uint32_t bulks = 0;  // by copy, the last 32
+        auto fetch = [&](int n) -> bool {
+          bulks <<= 1;
           if (n < copies) {
-            if (!(n & 1)) find(n / 2);
-            const uint64_t from = n & 1 ? bv : bk;
-            const uint32_t dst = raw + (tiles + n) % C::kRaws * C::kRaw;
+            if (!(n & 1)) {
+              bulk = boxes(n / 2);
+              if (bulk) no_holes(n / 2);
+              else find(n / 2);
+            }
+            bulks |= bulk;
+            const uint32_t i = tiles + n, at = i % C::kRaws;
+            if (!wait(sh.raw_empty[at], ((i / C::kRaws) & 1) ^ 1)) return false;
+            if (bulk) {
+              const uint32_t bar = smem_addr(&sh.raw_full[at]);
+              if (w == 0) {
+                if (lane == 0) bar_expect(bar, C::kRaw);
+                __syncwarp();
+                if (lane * box < kN)
+                  copy_box(sm + C::kOffRaw + at * C::kRaw + lane * box * DP, &map, bar, 0, off, n & 1 ? pv : pk);
+              }
+            } else {
+              const uint64_t from = n & 1 ? bv : bk;
 #pragma unroll
-            for (int x = 0; x < kCopies; ++x) {
-              const uint64_t b = __shfl_sync(~0u, from, x * kRpiRaw + subr);
-              const bool on = b != ~0ull && chr * 16 < c.D;
-              cp_async16(dst + x * 2048, c.pool + (on ? b + chr * 16 : 0), on);
+              for (int x = 0; x < kCopies; ++x) {
+                const uint64_t b = __shfl_sync(~0u, from, x * kRpiRaw + subr);
+                const bool on = b != ~0ull && chr * 16 < c.D;
+                cp_async16(raw + at * C::kRaw + x * 512, c.pool + (on ? b + chr * 16 : 0), on);
+              }
+              if (w == 0) arrive(sh.raw_full[at]);  // (its phases count copies)
             }
           }
           cp_commit();
+          return true;
         };
-        for (int n = 0; n < C::kRaws - 1; ++n) fetch(n);
+#pragma unroll 1
+        for (int n = 0; n < C::kRaws - 1 && alive; ++n) alive = fetch(n);
+        if (!alive || !wait(sh.q_empty, (sidx & 1) ^ 1)) {
+          alive = false;
+          break;
+        }
+        queries();
+        fence_async();
+        arrive(sh.q_full);
+#pragma unroll 1
         for (int n = 0; n < copies; ++n) {
-          fetch(n + C::kRaws - 1);
+          const uint32_t i = tiles + n, at = i % C::kRaws;
+          if (!(alive = fetch(n + C::kRaws - 1))) break;
           cp_wait<C::kRaws - 1>();
-          const uint32_t i = tiles + n;
-          if (!wait(sh.kv_empty[i % C::kSlots], ((i / C::kSlots) & 1) ^ 1)) {
+          if (bulks >> (C::kRaws - 1) & 1) alive = wait(sh.raw_full[at], (i / C::kRaws) & 1);
+          if (!alive || !wait(sh.kv_empty[i % C::kSlots], ((i / C::kSlots) & 1) ^ 1)) {
             alive = false;
             break;
           }
-          const uint32_t src = raw + i % C::kRaws * C::kRaw;
           const uint32_t dst = sm + C::kOffSlots + i % C::kSlots * C::kSlot;
-          const bool check = (n & 1) && masked(n / 2);
           bool any = false;
-#pragma unroll
-          for (int x = 0; x < kCopies; ++x) {
-            uint4 v = lds128(src + x * 2048);
-            uint32_t *e = &v.x;
-            if (check) {
+          if ((n & 1) && masked(n / 2)) {
+#pragma unroll 1
+            for (int x = 0; x < kCopies; ++x) {
+              uint4 v = lds128(raw + at * C::kRaw + x * 512);
+              uint32_t *e = &v.x, bad = 0;
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const uint32_t bad = __vcmpeq4(e[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                e[k] &= ~bad;
-                any = any || bad;
+                const uint32_t m = __vcmpeq4(e[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                e[k] &= ~m;
+                bad |= m;
+              }
+              if (bad) {
+                sts128(raw + at * C::kRaw + x * 512, v);
+                any = true;
               }
             }
-            uint4 y0, y1;
-            e4m3x4(v.x, y0.x, y0.y);
-            e4m3x4(v.y, y0.z, y0.w);
-            e4m3x4(v.z, y1.x, y1.y);
-            e4m3x4(v.w, y1.z, y1.w);
-            const int row = w * kRpw + x * kRpiRaw + subr;
-            sts128(dst + swz(kN, row, 2 * chr), y0);
-            sts128(dst + swz(kN, row, 2 * chr + 1), y1);
+          }
+          constexpr int kOnce = kCopies < 4 ? kCopies : 4;
+#pragma unroll
+          for (int x0 = 0; x0 < kCopies; x0 += kOnce) {
+            uint4 v[kOnce];
+#pragma unroll
+            for (int x = 0; x < kOnce; ++x) v[x] = lds128(raw + at * C::kRaw + (x0 + x) * 512);
+#pragma unroll
+            for (int x = 0; x < kOnce; ++x) {
+              uint4 y0, y1;
+              e4m3x4(v[x].x, y0.x, y0.y);
+              e4m3x4(v[x].y, y0.z, y0.w);
+              e4m3x4(v[x].z, y1.x, y1.y);
+              e4m3x4(v[x].w, y1.z, y1.w);
+              const int row = w * kRpw + (x0 + x) * kRpiRaw + subr;
+              // (of 8 lanes that write at once, 4 write their second half first: the chunks of
+              // channels 64 apart lie in the same banks)
+              const bool turn = kCprRaw >= 8 && (chr & 4);
+              sts128(dst + swz(kN, row, 2 * chr + turn), turn ? y1 : y0);
+              sts128(dst + swz(kN, row, 2 * chr + !turn), turn ? y0 : y1);
+            }
           }
           if (any) s.fix = 1;
+          arrive(sh.raw_empty[at]);
           fence_async();
           arrive(sh.kv_full[i % C::kSlots]);
         }
@@ -935,106 +1101,125 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
       blocks += nu;
     }
     cp_wait<0>();
+    // a block that gives up may have bulk copies under way: they land within microseconds
+    if (!alive)
+      for (const long long from = clock64(); clock64() - from < 2000000;) {
+      }
   } else {
     regs_less<C::kRegsM>();
     if (warp == kMma) {
       // -------------------------------------------------------------- products
-      if (lane == 0) {
-        const uint32_t half = 1u << 4 | (ES == 2 ? 1u << 7 | 1u << 10 : 0) | 8u << 24;
-        const uint32_t dn = (c.D + 15) / 16 * 16;
-        const uint32_t idesc_s = half | (uint32_t)(kN / 8) << 17;
-        const uint32_t idesc_o = half | 1u << 16 | (dn / 8) << 17;
-        uint32_t tiles = 0, sbuf = 0, items = 0;
-        uint32_t np[2] = {0, 0};  // P of each tile (buffer) so far
-        auto slot_wait = [&](uint32_t i) {
-          return wait1(sh.kv_full[i % C::kSlots], (i / C::kSlots) & 1);
-        };
-        auto free_slot = [&](uint32_t i) { mma_commit(smem_addr(&sh.kv_empty[i % C::kSlots])); };
-        auto scores = [&](int t, int buf, uint32_t i) {  // S of tile t with the keys in copy i
-          const uint32_t q = sm + t * C::kQ, k = sm + C::kOffSlots + i % C::kSlots * C::kSlot;
-          int from = 0, to = (c.D + 15) / 16;
-          if (DIFF && kTiles == 2) {
-            if (t == 0) to = (c.D / 2 + 15) / 16;
-            else from = c.D / 2 / 16;
-          }
-          for (int x = from; x < to; ++x)
-            mma_ss(tmem + buf * C::kS, desc_of(q + (x >> 2) * (128 * 128) + (x & 3) * 32, 16),
-                   desc_of(k + (x >> 2) * (kN * 128) + (x & 3) * 32, 16), idesc_s, x > from);
+      const uint32_t half = 1u << 4 | (ES == 2 ? 1u << 7 | 1u << 10 : 0) | 8u << 24;
+      const uint32_t dn = (c.D + 15) / 16 * 16;
+      const uint32_t idesc_s = half | (uint32_t)(kN / 8) << 17;
+      const uint32_t idesc_o = half | 1u << 16 | (dn / 8) << 17;
+      const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+      uint32_t tiles = 0, sbuf = 0, items = 0;
+      uint32_t np0 = 0, np1 = 0;  // P of each tile so far
+      auto commit = [&](uint64_t &bar) {
+        if (elect()) mma_commit(smem_addr(&bar));
+      };
+      auto slot_wait = [&](uint32_t i) {
+        return wait(sh.kv_full[i % C::kSlots], (i / C::kSlots) & 1);
+      };
+      auto free_slot = [&](uint32_t i) { commit(sh.kv_empty[i % C::kSlots]); };
+      auto scores = [&](int t, int buf, uint32_t i) {  // S of tile t with the keys in copy i
+        const uint32_t q = desc_of(sm + t * C::kQ, 16);
+        const uint32_t k = desc_of(sm + C::kOffSlots + i % C::kSlots * C::kSlot, 16);
+        int from = 0, to = (c.D + 15) / 16;
+        if (DIFF && kTiles == 2) {
+          if (t == 0) to = (c.D / 2 + 15) / 16;
+          else from = c.D / 2 / 16;
+        }
+        if (elect()) {
+#pragma unroll
+          for (int x = 0; x < DP / 16; ++x)
+            if (x >= from && x < to)
+              mma_ss(tm + buf * C::kS, q + ((x >> 2) * (128 * 128) + (x & 3) * 32) / 16,
+                     k + ((x >> 2) * (kN * 128) + (x & 3) * 32) / 16, idesc_s, x > from);
           mma_commit(smem_addr(&sh.s_full[buf]));
-        };
-        auto sums = [&](int t, int buf, uint32_t i, bool add) {  // O of tile t += P V, V in copy i
-          const uint32_t v = sm + C::kOffSlots + i % C::kSlots * C::kSlot;
+        }
+        __syncwarp();
+      };
+      auto sums = [&](int t, int buf, uint32_t i, bool add) {  // O of tile t += P V, V in copy i
+        const uint32_t v = desc_of(sm + C::kOffSlots + i % C::kSlots * C::kSlot, kN * 128);
+        if (elect()) {
 #pragma unroll
           for (int x = 0; x < kN / 16; ++x)
-            mma_ts(tmem + C::kO + t * DP, tmem + buf * C::kS + x * 8, desc_of(v + x * 2048, kN * 128),
-                   idesc_o, add || x > 0);
-        };
-        for (uint32_t sidx = 0;; ++sidx) {
-          Seg &s = sh.seg[sidx & 1];
-          if (!wait1(sh.seg_full[sidx & 1], (sidx >> 1) & 1)) break;
-          const int nu = s.nu;
-          const bool two = kTiles == 2 && (DIFF || s.p0 + 128 < s.p1);
-          bar_arrive(smem_addr(&sh.seg_empty[sidx & 1]));
-          if (nu < 0) break;
-          if (nu == 0) {
-            mma_commit(smem_addr(&sh.q_empty));  // its phases count segments
-            continue;
-          }
-          if (!wait1(sh.q_full, items++ & 1) || !slot_wait(tiles)) break;
-          fence_after();
-          bool ok = true;
-          if constexpr (kTiles == 2) {
-            scores(0, 0, tiles);
-            if (two) scores(1, 1, tiles);
-            free_slot(tiles);
-            if (nu == 1) mma_commit(smem_addr(&sh.q_empty));
-            for (int u = 0; u < nu && ok; ++u) {
-              const uint32_t iv = tiles + 2 * u + 1, ik = iv + 1;
-              if (!(ok = slot_wait(iv))) break;
-              for (int t = 0; t < (two ? 2 : 1); ++t) {
-                if (!(ok = wait1(sh.p_full[t], np[t]++ & 1))) break;
+            mma_ts(tm + C::kO + t * DP, tm + buf * C::kS + x * 8, v + x * 2048 / 16, idesc_o,
+                   add || x > 0);
+        }
+        __syncwarp();
+      };
+#pragma unroll 1
+      for (uint32_t sidx = 0;; ++sidx) {
+        Seg &s = sh.seg[sidx & 1];
+        if (!wait(sh.seg_full[sidx & 1], (sidx >> 1) & 1)) break;
+        const int nu = __shfl_sync(~0u, s.nu, 0);
+        const bool two = kTiles == 2 && (DIFF || __shfl_sync(~0u, (int)(s.p0 + 128 < s.p1), 0));
+        arrive(sh.seg_empty[sidx & 1]);
+        if (nu < 0) break;
+        if (nu == 0) {
+          commit(sh.q_empty);  // its phases count segments
+          continue;
+        }
+        if (!wait(sh.q_full, items++ & 1) || !slot_wait(tiles)) break;
+        fence_after();
+        bool ok = true;
+        if constexpr (kTiles == 2) {
+          // tile by tile: the sums of block u, then the scores of block u + 1
+#pragma unroll 1
+          for (int u = -1; u < nu && ok; ++u) {
+            const uint32_t iv = tiles + 2 * u + 1, ik = iv + 1;
+            if (u >= 0 && !(ok = slot_wait(iv))) break;
+#pragma unroll 1
+            for (int t = 0; t < (two ? 2 : 1); ++t) {
+              if (u >= 0) {
+                if (!(ok = wait(sh.p_full[t], (t ? np1++ : np0++) & 1))) break;
                 fence_after();
                 sums(t, t, iv, u > 0);
-                if (t == (two ? 1 : 0)) free_slot(iv);
-                if (u + 1 < nu) {
-                  if (t == 0 && !(ok = slot_wait(ik))) break;
-                  scores(t, t, ik);
-                } else {
-                  mma_commit(smem_addr(&sh.o_full[t]));
-                }
               }
-              if (ok && u + 1 < nu) {
-                free_slot(ik);
-                if (u + 2 == nu) mma_commit(smem_addr(&sh.q_empty));
+              if (u + 1 < nu) {
+                if (t == 0 && u >= 0 && !(ok = slot_wait(ik))) break;
+                scores(t, t, ik);
+              } else {
+                commit(sh.o_full[t]);
               }
             }
-          } else {
-            scores(0, sbuf & 1, tiles);
-            free_slot(tiles);
-            if (nu == 1) mma_commit(smem_addr(&sh.q_empty));
-            for (int u = 0; u < nu && ok; ++u, ++sbuf) {
-              const uint32_t iv = tiles + 2 * u + 1, ik = iv + 1;
-              if (u + 1 < nu) {
-                if (!(ok = slot_wait(ik))) break;
-                scores(0, (sbuf + 1) & 1, ik);
-                free_slot(ik);
-                if (u + 2 == nu) mma_commit(smem_addr(&sh.q_empty));
-              }
-              if (!(ok = slot_wait(iv) && wait1(sh.p_full[sbuf & 1], (sbuf >> 1) & 1))) break;
-              fence_after();
-              sums(0, sbuf & 1, iv, u > 0);
-              free_slot(iv);
-              mma_commit(smem_addr(&sh.o_full[0]));
-              if (u + 1 == nu) mma_commit(smem_addr(&sh.o_full[1]));
+            if (ok && u >= 0) free_slot(iv);
+            if (ok && u + 1 < nu) {
+              free_slot(ik);
+              if (u + 2 == nu) commit(sh.q_empty);
             }
           }
-          if (!ok) break;
-          tiles += 2 * nu;
+        } else {
+#pragma unroll 1
+          for (int u = -1; u < nu && ok; ++u) {
+            const uint32_t iv = tiles + 2 * u + 1, ik = iv + 1;
+            if (u + 1 < nu) {
+              if (u >= 0 && !(ok = slot_wait(ik))) break;
+              scores(0, (sbuf + u + 1) & 1, ik);
+              free_slot(ik);
+              if (u + 2 == nu) commit(sh.q_empty);
+            }
+            if (u >= 0) {
+              const uint32_t n = sbuf + u;
+              if (!(ok = slot_wait(iv) && wait(sh.p_full[n & 1], (n >> 1) & 1))) break;
+              fence_after();
+              sums(0, n & 1, iv, u > 0);
+              free_slot(iv);
+              commit(sh.o_full[0]);
+              if (u + 1 == nu) commit(sh.o_full[1]);
+            }
+          }
+          sbuf += nu;
         }
-        // nothing of the matrix unit is in flight when the tensor memory is given back
-        mma_commit(smem_addr(&sh.last));
-        for (const uint64_t from = now(); !bar_try(smem_addr(&sh.last), 0) && now() - from < kPatience;) {
-        }
+        if (!ok) break;
+        tiles += 2 * nu;
+      }
+      // nothing of the matrix unit is in flight when the tensor memory is given back
+      commit(sh.last);
+      for (const long long from = clock64(); !bar_try(smem_addr(&sh.last), 0) && clock64() - from < kPatience;) {
       }
       __syncwarp();
     } else if (warp == kDeal) {
@@ -1044,11 +1229,13 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
       auto cost_of = [&](const Span &sp) -> uint32_t { return cut ? sp.units + kItemCost : 1; };
       auto one_cost = [&](const Entry &e) -> uint64_t {  // of one kv head, this lane alone
         uint64_t x = 0;
+#pragma unroll 1
         for (int i = 0; i < e.items; ++i) x += cost_of(span_of<C>(a, group, e, i));
         return x;
       };
       auto warp_cost = [&](const Entry &e) -> uint64_t {  // the same, all lanes
         uint64_t x = 0;
+#pragma unroll 1
         for (int i = lane; i < e.items; i += 32) x += cost_of(span_of<C>(a, group, e, i));
 #pragma unroll
         for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
@@ -1056,6 +1243,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
       };
       constexpr int kFew = 8;
       uint64_t own = 0;
+#pragma unroll 1
       for (int k = 0; k < per; ++k) {
         const int b = b0 + k;
         Entry e;
@@ -1063,6 +1251,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
         if (b < a.batch) e = entry_of<C>(a, group, b, blockIdx.x == 0);
         const bool big = e.items > kFew;
         if (!big) own += one_cost(e) * c.heads;
+#pragma unroll 1
         for (uint32_t todo = __ballot_sync(~0u, big); todo; todo &= todo - 1) {
           const int who = __ffs(todo) - 1;
           const Entry x = entry_of<C>(a, group, who * per + k, false);
@@ -1107,6 +1296,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
         int b = owner * per;
         Entry e = entry_of<C>(a, group, b, false);
         uint64_t x = warp_cost(e);
+#pragma unroll 1
         while (b + 1 < a.batch && pos >= at + x * c.heads) {
           at += x * c.heads;
           e = entry_of<C>(a, group, ++b, false);
@@ -1115,6 +1305,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
         const int h0 = x ? min((int)((pos - at) / x), c.heads - 1) : 0;
         at += x * h0;
         int i = 0;
+#pragma unroll 1
         for (;;) {  // 32 items at a time
           const uint32_t mine = i + lane < e.items ? cost_of(span_of<C>(a, group, e, i + lane)) : 0;
           uint32_t y = mine;
@@ -1137,6 +1328,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(Chun
         if (lane == 0) {
           int h = h0;
           bool ok = true;
+#pragma unroll 1
           while (ok && pos < stop && b < a.batch) {
             if (i >= e.items) {
               i = 0;
@@ -1265,6 +1457,35 @@ __global__ void __launch_bounds__(kJoin * 32) k_chunk_join(ChunkArgs a) {
   }
 }
 
+// Boxes of `rows` tokens of the pool's pages; false where the driver refuses them.
+using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                            const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                            CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                            CUtensorMapFloatOOBfill);
+bool map_pages(CUtensorMap *map, const CacheView &c, int channels, int rows) {
+  static std::atomic<void *> known{nullptr};
+  void *fn = known.load(std::memory_order_relaxed);
+  if (!fn) {
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      return false;
+    }
+    known.store(fn, std::memory_order_relaxed);
+  }
+  const bool codes = c.dtype == 1;
+  const cuuint64_t dims[3] = {(cuuint64_t)c.D, (cuuint64_t)c.Tb, c.pages};
+  const cuuint64_t strides[2] = {c.row_bytes, c.page_bytes};
+  const cuuint32_t sizes[3] = {(cuuint32_t)channels, (cuuint32_t)rows, 1}, steps[3] = {1, 1, 1};
+  return reinterpret_cast<Encode>(fn)(
+             map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c.pool, dims,
+             strides, sizes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int sm_count() {
   static std::atomic<int> known[64];  // by device; a device's SMs do not change
   int dev = 0, n = 0;
@@ -1300,7 +1521,12 @@ cudaError_t run(const ChunkArgs &a, cudaStream_t st) {
   }
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  e = launch(kern, dim3((unsigned)grid), C::kThreads, smem, st, a, cut);
+  // boxes of the largest power of two of tokens that pages are made of, 8 (a swizzle's) at least
+  CUtensorMap map = {};
+  int box = a.c.Tb & -a.c.Tb;
+  if (box > C::kN) box = C::kN;
+  if (box < 8 || a.c.pages > 0x7fffffff || !map_pages(&map, a.c, ES == 2 ? 64 : DP, box)) box = 0;
+  e = launch(kern, dim3((unsigned)grid), C::kThreads, smem, st, a, cut, box, map);
   if (e != cudaSuccess || !cut) return e;
   return launch(k_chunk_join<ES, DP, DIFF>, dim3((unsigned)grid, C::kItem / kJoin), kJoin * 32, 0, st, a);
 }

@@ -6,8 +6,8 @@ of round (2^-23 each), one multiplication and the exponential (2^-22): the weigh
 e = (2 (d + 8) * max_t sum_d |q_d k_d| * scale + tokens + 64) * 2^-23 relative (their sum is
 taken in fp32).  e4m3: q is held in fp16 after a power of two per row, which leaves at most
 2^-25 of its largest channel in each: e grows by that times sum_d |k_d|.  Weights round to
-bf16 (2^-8) or, for e4m3, to fp16 (2^-11, and by at most 2^-36 of the row's largest weight
-where that is more).  The result rounds to bf16 (2^-8)."""
+bf16 (2^-8) or, for e4m3, to fp16 (2^-11; where that is more, half of fp16's smallest step, 2^-25,
+with the row's largest weight at 2^8 or above: 2^-33 of that one).  The result rounds to bf16 (2^-8)."""
 import math
 
 import torch
@@ -58,7 +58,7 @@ def one_map(dtype, q, k, v, ok, scale):
     if dtype == 1:
         e = e + 2.0 ** -25 * q.abs().amax(1) * k.abs().sum(1).amax() * abs(scale)
     p = 2.0 ** -8 if dtype == 0 else 2.0 ** -11
-    tol = (p + 2 * e[:, None]) * absw + (2.0 ** -36 * absv if dtype == 1 else 0) + 1e-30
+    tol = (p + 2 * e[:, None]) * absw + (2.0 ** -33 * absv if dtype == 1 else 0) + 1e-30
     return out, lse, tol, e + 2.0 ** -22 * torch.where(none, 0.0, lse.abs())
 
 
