@@ -12,8 +12,8 @@ OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libskv.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["skv_code.cu", "skv_bits.cu", "skv_scale.cu", "skv_adapt.cu", "skv_api.cu",
-           "skv_cache_pages.cu", "skv_cache_append.cu", "skv_cache_attend.cu", "skv_cache_chunk.cu",
-           "skv_cache_api.cu"]
+           "skv_cache_pages.cu", "skv_cache_append.cu", "skv_cache_attend.cu",
+           "skv_cache_attend_diff.cu", "skv_cache_chunk.cu", "skv_cache_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

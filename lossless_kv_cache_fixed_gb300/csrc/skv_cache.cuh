@@ -1,5 +1,5 @@
 // skv_cache.cuh -- what the paged-cache kernels (skv_cache_pages.cu,
-// skv_cache_append.cu, skv_cache_attend.cu, skv_cache_chunk.cu) and their C ABI
+// skv_cache_append.cu, skv_cache_attend*, skv_cache_chunk.cu) and their C ABI
 // (skv_cache_api.cu) share.  Not installed; not part of the ABI.
 #pragma once
 #include <cuda_runtime.h>
@@ -109,9 +109,14 @@ struct AttendArgs {
   uint8_t *ws;
   float scale;
   int32_t batch, q_heads, layer, max_len;
+  int32_t window = 0;                               // tokens that are seen; 0: all
+  const float *lambda = nullptr, *norm = nullptr;   // differential attention
+  float eps = 0.f;
 };
 size_t attend_ws_bytes(const CacheView &c, int32_t q_heads);
 cudaError_t launch_attend(const AttendArgs &a, cudaStream_t st);
+size_t attend_diff_ws_bytes(const CacheView &c, int32_t q_heads);
+cudaError_t launch_attend_diff(const AttendArgs &a, cudaStream_t st);
 
 struct ChunkArgs {
   CacheView c;

@@ -91,7 +91,8 @@ int attend_chunk(const skv_cache *cache, int32_t layer, const skv_chunk *k, cons
   const int64_t group = q_heads / c.heads;
   const int64_t items = (k->tokens * group / 64 + k->batch) * c.heads;
   if (k->tokens * (int64_t)q_heads > INT_MAX || items > INT_MAX ||
-      items * (k->max_len / 64 + 4) > INT_MAX)
+      items * (k->max_len / 64 + 4) > INT_MAX ||
+      (!k->starts && (int64_t)k->batch * q_heads * (k->max_len / 64 + 4) > INT_MAX))
     return SKV_ERR_ARG;
   a.lambda = a.norm = nullptr;
   a.eps = 0.f;

@@ -18,7 +18,7 @@
 // tile while the softmax of the other runs; with one (more than 128 channels, whose sums take
 // half of the tensor memory), S has two buffers.
 //
-// Work is dealt as in skv_cache_attend.cu: the blocks of all items in a row, cut evenly over one
+// Work is dealt as in skv_cache_attend.cuh: the blocks of all items in a row, cut evenly over one
 // wave of persistent thread blocks whatever the lengths; items that lie in several leave partial
 // results, which k_chunk_join adds up in a fixed order.
 //
@@ -70,7 +70,7 @@ struct Cfg {
   // tensor memory columns
   static constexpr int kS = kN;            // S of a tile (or buffer); P in the first half
   static constexpr int kO = 2 * kN;        // O, DP columns per tile
-  // see skv_cache_attend.cu: m is kLift below the running maximum when x - m passes kMost
+  // see skv_cache_attend.cuh: m is kLift below the running maximum when x - m passes kMost
   static constexpr float kLift = ES == 1 ? 11.f : 0.f, kMost = ES == 1 ? 15.f : 8.f;
 };
 
@@ -313,7 +313,7 @@ __device__ __noinline__ Span span_of(const ChunkArgs &a, int group, const Entry 
   s.units = s.hi > s.lo ? (s.hi - s.start + C::kN - 1) / C::kN : 0;
   return s;
 }
-// How units are dealt: see skv_cache_attend.cu.
+// How units are dealt: see skv_cache_attend.cuh.
 __device__ __forceinline__ uint32_t deal(uint32_t W, uint32_t n, uint32_t i) {
   const uint32_t q = W / n;
   return i * q + i * (W - q * n) / n;
@@ -1540,16 +1540,40 @@ cudaError_t run_d(const ChunkArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-size_t chunk_ws_bytes(const CacheView &c, int32_t) {
+size_t chunk_ws_bytes(const CacheView &c, int32_t q_heads) {
   const int sms = sm_count();
   if (!sms) return 0;
   const size_t rows = c.D <= 128 ? 256 : 128, DP = c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256;
-  return kCutBytes + (size_t)sms * 2 * rows * (DP + 2) * sizeof(float);
+  const size_t chunk = kCutBytes + (size_t)sms * 2 * rows * (DP + 2) * sizeof(float);
+  const size_t one = attend_diff_ws_bytes(c, q_heads);
+  return chunk > one ? chunk : one;
 }
 
 cudaError_t launch_chunk(const ChunkArgs &a, cudaStream_t st) {
-  if (a.lambda) return a.c.dtype == 1 ? run_d<1, true>(a, st) : run_d<2, true>(a, st);
-  return a.c.dtype == 1 ? run_d<1, false>(a, st) : run_d<2, false>(a, st);
+  if (!a.lambda) return a.c.dtype == 1 ? run_d<1, false>(a, st) : run_d<2, false>(a, st);
+  if (a.starts) return a.c.dtype == 1 ? run_d<1, true>(a, st) : run_d<2, true>(a, st);
+  // one new token per sequence: nearly all of a tile's rows would be empty
+  AttendArgs b;
+  b.c = a.c;
+  b.slots = a.slots;
+  b.lens = a.lens;
+  b.begins = a.begins;
+  b.q = a.q;
+  b.qs = a.qs;
+  b.qhs = a.qhs;
+  b.out = a.out;
+  b.lse = a.lse;
+  b.ws = a.ws;
+  b.scale = a.scale;
+  b.batch = a.batch;
+  b.q_heads = a.q_heads;
+  b.layer = a.layer;
+  b.max_len = a.max_len;
+  b.window = a.window;
+  b.lambda = a.lambda;
+  b.norm = a.norm;
+  b.eps = a.eps;
+  return launch_attend_diff(b, st);
 }
 
 }  // namespace skv
