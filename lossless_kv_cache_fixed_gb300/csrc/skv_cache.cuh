@@ -118,8 +118,23 @@ cudaError_t launch_attend(const AttendArgs &a, cudaStream_t st);
 size_t attend_diff_ws_bytes(const CacheView &c, int32_t q_heads);
 cudaError_t launch_attend_diff(const AttendArgs &a, cudaStream_t st);
 
+// Division by a number that the host knows, of numbers below 2^31 (Granlund and Montgomery:
+// n / d = (n + floor(n m / 2^32)) >> s with s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1).
+struct Div {
+  uint32_t mul = 1, shift = 0;
+  Div() = default;
+  explicit Div(uint32_t d) {
+    while ((1ull << shift) < d) ++shift;
+    mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int of(int n) const {
+    return (int)(((uint32_t)n + __umulhi((uint32_t)n, mul)) >> shift);
+  }
+};
+
 struct ChunkArgs {
   CacheView c;
+  Div by_group, by_page;  // query heads of a kv head; tokens of a page
   const int32_t *slots, *lens, *begins, *starts;
   const uint16_t *q;
   int64_t qs, qhs;

@@ -54,9 +54,9 @@ struct Cfg {
   static constexpr int kItem = (DIFF ? 64 : 128) * kTiles;  // packed rows of an item
   static constexpr int kQ = 128 * DP * 2;                // bytes of a tile of queries
   static constexpr int kSlot = kN * DP * 2;              // bytes of a block of keys or values
-  static constexpr int kSlots = DP == 64 ? (ES == 2 ? 10 : 8) : (ES == 2 ? 5 : 3);
+  static constexpr int kSlots = DP == 64 ? (ES == 2 ? 10 : 8) : (ES == 2 ? 4 : 3);
   static constexpr int kRaw = kN * DP;                   // bytes of a block of codes
-  static constexpr int kRaws = ES == 1 ? 4 : 0;
+  static constexpr int kRaws = ES == 2 ? 0 : DP == 64 ? 4 : 3;
   static constexpr int kSoftmax = 4 * kTiles;            // warps of the softmax
   static constexpr int kThreads = (kSoftmax + 8) * 32;
   // registers per thread of the softmax, the loads and the others; their sum over the threads
@@ -66,12 +66,17 @@ struct Cfg {
   static constexpr int kRegs = 32 * (kSoftmax * kRegsS + 4 * kRegsL + 4 * kRegsM);
   static constexpr int kOffSlots = kTiles * kQ;
   static constexpr int kOffRaw = kOffSlots + kSlots * kSlot;
-  static constexpr int kOffMisc = kOffRaw + kRaws * kRaw;
+  static constexpr int kOffStage = kOffRaw + kRaws * kRaw;  // results on their way out, 2 KB a warp
+  static constexpr int kOffMisc = kOffStage + kSoftmax * 2048;
   // tensor memory columns
   static constexpr int kS = kN;            // S of a tile (or buffer); P in the first half
   static constexpr int kO = 2 * kN;        // O, DP columns per tile
-  // see skv_cache_attend.cuh: m is kLift below the running maximum when x - m passes kMost
-  static constexpr float kLift = ES == 1 ? 11.f : 0.f, kMost = ES == 1 ? 15.f : 8.f;
+  // A row's m grows, to kLift below its maximum, when a block's weights add up to more than kFull
+  // (so no weight is larger).  e4m3: weights meet the values as fp16, which ends at 2^16, holds
+  // 11 bits down to 2^-14 and nothing below 2^-25; with the largest weight at 2^8 to 2^15, and
+  // 128 of them at most 2^15, weights keep 11 bits down to 2^-22 of it and the others are off
+  // by 2^-33 of it at most.  bf16 has a float's exponent.
+  static constexpr float kLift = ES == 1 ? 8.f : 0.f, kFull = ES == 1 ? 0x1p15f : 0x1p20f;
 };
 
 // What a thread block works on: blocks of tokens of one item.
@@ -273,6 +278,18 @@ __device__ __forceinline__ uint32_t desc_of(uint32_t addr, uint32_t lbo) {
   return (addr & 0x3ffff) >> 4 | (lbo >> 4) << 16;
 }
 
+// A place in the ring of slots and the parity of its round.
+template <int N>
+struct Ring {
+  uint32_t at = 0, round = 0;
+  __device__ __forceinline__ Ring after() const {
+    Ring r;
+    r.at = at + 1 == N ? 0 : at + 1;
+    r.round = round ^ (at + 1 == N);
+    return r;
+  }
+};
+
 // A sequence of the batch.
 struct Entry {
   int32_t slot, len, begin, q0, n;
@@ -296,6 +313,17 @@ __device__ __noinline__ Entry entry_of(const ChunkArgs &a, int group, int b, boo
   e.items = (e.rows + C::kItem - 1) / C::kItem;
   return e;
 }
+__device__ __forceinline__ Entry from_lane(const Entry &e, int who) {
+  Entry r;
+  r.slot = __shfl_sync(~0u, e.slot, who);
+  r.len = __shfl_sync(~0u, e.len, who);
+  r.begin = __shfl_sync(~0u, e.begin, who);
+  r.q0 = __shfl_sync(~0u, e.q0, who);
+  r.n = __shfl_sync(~0u, e.n, who);
+  r.rows = __shfl_sync(~0u, e.rows, who);
+  r.items = __shfl_sync(~0u, e.items, who);
+  return r;
+}
 // The tokens [lo, hi) that item i of a sequence sees, in blocks from lo's one on.
 struct Span {
   int32_t lo, hi, start, units;
@@ -306,8 +334,8 @@ __device__ __noinline__ Span span_of(const ChunkArgs &a, int group, const Entry 
   const int p0 = i * C::kItem, p1 = min(p0 + C::kItem, e.rows);
   const int base = e.len - e.n;
   s.lo = e.begin;
-  if (a.window) s.lo = (int32_t)max((int64_t)s.lo, (int64_t)base + p0 / group - a.window + 1);
-  s.hi = a.full ? e.len : min(e.len, base + (p1 - 1) / group + 1);
+  if (a.window) s.lo = (int32_t)max((int64_t)s.lo, (int64_t)base + a.by_group.of(p0) - a.window + 1);
+  s.hi = a.full ? e.len : min(e.len, base + a.by_group.of(p1 - 1) + 1);
   if (s.hi < s.lo) s.hi = s.lo;
   s.start = s.lo / C::kN * C::kN;
   s.units = s.hi > s.lo ? (s.hi - s.start + C::kN - 1) / C::kN : 0;
@@ -318,10 +346,6 @@ __device__ __forceinline__ uint32_t deal(uint32_t W, uint32_t n, uint32_t i) {
   const uint32_t q = W / n;
   return i * q + i * (W - q * n) / n;
 }
-__device__ __forceinline__ int block_of(uint32_t W, uint32_t n, uint32_t u) {
-  return (int)((((uint64_t)u + 1) * n - 1) / W);
-}
-
 // What the join has to know of an item that begins in thread block i and ends in another.
 struct Cut {
   int32_t q0, p0, p1, h, parts;
@@ -334,11 +358,6 @@ struct Part {
 };
 constexpr size_t kCutBytes = (sizeof(Cut) * kMostBlocks + 255) / 256 * 256;
 
-__device__ __forceinline__ void store8(float *p, const float *v) {
-  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
-
 template <int ES, int DP, bool DIFF>
 __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
     ChunkArgs a, int cut, int box, const __grid_constant__ CUtensorMap map) {
@@ -350,15 +369,19 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheView &c = a.c;
   const int group = a.q_heads / c.heads;
-  constexpr int kLoad0 = C::kSoftmax, kMma = C::kSoftmax + 4, kDeal = C::kSoftmax + 5;
+  constexpr int kLoad0 = C::kSoftmax, kMma = C::kSoftmax + 4, kDeal = C::kSoftmax + 5,
+                kFetch = C::kSoftmax + 6;  // of codes
 
   // Waits for a phase of a barrier, with a limit: then the block gives up and says so.
   auto wait1 = [&](uint64_t &bar, uint32_t parity) -> bool {
     const uint32_t b = smem_addr(&bar);
     if (bar_try(b, parity)) return true;
+    // (the device's clock; the global timer takes a microsecond to read)
     const long long from = clock64();
     do {
-      if (bar_try(b, parity)) return true;
+#pragma unroll 1
+      for (int i = 0; i < 32; ++i)
+        if (bar_try(b, parity)) return true;
       if (*reinterpret_cast<volatile uint32_t *>(&sh.dead)) return false;
     } while (clock64() - from < kPatience);
     *reinterpret_cast<volatile uint32_t *>(&sh.dead) = 1;
@@ -390,10 +413,10 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       bar_init(smem_addr(&sh.p_full[i]), 4);
       bar_init(smem_addr(&sh.o_full[i]), 1);
       bar_init(smem_addr(&sh.seg_full[i]), 1);
-      bar_init(smem_addr(&sh.seg_empty[i]), C::kSoftmax + 5);
+      bar_init(smem_addr(&sh.seg_empty[i]), C::kSoftmax + 5 + (ES == 1));
     }
     for (int i = 0; i < C::kRaws; ++i) {
-      bar_init(smem_addr(&sh.raw_full[i]), 1);
+      bar_init(smem_addr(&sh.raw_full[i]), 32);
       bar_init(smem_addr(&sh.raw_empty[i]), 4);
     }
     bar_init(smem_addr(&sh.pair), 8);
@@ -433,7 +456,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       if (nu < 0) break;
       const int p = s.p0 + rr;
       const bool on = p < s.p1;
-      const int j = p / group, head = s.h * group + (p - j * group);
+      const int j = a.by_group.of(p), head = s.h * group + (p - j * group);
       const int place = s.base + j;
       int lo = 0, hi = 0x7fffffff;
       if (on) {
@@ -443,7 +466,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       }
       const bool rows = DIFF || s.p0 + tile * 128 < s.p1;  // the tile has some
       float m = -INFINITY;
-      float2 l = make_float2(0.f, 0.f);  // two sums of the weights
+      float l = 0.f;
       bool far = false, some_far = false;  // |m| > 2^20; of a row of the warp
       float unit = 1.f;
       if (ES == 1 && c.scale) unit = c.scale[a.layer * c.heads + s.h];
@@ -459,6 +482,8 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           fence_after();
           if (ES == 1 && u == 0) f *= __uint_as_float((uint32_t)sh.qe[sidx & 1][tile][r] << 23);
           const uint32_t tm_s = lanes + buf * C::kS;
+          float x[2][32];
+          tm_ld32(x[0], tm_s);
           const int t0 = first + u * kN;
           const uint4 hole = sh.holes[(blocks + u) % kHoles];
           const bool holes = hole.x | hole.y | hole.z | hole.w;
@@ -491,33 +516,37 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
             fx = mul ? 1.f : f;
           };
           bool settled = edge || f < 0.f || some_far;
-          if (settled) settle();
+          if (settled) {
+            settle();
+            tm_ld32(x[0], tm_s);
+          }
           uint32_t w[kN / 2];
-          float2 sum[2];
-          // A guess: the weights with the m so far.  Where that lets one pass kMost, m grows and
-          // they are made again: S is there until the weights are written over it.
+          float total = 0.f;
+          // The weights with the m so far.  Where they add up to more than kFull, or a row has
+          // not seen a token yet, m grows and they are made again: S is there until the weights
+          // are written over it.
           bool ok = true;
 #pragma unroll 1
-          for (int guess = u > 0 ? 0 : 1; guess < 2; ++guess) {
-            if (guess) {
+          for (int again = u > 0 ? 0 : 1; again < 2; ++again) {
+            if (again) {
+              // only rows that pass it change, so that no row's bits depend on another's
+              const bool grow = total > C::kFull || m == -INFINITY;
               float top = -INFINITY;
 #pragma unroll 1
               for (int i = 0; i < kN; i += 32) {
-                float x[32];
-                tm_ld32(x, tm_s + i);
+                float y[32];
+                tm_ld32(y, tm_s + i);
                 tm_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) top = fmaxf(top, __fmul_rn(x[k], fx));
+                for (int k = 0; k < 32; ++k) top = fmaxf(top, __fmul_rn(y[k], fx));
               }
-              // only rows that pass it change, so that no row's bits depend on another's
               // (beyond 2^23 a float has no room for kLift)
-              const float mn = top - m > C::kMost ? (fabsf(top) < 0x1p23f ? top - C::kLift : top) : m;
+              const float mn = grow ? (fabsf(top) < 0x1p23f ? top - C::kLift : top) : m;
               const float by = mn == -INFINITY ? 1.f : ex2(m - mn);
               m = mn;
               far = fabsf(m) > 0x1p20f && m != -INFINITY;
               some_far = __any_sync(~0u, far);
-              l.x *= by;
-              l.y *= by;
+              l *= by;
               if (u > 0) {
                 // With two buffers S may be there before the last product with the values is done
                 // (but not before the one before that, so the barrier is one phase ahead at most).
@@ -534,13 +563,11 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
                 }
               }
               if (some_far && !settled) settle();
+              tm_ld32(x[0], tm_s);
             }
             const float m0 = m == -INFINITY ? 0.f : m;
             const float2 f2 = make_float2(fx, fx), m2 = make_float2(-m0, -m0);
-            float t[2] = {-INFINITY, -INFINITY};
-            sum[0] = sum[1] = make_float2(0.f, 0.f);
-            float x[2][32];
-            tm_ld32(x[0], tm_s);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int i = 0; i < kN; i += 32) {
               float *y = x[(i >> 5) & 1];
@@ -549,20 +576,18 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
 #pragma unroll
               for (int k = 0; k < 32; k += 2) {
                 const float2 z = fma2(make_float2(y[k], y[k + 1]), f2, m2);
-                t[(k >> 1) & 1] = fmaxf(fmaxf(t[(k >> 1) & 1], z.x), z.y);
                 const float2 e = make_float2(ex2(z.x), ex2(z.y));
                 sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], e);
                 w[(i + k) / 2] = pack2<ES>(e.x, e.y);
               }
             }
-            if (guess == 0 &&
-                !__any_sync(~0u, fmaxf(t[0], t[1]) > (m == -INFINITY ? -INFINITY : C::kMost)))
-              break;
+            total = (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+            if (again == 0 && !__any_sync(~0u, total > C::kFull || m == -INFINITY)) break;
           }
           if (!ok) break;
 #pragma unroll
           for (int i = 0; i < kN / 2; i += 16) tm_st16(tm_s + i, w + i);
-          l = add2(l, add2(sum[0], sum[1]));
+          l += total;
           tm_wait_st();
           fence_before();
           arrive(sh.p_full[buf]);
@@ -576,13 +601,13 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       } else if (nu > 0) {
         blocks += nu;
       }
-      const float m0 = m == -INFINITY ? 0.f : m, L = l.x + l.y;
+      const float m0 = m == -INFINITY ? 0.f : m, L = l;
       const int64_t oh = ((int64_t)s.q0 + j) * a.q_heads + head;
       if (nu > 0 && rows && s.fix) {
         // values that are not finite, of partly masked blocks: those that this row sees
-        const int jl = (min(s.p0 + C::kItem, s.p1) - 1) / group;
+        const int jl = a.by_group.of(s.p1 - 1);
         const int most = a.window ? (int)max((int64_t)s.begin, (int64_t)s.base + jl - a.window + 1) : s.begin;
-        const int least = a.full ? s.len : min(s.len, s.base + s.p0 / group + 1);
+        const int least = a.full ? s.len : min(s.len, s.base + a.by_group.of(s.p0) + 1);
         const uint32_t *tab =
             c.table + ((int64_t)s.slot * c.rows + ((int64_t)a.layer * 2) * c.heads + s.h) * c.blocks;
 #pragma unroll 1
@@ -596,9 +621,9 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
             if (!on || (t0 >= most && t0 + kN <= least)) continue;
 #pragma unroll 1
             for (int t = max(t0, lo); t < min(t0 + kN, hi); ++t) {
-              const uint32_t pk = tab[t / c.Tb], pv = tab[(int64_t)c.heads * c.blocks + t / c.Tb];
+              const uint32_t pk = tab[a.by_page.of(t)], pv = tab[(int64_t)c.heads * c.blocks + a.by_page.of(t)];
               if (pk >= c.pages || pv >= c.pages) continue;
-              const uint8_t *row = c.pool + (uint64_t)pv * c.page_bytes + (uint32_t)(t % c.Tb) * c.row_bytes;
+              const uint8_t *row = c.pool + (uint64_t)pv * c.page_bytes + (uint32_t)(t - a.by_page.of(t) * c.Tb) * c.row_bytes;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 if (d + i >= c.D) continue;
@@ -616,19 +641,63 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         }
         tm_wait_st();
       }
-      // 8 channels of a result
-      auto write8 = [&](int d, const float *o, float by) {
-        uint32_t w[4];
+      // Results leave through shared memory, so that 4 lanes write 64 bytes of one row: a lane's
+      // own row in 16-byte pieces would be 32 rows per store (10000 clocks a tile, 2000 so).
+      const bool emits = on && !(DIFF && kTiles == 1 && lane >= 16);
+      uint32_t writes = 0;  // which of the four rows that this lane writes are there
+      int64_t to_row[4];
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          float x0 = o[i] * by, x1 = o[i + 1] * by;
-          if (DIFF && a.norm) {
-            x0 *= a.norm[d + i];
-            x1 *= a.norm[d + i + 1];
+      for (int i = 0; i < 4; ++i) {
+        to_row[i] = __shfl_sync(~0u, oh, i * 8 + (lane >> 2)) * c.D;
+        writes |= (uint32_t)__shfl_sync(~0u, (int)emits, i * 8 + (lane >> 2)) << i;
+      }
+      const uint32_t stage = sm + C::kOffStage + warp * 2048;
+      auto place_of = [&](int row, int piece) { return stage + row * 64 + ((piece ^ (row >> 1)) & 3) * 16; };
+      // 32 channels of the warp's rows, times by
+      auto emit = [&](int d, const float *o, float by) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float x0 = o[k * 8 + 2 * i] * by, x1 = o[k * 8 + 2 * i + 1] * by;
+            if (DIFF && a.norm && d + k * 8 < c.D) {
+              x0 *= a.norm[d + k * 8 + 2 * i];
+              x1 *= a.norm[d + k * 8 + 2 * i + 1];
+            }
+            w[i] = pack2<2>(x0, x1);
           }
-          w[i / 2] = pack2<2>(x0, x1);
+          sts128(place_of(lane, k), make_uint4(w[0], w[1], w[2], w[3]));
         }
-        *reinterpret_cast<uint4 *>(a.out + oh * c.D + d) = make_uint4(w[0], w[1], w[2], w[3]);
+        __syncwarp();
+        const int at = d + (lane & 3) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = lds128(place_of(i * 8 + (lane >> 2), lane & 3));
+          if ((writes >> i & 1) && at < c.D) *reinterpret_cast<uint4 *>(a.out + to_row[i] + at) = v;
+        }
+        __syncwarp();
+      };
+      // the same of a partial result, fp32
+      auto emit_part = [&](float (*to)[DP], int d, const float *o) {
+#pragma unroll
+        for (int half = 0; half < 32; half += 16) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float *x = o + half + k * 4;
+            sts128(place_of(lane, k), make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
+                                                 __float_as_uint(x[2]), __float_as_uint(x[3])));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = i * 8 + (lane >> 2);
+            const uint4 v = lds128(place_of(row, lane & 3));
+            if (__shfl_sync(~0u, (int)on, row))
+              *reinterpret_cast<uint4 *>(&to[row][d + half + (lane & 3) * 4]) = v;
+          }
+          __syncwarp();
+        }
       };
       if (nu == 0) {
         if (on && (!DIFF || map == 0)) {
@@ -647,14 +716,8 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           float o[32];
           tm_ld32(o, tm_o + d);
           tm_wait_ld();
-          if (on && s.part) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) store8(&part.o[tile * 128 + r][d + i], o + i);
-          } else if (on) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              if (d + i < c.D) write8(d + i, o + i, by);
-          }
+          if (s.part) emit_part(&part.o[tile * 128 + r - lane], d, o);
+          else emit(d, o, by);
         }
         if (on && s.part) {
           part.m[tile * 128 + r] = m;
@@ -685,13 +748,8 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               o[i] = o[i] * f0 - o1[i] * f1;
               if (d + i < c.D) q = fmaf(o[i], o[i], q);
             }
-            if (a.norm) {
-              tm_st32(lanes + C::kO + d, o);
-            } else if (on) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 8)
-                if (d + i < c.D) write8(d + i, o + i, 1.f);
-            }
+            if (a.norm) tm_st32(lanes + C::kO + d, o);
+            else emit(d, o, 1.f);
           }
           if (a.norm) {
             tm_wait_st();
@@ -705,10 +763,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               float o[32];
               tm_ld32(o, lanes + C::kO + d);
               tm_wait_ld();
-              if (on)
-#pragma unroll
-                for (int i = 0; i < 32; i += 8)
-                  if (d + i < c.D) write8(d + i, o + i, n);
+              emit(d, o, n);
             }
           }
           fence_before();
@@ -728,10 +783,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
                 o[i] = map ? y - x : x - y;
                 if (pass == 0 && d + i < c.D) q = fmaf(o[i], o[i], q);
               }
-              if (pass == 1 && on)
-#pragma unroll
-                for (int i = 0; i < 32; i += 8)
-                  if (d + i < c.D && (i >> 4) == map) write8(d + i, o + i, n);
+              if (pass == 1) emit(d, o, n);
             }
             if (pass == 0) n = q == 0.f ? 0.f : rsqrtf(q / c.D + a.eps);
           }
@@ -748,6 +800,8 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
     constexpr int kRpi = 32 / kCpr;                  // rows that a warp copies at once
     const int w = warp - kLoad0, ch = lane % kCpr, sub = lane / kCpr;
     uint32_t tiles = 0, blocks = 0;                  // K and V blocks so far; blocks
+    Ring<C::kSlots> ring;                            // of the next copy
+    Ring<(C::kRaws > 0 ? C::kRaws : 1)> rawr;        // and of its codes
     bool alive = true;
     constexpr int kLag = 2;  // copies under way whose arrival is not told yet (bf16)
 #pragma unroll 1
@@ -759,9 +813,9 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       // blocks before `most` or that end after `least` are masked for some rows
       int most = s.begin, least = s.len;
       if (nu > 0) {
-        const int jl = (min(p0 + C::kItem, p1) - 1) / group;
+        const int jl = a.by_group.of(p1 - 1);
         if (a.window) most = (int)max((int64_t)most, (int64_t)s.base + jl - a.window + 1);
-        if (!a.full) least = min(least, s.base + p0 / group + 1);
+        if (!a.full) least = min(least, s.base + a.by_group.of(p0) + 1);
       }
       arrive(sh.seg_empty[sidx & 1]);
       if (nu < 0) break;
@@ -780,7 +834,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         const bool in = t >= lo && t < hi;
         bk = bv = ~0ull;
         if (in) {
-          const int blk = t / c.Tb;
+          const int blk = a.by_page.of(t);
           const uint32_t pk = tab_k[blk], pv = tab_v[blk];
           if (pk < c.pages && pv < c.pages) {
             const uint32_t off = (uint32_t)(t - blk * c.Tb) * c.row_bytes;
@@ -796,20 +850,35 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       };
       // A block that all rows see, in whole boxes of existing pages, is copied by the TMA: lane i
       // has box i.  Other blocks are copied row by row (zeros where there is nothing).
-      uint32_t pk = 0, pv = 0;
-      int off = 0;
-      auto boxes = [&](int u) -> bool {
-        if (!box || masked(u) || first + u * kN < lo || first + (u + 1) * kN > hi) return false;
-        const int t = first + u * kN + lane * box;
-        bool ok = true;
-        if (lane * box < kN) {
-          const int blk = t / c.Tb;
-          off = t - blk * c.Tb;
-          pk = tab_k[blk];
-          pv = tab_v[blk];
-          ok = pk < c.pages && pv < c.pages;
+      // (The pages of the next such block are looked up meanwhile.)
+      uint32_t pk = 0, pv = 0, next_k = 0, next_v = 0;
+      int off = 0, at_blk = 0, at_off = 0, at_u = -1;
+      const bool has_box = lane * box < kN;
+      auto inside = [&](int u) {
+        return box && u < nu && !masked(u) && first + u * kN >= lo && first + (u + 1) * kN <= hi;
+      };
+      auto look = [&](int u) {  // calls come with u that grows
+        if (at_u < 0) {
+          const int t = first + u * kN + lane * box;
+          at_blk = a.by_page.of(t);
+          at_off = t - at_blk * c.Tb;
+        } else {
+          for (at_off += (u - at_u) * kN; at_off >= c.Tb; at_off -= c.Tb) ++at_blk;
         }
-        return __all_sync(~0u, ok);
+        at_u = u;
+        if (has_box) {
+          next_k = tab_k[at_blk];
+          next_v = tab_v[at_blk];
+        }
+      };
+      auto boxes = [&](int u) -> bool {
+        if (!inside(u)) return false;
+        if (at_u != u) look(u);
+        pk = next_k;
+        pv = next_v;
+        off = at_off;
+        if (inside(u + 1)) look(u + 1);
+        return __all_sync(~0u, !has_box || (pk < c.pages && pv < c.pages));
       };
       auto no_holes = [&](int u) {
         if (lane == 0) reinterpret_cast<uint32_t *>(&sh.holes[(blocks + u) % kHoles])[w] = 0;
@@ -823,15 +892,15 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
             int row = w * 32 + sub;
             const int step = DIFF && kTiles == 1 ? 0 : kRpi;
             int p = p0 + (!DIFF ? t * 128 + row : row);
-            int j = p / group, g = p - j * group;
-            const int dj = step / group, dg = step - dj * group;
+            int j = a.by_group.of(p), g = p - j * group;
+            const int dj = a.by_group.of(step), dg = step - dj * group;
 #pragma unroll 1
             for (int i = 0; i < 32 / kRpi; ++i, row += kRpi) {
               int of = t;
               if (DIFF && kTiles == 1) {
                 p = p0 + (row >> 5) * 16 + (row & 15);
                 of = (row >> 4) & 1;
-                j = p / group;
+                j = a.by_group.of(p);
                 g = p - j * group;
               }
               bool on = p < p1 && ch * 8 < c.D;
@@ -858,7 +927,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               rr = (row >> 5) * 16 + (row & 15);
               of = (row >> 4) & 1;
             }
-            const int p = p0 + rr, j = p / group, g = p - j * group;
+            const int p = p0 + rr, j = a.by_group.of(p), g = p - j * group;
             const uint16_t *src = a.q + ((int64_t)q0 + j) * a.qs + (int64_t)(h * group + g) * a.qhs;
             int from = 0, to = c.D / 8;
             if (DIFF) (of ? from : to) = c.D / 16;
@@ -923,9 +992,11 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           arrive(sh.kv_full[i % C::kSlots]);
         };
         const int copies = 2 * nu;
+        // the queries: at once when the item before has read its own, else after the first block
+        bool asked = __all_sync(~0u, bar_try(smem_addr(&sh.q_empty), (sidx & 1) ^ 1));
+        if (asked) queries();
 #pragma unroll 1
         for (int n = 0; n < copies; ++n) {
-          const uint32_t i = tiles + n;
           const int u = n / 2;
           const bool is_v = n & 1;
           if (!is_v) {
@@ -934,13 +1005,13 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
             if (bulk) no_holes(u);
             else find(u);
           }
-          if (!wait(sh.kv_empty[i % C::kSlots], ((i / C::kSlots) & 1) ^ 1)) {
+          if (!wait(sh.kv_empty[ring.at], ring.round ^ 1)) {
             alive = false;
             break;
           }
-          const uint32_t dst = sm + C::kOffSlots + i % C::kSlots * C::kSlot;
+          const uint32_t dst = sm + C::kOffSlots + ring.at * C::kSlot;
           if (bulk) {
-            const uint32_t bar = smem_addr(&sh.kv_full[i % C::kSlots]);
+            const uint32_t bar = smem_addr(&sh.kv_full[ring.at]);
             const int wide = (c.D + 63) / 64;
             if (w == 0) {
               if (lane == 0) bar_expect(bar, wide * kN * 128);
@@ -949,7 +1020,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
                 for (int x = 0; x < wide; ++x)
                   copy_box(dst + x * kN * 128 + lane * box * 128, &map, bar, x * 64, off, is_v ? pv : pk);
             } else {
-              arrive(sh.kv_full[i % C::kSlots]);
+              arrive(sh.kv_full[ring.at]);
             }
           } else {
             const uint64_t from = is_v ? bv : bk;
@@ -962,14 +1033,16 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
             }
           }
           cp_commit();
+          ring = ring.after();
           if (n == 1) {
-            // the queries, which wait for the end of the item before, after the first block
-            if (!wait(sh.q_empty, (sidx & 1) ^ 1)) {
-              alive = false;
-              break;
+            if (!asked) {
+              if (!wait(sh.q_empty, (sidx & 1) ^ 1)) {
+                alive = false;
+                break;
+              }
+              queries();
+              cp_commit();
             }
-            queries();
-            cp_commit();
             cp_wait<0>();
             fence_async();
             arrive(sh.q_full);
@@ -991,49 +1064,13 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           tell(copies - 1);
         }
       } else {
+        // codes, which the warp kFetch brings to the ring of raw blocks, become fp16
         constexpr int kCprRaw = DP / 16, kRpiRaw = 32 / kCprRaw;
         constexpr int kCopies = kRpw * kCprRaw / 32;  // chunks of 16 codes of a thread per block
         const int chr = lane % kCprRaw, subr = lane / kCprRaw;
-        const uint32_t raw = sm + C::kOffRaw + (w * kRpw + subr) * DP + chr * 16;
+        const uint32_t raw0 = sm + C::kOffRaw + (w * kRpw + subr) * DP + chr * 16;
         const int copies = 2 * nu;
-        bool bulk = false;
-        uint32_t bulks = 0;  // by copy, the last 32
-        auto fetch = [&](int n) -> bool {
-          bulks <<= 1;
-          if (n < copies) {
-            if (!(n & 1)) {
-              bulk = boxes(n / 2);
-              if (bulk) no_holes(n / 2);
-              else find(n / 2);
-            }
-            bulks |= bulk;
-            const uint32_t i = tiles + n, at = i % C::kRaws;
-            if (!wait(sh.raw_empty[at], ((i / C::kRaws) & 1) ^ 1)) return false;
-            if (bulk) {
-              const uint32_t bar = smem_addr(&sh.raw_full[at]);
-              if (w == 0) {
-                if (lane == 0) bar_expect(bar, C::kRaw);
-                __syncwarp();
-                if (lane * box < kN)
-                  copy_box(sm + C::kOffRaw + at * C::kRaw + lane * box * DP, &map, bar, 0, off, n & 1 ? pv : pk);
-              }
-            } else {
-              const uint64_t from = n & 1 ? bv : bk;
-#pragma unroll
-              for (int x = 0; x < kCopies; ++x) {
-                const uint64_t b = __shfl_sync(~0u, from, x * kRpiRaw + subr);
-                const bool on = b != ~0ull && chr * 16 < c.D;
-                cp_async16(raw + at * C::kRaw + x * 512, c.pool + (on ? b + chr * 16 : 0), on);
-              }
-              if (w == 0) arrive(sh.raw_full[at]);  // (its phases count copies)
-            }
-          }
-          cp_commit();
-          return true;
-        };
-#pragma unroll 1
-        for (int n = 0; n < C::kRaws - 1 && alive; ++n) alive = fetch(n);
-        if (!alive || !wait(sh.q_empty, (sidx & 1) ^ 1)) {
+        if (!wait(sh.q_empty, (sidx & 1) ^ 1)) {
           alive = false;
           break;
         }
@@ -1042,20 +1079,17 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         arrive(sh.q_full);
 #pragma unroll 1
         for (int n = 0; n < copies; ++n) {
-          const uint32_t i = tiles + n, at = i % C::kRaws;
-          if (!(alive = fetch(n + C::kRaws - 1))) break;
-          cp_wait<C::kRaws - 1>();
-          if (bulks >> (C::kRaws - 1) & 1) alive = wait(sh.raw_full[at], (i / C::kRaws) & 1);
-          if (!alive || !wait(sh.kv_empty[i % C::kSlots], ((i / C::kSlots) & 1) ^ 1)) {
+          if (!wait(sh.raw_full[rawr.at], rawr.round) || !wait(sh.kv_empty[ring.at], ring.round ^ 1)) {
             alive = false;
             break;
           }
-          const uint32_t dst = sm + C::kOffSlots + i % C::kSlots * C::kSlot;
+          const uint32_t raw = raw0 + rawr.at * C::kRaw;
+          const uint32_t dst = sm + C::kOffSlots + ring.at * C::kSlot;
           bool any = false;
           if ((n & 1) && masked(n / 2)) {
 #pragma unroll 1
             for (int x = 0; x < kCopies; ++x) {
-              uint4 v = lds128(raw + at * C::kRaw + x * 512);
+              uint4 v = lds128(raw + x * 512);
               uint32_t *e = &v.x, bad = 0;
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -1064,7 +1098,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
                 bad |= m;
               }
               if (bad) {
-                sts128(raw + at * C::kRaw + x * 512, v);
+                sts128(raw + x * 512, v);
                 any = true;
               }
             }
@@ -1074,7 +1108,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           for (int x0 = 0; x0 < kCopies; x0 += kOnce) {
             uint4 v[kOnce];
 #pragma unroll
-            for (int x = 0; x < kOnce; ++x) v[x] = lds128(raw + at * C::kRaw + (x0 + x) * 512);
+            for (int x = 0; x < kOnce; ++x) v[x] = lds128(raw + (x0 + x) * 512);
 #pragma unroll
             for (int x = 0; x < kOnce; ++x) {
               uint4 y0, y1;
@@ -1091,11 +1125,12 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
             }
           }
           if (any) s.fix = 1;
-          arrive(sh.raw_empty[at]);
+          arrive(sh.raw_empty[rawr.at]);
           fence_async();
-          arrive(sh.kv_full[i % C::kSlots]);
+          arrive(sh.kv_full[ring.at]);
+          ring = ring.after();
+          rawr = rawr.after();
         }
-        cp_wait<0>();
       }
       tiles += 2 * nu;
       blocks += nu;
@@ -1114,40 +1149,44 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       const uint32_t idesc_s = half | (uint32_t)(kN / 8) << 17;
       const uint32_t idesc_o = half | 1u << 16 | (dn / 8) << 17;
       const uint32_t tm = __shfl_sync(~0u, tmem, 0);
-      uint32_t tiles = 0, sbuf = 0, items = 0;
-      uint32_t np0 = 0, np1 = 0;  // P of each tile so far
+      uint32_t done0 = 0, done1 = 0, items = 0;  // blocks of each tile, items so far
+      Ring<C::kSlots> ring;                  // of the next copy, in the order K0, V0, K1, ...
       auto commit = [&](uint64_t &bar) {
         if (elect()) mma_commit(smem_addr(&bar));
       };
-      auto slot_wait = [&](uint32_t i) {
-        return wait(sh.kv_full[i % C::kSlots], (i / C::kSlots) & 1);
-      };
-      auto free_slot = [&](uint32_t i) { commit(sh.kv_empty[i % C::kSlots]); };
-      auto scores = [&](int t, int buf, uint32_t i) {  // S of tile t with the keys in copy i
-        const uint32_t q = desc_of(sm + t * C::kQ, 16);
-        const uint32_t k = desc_of(sm + C::kOffSlots + i % C::kSlots * C::kSlot, 16);
-        int from = 0, to = (c.D + 15) / 16;
-        if (DIFF && kTiles == 2) {
-          if (t == 0) to = (c.D / 2 + 15) / 16;
-          else from = c.D / 2 / 16;
-        }
+      const int steps = (c.D + 15) / 16;     // of 16 channels
+      const uint32_t q_desc = desc_of(sm, 16);
+      const uint32_t k_desc = desc_of(sm + C::kOffSlots, 16), v_desc = desc_of(sm + C::kOffSlots, kN * 128);
+      // S of tile t with the keys in slot `at`, which is free after the last tile
+      auto scores = [&](int t, int buf, uint32_t at, bool last) {
+        const uint32_t d = tm + buf * C::kS, q = q_desc + t * (C::kQ / 16), k = k_desc + at * (C::kSlot / 16);
         if (elect()) {
+          if (!DIFF && steps == DP / 16) {
 #pragma unroll
-          for (int x = 0; x < DP / 16; ++x)
-            if (x >= from && x < to)
-              mma_ss(tm + buf * C::kS, q + ((x >> 2) * (128 * 128) + (x & 3) * 32) / 16,
+            for (int x = 0; x < DP / 16; ++x)
+              mma_ss(d, q + ((x >> 2) * (128 * 128) + (x & 3) * 32) / 16,
+                     k + ((x >> 2) * (kN * 128) + (x & 3) * 32) / 16, idesc_s, x > 0);
+          } else {
+            // (the halves of a differential query have zeros in the other's channels)
+            const int from = DIFF && kTiles == 2 && t ? c.D / 2 / 16 : 0;
+            const int to = DIFF && kTiles == 2 && !t ? (c.D / 2 + 15) / 16 : steps;
+#pragma unroll 1
+            for (int x = from; x < to; ++x)
+              mma_ss(d, q + ((x >> 2) * (128 * 128) + (x & 3) * 32) / 16,
                      k + ((x >> 2) * (kN * 128) + (x & 3) * 32) / 16, idesc_s, x > from);
+          }
           mma_commit(smem_addr(&sh.s_full[buf]));
+          if (last) mma_commit(smem_addr(&sh.kv_empty[at]));
         }
         __syncwarp();
       };
-      auto sums = [&](int t, int buf, uint32_t i, bool add) {  // O of tile t += P V, V in copy i
-        const uint32_t v = desc_of(sm + C::kOffSlots + i % C::kSlots * C::kSlot, kN * 128);
+      auto sums = [&](int t, int buf, uint32_t at, bool add, bool last) {  // O += P V, V in slot `at`
+        const uint32_t d = tm + C::kO + t * DP, p = tm + buf * C::kS, v = v_desc + at * (C::kSlot / 16);
         if (elect()) {
 #pragma unroll
           for (int x = 0; x < kN / 16; ++x)
-            mma_ts(tm + C::kO + t * DP, tm + buf * C::kS + x * 8, v + x * 2048 / 16, idesc_o,
-                   add || x > 0);
+            mma_ts(d, p + x * 8, v + x * 2048 / 16, idesc_o, add || x > 0);
+          if (last) mma_commit(smem_addr(&sh.kv_empty[at]));
         }
         __syncwarp();
       };
@@ -1163,59 +1202,60 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           commit(sh.q_empty);  // its phases count segments
           continue;
         }
-        if (!wait(sh.q_full, items++ & 1) || !slot_wait(tiles)) break;
+        if (!wait(sh.q_full, items++ & 1)) break;
         fence_after();
         bool ok = true;
         if constexpr (kTiles == 2) {
           // tile by tile: the sums of block u, then the scores of block u + 1
+          const int both = two ? 2 : 1;
 #pragma unroll 1
           for (int u = -1; u < nu && ok; ++u) {
-            const uint32_t iv = tiles + 2 * u + 1, ik = iv + 1;
-            if (u >= 0 && !(ok = slot_wait(iv))) break;
+            const Ring<C::kSlots> rv = ring, rk = u < 0 ? ring : ring.after();
+            const bool more = u + 1 < nu;
+            const bool early = more && __all_sync(~0u, bar_try(smem_addr(&sh.kv_full[rk.at]), rk.round));
+            if (u >= 0 && !(ok = wait(sh.kv_full[rv.at], rv.round))) break;
 #pragma unroll 1
-            for (int t = 0; t < (two ? 2 : 1); ++t) {
+            for (int t = 0; t < both; ++t) {
+              const bool last = t == both - 1;
               if (u >= 0) {
-                if (!(ok = wait(sh.p_full[t], (t ? np1++ : np0++) & 1))) break;
+                if (!(ok = wait(sh.p_full[t], ((t ? done1 : done0) + u) & 1))) break;
                 fence_after();
-                sums(t, t, iv, u > 0);
+                sums(t, t, rv.at, u > 0, last);
+                if (!more) commit(sh.o_full[t]);
               }
-              if (u + 1 < nu) {
-                if (t == 0 && u >= 0 && !(ok = slot_wait(ik))) break;
-                scores(t, t, ik);
-              } else {
-                commit(sh.o_full[t]);
+              if (more) {
+                if (t == 0 && !early && !(ok = wait(sh.kv_full[rk.at], rk.round))) break;
+                scores(t, t, rk.at, last);
               }
             }
-            if (ok && u >= 0) free_slot(iv);
-            if (ok && u + 1 < nu) {
-              free_slot(ik);
-              if (u + 2 == nu) commit(sh.q_empty);
-            }
+            if (u + 2 == nu) commit(sh.q_empty);
+            ring = more ? rk.after() : rv.after();
           }
         } else {
+          // two buffers: the scores of block u + 1 first
 #pragma unroll 1
           for (int u = -1; u < nu && ok; ++u) {
-            const uint32_t iv = tiles + 2 * u + 1, ik = iv + 1;
-            if (u + 1 < nu) {
-              if (u >= 0 && !(ok = slot_wait(ik))) break;
-              scores(0, (sbuf + u + 1) & 1, ik);
-              free_slot(ik);
+            const Ring<C::kSlots> rv = ring, rk = u < 0 ? ring : ring.after();
+            const bool more = u + 1 < nu;
+            const uint32_t n = done0 + u;
+            if (more) {
+              if (!(ok = wait(sh.kv_full[rk.at], rk.round))) break;
+              scores(0, (n + 1) & 1, rk.at, true);
               if (u + 2 == nu) commit(sh.q_empty);
             }
             if (u >= 0) {
-              const uint32_t n = sbuf + u;
-              if (!(ok = slot_wait(iv) && wait(sh.p_full[n & 1], (n >> 1) & 1))) break;
+              if (!(ok = wait(sh.kv_full[rv.at], rv.round) && wait(sh.p_full[n & 1], (n >> 1) & 1))) break;
               fence_after();
-              sums(0, n & 1, iv, u > 0);
-              free_slot(iv);
+              sums(0, n & 1, rv.at, u > 0, true);
               commit(sh.o_full[0]);
-              if (u + 1 == nu) commit(sh.o_full[1]);
+              if (!more) commit(sh.o_full[1]);
             }
+            ring = more ? rk.after() : rv.after();
           }
-          sbuf += nu;
         }
+        done0 += nu;
+        if (two) done1 += nu;
         if (!ok) break;
-        tiles += 2 * nu;
       }
       // nothing of the matrix unit is in flight when the tensor memory is given back
       commit(sh.last);
@@ -1241,23 +1281,25 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
         return x;
       };
-      constexpr int kFew = 8;
+      constexpr int kFew = 4;
       uint64_t own = 0;
+      Entry e;             // of the lane's last sequence, its only one in batches of up to 32
+      uint32_t x = 0;      // and its cost, of one kv head
 #pragma unroll 1
       for (int k = 0; k < per; ++k) {
         const int b = b0 + k;
-        Entry e;
         e.items = 0;
         if (b < a.batch) e = entry_of<C>(a, group, b, blockIdx.x == 0);
+        x = 0;
         const bool big = e.items > kFew;
-        if (!big) own += one_cost(e) * c.heads;
+        if (!big) x = (uint32_t)one_cost(e);
 #pragma unroll 1
         for (uint32_t todo = __ballot_sync(~0u, big); todo; todo &= todo - 1) {
           const int who = __ffs(todo) - 1;
-          const Entry x = entry_of<C>(a, group, who * per + k, false);
-          const uint64_t y = warp_cost(x) * c.heads;
-          if (lane == who) own += y;
+          const uint32_t y = (uint32_t)warp_cost(from_lane(e, who));
+          if (lane == who) x = y;
         }
+        own += (uint64_t)x * c.heads;
       }
       uint64_t before = own;
 #pragma unroll
@@ -1292,15 +1334,19 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       if (pos < stop) {
         // the sequence b, the kv head h and the item i that unit `pos` lies in
         const int owner = __ffs(__ballot_sync(~0u, pos < before + own)) - 1;
-        uint64_t at = __shfl_sync(~0u, before, owner);
+        uint32_t at = (uint32_t)__shfl_sync(~0u, before, owner);
         int b = owner * per;
-        Entry e = entry_of<C>(a, group, b, false);
-        uint64_t x = warp_cost(e);
+        e = from_lane(e, owner);
+        x = __shfl_sync(~0u, x, owner);
+        if (per > 1) {
+          e = entry_of<C>(a, group, b, false);
+          x = (uint32_t)warp_cost(e);
 #pragma unroll 1
-        while (b + 1 < a.batch && pos >= at + x * c.heads) {
-          at += x * c.heads;
-          e = entry_of<C>(a, group, ++b, false);
-          x = warp_cost(e);
+          while (b + 1 < a.batch && pos >= at + x * c.heads) {
+            at += x * c.heads;
+            e = entry_of<C>(a, group, ++b, false);
+            x = (uint32_t)warp_cost(e);
+          }
         }
         const int h0 = x ? min((int)((pos - at) / x), c.heads - 1) : 0;
         at += x * h0;
@@ -1341,7 +1387,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
             }
             const Span sp = span_of<C>(a, group, e, i);
             const uint32_t cost = cost_of(sp);
-            const int c0 = (int)(pos - (uint32_t)at);
+            const int c0 = (int)(pos - at);
             const int c1 = (int)min(cost, (uint32_t)c0 + (stop - pos));
             const int u0 = cut ? max(c0 - kItemCost, 0) : 0;
             const int nu = cut ? c1 - kItemCost - u0 : sp.units;
@@ -1365,7 +1411,10 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
                 k.p0 = s.p0;
                 k.p1 = s.p1;
                 k.h = h;
-                k.parts = min(block_of(W, nblk, (uint32_t)at + cost - 1), (int)nblk - 1) - blockIdx.x + 1;
+                // the blocks that begin in the rest of the item: shares differ by one at most
+                const uint32_t rest = at + cost - stop;
+                k.parts = 1 + rest / (W / nblk + 1);
+                while (blockIdx.x + k.parts < nblk && deal(W, nblk, blockIdx.x + k.parts) < at + cost) ++k.parts;
                 cuts[blockIdx.x] = k;
               }
               ok = hand();
@@ -1382,6 +1431,97 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       s.nu = -1;
       if (lane == 0) hand();
       __syncwarp();
+    } else if (ES == 1 && warp == kFetch) {
+      // -------------------------------------------------------------- codes
+      // Blocks of codes to the ring of raw ones: in whole boxes of existing pages by the TMA, lane i
+      // has box i, else row by row with zeros where there is nothing.
+      constexpr int kCprRaw = DP / 16;
+      Ring<(C::kRaws > 0 ? C::kRaws : 1)> ring;
+      uint32_t blocks = 0;
+      bool alive = true;
+#pragma unroll 1
+      for (uint32_t sidx = 0; alive; ++sidx) {
+        Seg &s = sh.seg[sidx & 1];
+        if (!wait(sh.seg_full[sidx & 1], (sidx >> 1) & 1)) break;
+        const int nu = s.nu, lo = s.lo, hi = s.hi, first = s.t0;
+        const uint32_t *tab_k =
+            c.table + ((int64_t)s.slot * c.rows + ((int64_t)a.layer * 2) * c.heads + s.h) * c.blocks;
+        const uint32_t *tab_v = tab_k + (int64_t)c.heads * c.blocks;
+        arrive(sh.seg_empty[sidx & 1]);
+        if (nu < 0) break;
+        int blk = 0, off = 0;  // of this lane's box
+        const bool has_box = box && lane * box < kN;
+        if (has_box) {
+          blk = a.by_page.of(first + lane * box);
+          off = first + lane * box - blk * c.Tb;
+        }
+#pragma unroll 1
+        for (int u = 0; u < nu && alive; ++u) {
+          const int t0 = first + u * kN;
+          uint32_t pk = 0, pv = 0;
+          bool bulk = box && t0 >= lo && t0 + kN <= hi;
+          if (bulk && has_box) {
+            pk = tab_k[blk];
+            pv = tab_v[blk];
+          }
+          bulk = __all_sync(~0u, bulk && (!has_box || (pk < c.pages && pv < c.pages)));
+#pragma unroll 1
+          for (int side = 0; side < 2; ++side) {
+            if (!(alive = wait(sh.raw_empty[ring.at], ring.round ^ 1))) break;
+            const uint32_t bar = smem_addr(&sh.raw_full[ring.at]);
+            const uint32_t dst = sm + C::kOffRaw + ring.at * C::kRaw;
+            if (bulk) {
+              if (side == 0 && lane < 4) reinterpret_cast<uint32_t *>(&sh.holes[(blocks + u) % kHoles])[lane] = 0;
+              if (lane == 0) bar_expect(bar, C::kRaw);
+              else bar_arrive(bar);
+              __syncwarp();
+              if (has_box) copy_box(dst + lane * box * DP, &map, bar, 0, off, side ? pv : pk);
+            } else {
+#pragma unroll 1
+              for (int i = 0; i < kN / 32; ++i) {
+                const int t = t0 + i * 32 + lane;
+                const bool in = t >= lo && t < hi;
+                uint64_t from = ~0ull;
+                if (in) {
+                  const int b = a.by_page.of(t);
+                  const uint32_t qk = tab_k[b], qv = tab_v[b];
+                  if (qk < c.pages && qv < c.pages)
+                    from = (uint64_t)(side ? qv : qk) * c.page_bytes + (uint32_t)(t - b * c.Tb) * c.row_bytes;
+                }
+                const uint32_t gone = __ballot_sync(~0u, in && from == ~0ull);
+                if (side == 0 && lane == 0) {
+                  uint32_t *words = reinterpret_cast<uint32_t *>(&sh.holes[(blocks + u) % kHoles]);
+                  if (kN == 128) {
+                    words[i] = gone;
+                  } else {
+                    words[2 * i] = gone & 0xffffu;
+                    words[2 * i + 1] = gone >> 16;
+                  }
+                  if (gone) atomicOr(c.status, kCacheArg);
+                  __threadfence_block();
+                }
+#pragma unroll 4
+                for (int y = 0; y < kCprRaw; ++y) {
+                  const int row = (y * 32 + lane) / kCprRaw, ch = lane % kCprRaw;
+                  const uint64_t b = __shfl_sync(~0u, from, row);
+                  const bool on = b != ~0ull && ch * 16 < c.D;
+                  cp_async16(dst + (i * 32 + row) * DP + ch * 16, c.pool + (on ? b + ch * 16 : 0), on);
+                }
+              }
+              // this lane's arrival comes when its copies have
+              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+            }
+            ring = ring.after();
+          }
+          if (has_box)
+            for (off += kN; off >= c.Tb; off -= c.Tb) ++blk;
+        }
+        blocks += nu;
+      }
+      cp_wait<0>();
+      if (!alive)
+        for (const long long from = clock64(); clock64() - from < 2000000;) {
+        }
     }
   }
   fence_before();
@@ -1407,7 +1547,7 @@ __global__ void __launch_bounds__(kJoin * 32) k_chunk_join(ChunkArgs a) {
   if (parts <= 0 || p >= k.p1) return;
   const Part<C, DP> *part = reinterpret_cast<const Part<C, DP> *>(a.ws + kCutBytes) + blockIdx.x * 2;
   const int group = a.q_heads / c.heads;
-  const int j = p / group, head = k.h * group + (p - j * group);
+  const int j = a.by_group.of(p), head = k.h * group + (p - j * group);
   const int64_t oh = ((int64_t)k.q0 + j) * a.q_heads + head;
   float unit = 1.f;
   if (ES == 1 && c.scale) unit = c.scale[a.layer * c.heads + k.h];
@@ -1498,8 +1638,10 @@ int sm_count() {
 }
 
 template <int ES, int DP, bool DIFF>
-cudaError_t run(const ChunkArgs &a, cudaStream_t st) {
+cudaError_t run(ChunkArgs a, cudaStream_t st) {
   using C = Cfg<ES, DP, DIFF>;
+  a.by_group = Div(a.q_heads / a.c.heads);
+  a.by_page = Div(a.c.Tb);
   constexpr size_t smem = C::kOffMisc + sizeof(Misc<C>);
   static_assert(smem <= 227 * 1024, "shared memory of a block");
   const int sms = sm_count();
