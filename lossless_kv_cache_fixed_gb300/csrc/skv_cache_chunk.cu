@@ -93,7 +93,7 @@ template <typename C>
 struct Misc {
   uint64_t q_full, q_empty, kv_full[C::kSlots], kv_empty[C::kSlots];
   uint64_t raw_full[4], raw_empty[4];
-  uint64_t s_full[2], p_full[2], o_full[2], seg_full[2], seg_empty[2], pair, last;
+  uint64_t s_full[2], p_full[2], o_full[2], seg_full[2], seg_empty[2], turn[2], pair, last;
   uint32_t tmem, dead;
   Seg seg[2];
   uint4 holes[kHoles];
@@ -133,18 +133,26 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// a box of the pool: x (channel), y (token of the page), z (page)
+// a box of the pool (see map_pages): channel, token of the page, block of 64 channels, page
 __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y,
-                                         uint32_t z) {
+                                         int b, uint32_t z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
-      "[%2];" ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"((int)z)
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, "
+      "%6}], [%2];" ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(b), "r"((int)z)
       : "memory");
 }
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{.reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p;}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok;
+}
+// the same without waiting (try_wait may sleep for a microsecond)
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{.reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p;}"
       : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok;
 }
@@ -369,8 +377,10 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheView &c = a.c;
   const int group = a.q_heads / c.heads;
-  constexpr int kLoad0 = C::kSoftmax, kMma = C::kSoftmax + 4, kDeal = C::kSoftmax + 5,
-                kFetch = C::kSoftmax + 6;  // of codes
+  // the warps behind those of the softmax: loads, the matrix instructions of the tiles, the work,
+  // codes
+  constexpr int kLoad0 = C::kSoftmax, kMma = kLoad0 + 4, kDeal = kLoad0 + 5, kFetch = kLoad0 + 6,
+                kMma1 = kTiles == 2 ? kLoad0 + 7 : kMma;
 
   // Waits for a phase of a barrier, with a limit: then the block gives up and says so.
   auto wait1 = [&](uint64_t &bar, uint32_t parity) -> bool {
@@ -389,7 +399,8 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
     return false;
   };
   auto wait = [&](uint64_t &bar, uint32_t parity) -> bool {
-    return __all_sync(~0u, wait1(bar, parity));
+    const bool ok = wait1(bar, parity);
+    return __all_sync(~0u, ok);
   };
   auto arrive = [&](uint64_t &bar) {  // one arrival per warp
     __syncwarp();
@@ -403,24 +414,25 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
   }
   if (threadIdx.x == 0) {
     bar_init(smem_addr(&sh.q_full), 4);
-    bar_init(smem_addr(&sh.q_empty), 1);
+    bar_init(smem_addr(&sh.q_empty), kTiles);
     for (int i = 0; i < C::kSlots; ++i) {
       bar_init(smem_addr(&sh.kv_full[i]), 4);
-      bar_init(smem_addr(&sh.kv_empty[i]), 1);
+      bar_init(smem_addr(&sh.kv_empty[i]), kTiles);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(smem_addr(&sh.s_full[i]), 1);
       bar_init(smem_addr(&sh.p_full[i]), 4);
       bar_init(smem_addr(&sh.o_full[i]), 1);
       bar_init(smem_addr(&sh.seg_full[i]), 1);
-      bar_init(smem_addr(&sh.seg_empty[i]), C::kSoftmax + 5 + (ES == 1));
+      bar_init(smem_addr(&sh.turn[i]), 1);
+      bar_init(smem_addr(&sh.seg_empty[i]), C::kSoftmax + 4 + kTiles + (ES == 1));
     }
     for (int i = 0; i < C::kRaws; ++i) {
       bar_init(smem_addr(&sh.raw_full[i]), 32);
       bar_init(smem_addr(&sh.raw_empty[i]), 4);
     }
     bar_init(smem_addr(&sh.pair), 8);
-    bar_init(smem_addr(&sh.last), 1);
+    bar_init(smem_addr(&sh.last), kTiles);
     sh.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async();
@@ -993,7 +1005,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         };
         const int copies = 2 * nu;
         // the queries: at once when the item before has read its own, else after the first block
-        bool asked = __all_sync(~0u, bar_try(smem_addr(&sh.q_empty), (sidx & 1) ^ 1));
+        bool asked = __all_sync(~0u, bar_test(smem_addr(&sh.q_empty), (sidx & 1) ^ 1));
         if (asked) queries();
 #pragma unroll 1
         for (int n = 0; n < copies; ++n) {
@@ -1011,16 +1023,18 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           }
           const uint32_t dst = sm + C::kOffSlots + ring.at * C::kSlot;
           if (bulk) {
+            // every warp issues a quarter of the boxes; one arrival brings the bytes
             const uint32_t bar = smem_addr(&sh.kv_full[ring.at]);
-            const int wide = (c.D + 63) / 64;
-            if (w == 0) {
-              if (lane == 0) bar_expect(bar, wide * kN * 128);
-              __syncwarp();
-              if (lane * box < kN)
-                for (int x = 0; x < wide; ++x)
-                  copy_box(dst + x * kN * 128 + lane * box * 128, &map, bar, x * 64, off, is_v ? pv : pk);
-            } else {
-              arrive(sh.kv_full[ring.at]);
+            const int wide = (c.D + 63) / 64, per = c.D % 64 == 0 && box == kN ? wide : 1;
+            const bool blocked = c.D % 64 == 0;
+            if (has_box && (lane & 3) == w)
+              for (int x = 0; x < wide; x += per)
+                copy_box(dst + x * kN * 128 + lane * box * 128, &map, bar, blocked ? 0 : x * 64, off,
+                         blocked ? x : 0, is_v ? pv : pk);
+            __syncwarp();
+            if (lane == 0) {
+              if (w == 0) bar_expect(bar, wide * kN * 128);
+              else bar_arrive(bar);
             }
           } else {
             const uint64_t from = is_v ? bv : bk;
@@ -1142,14 +1156,18 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       }
   } else {
     regs_less<C::kRegsM>();
-    if (warp == kMma) {
+    if (warp == kMma || warp == kMma1) {
       // -------------------------------------------------------------- products
       const uint32_t half = 1u << 4 | (ES == 2 ? 1u << 7 | 1u << 10 : 0) | 8u << 24;
       const uint32_t dn = (c.D + 15) / 16 * 16;
       const uint32_t idesc_s = half | (uint32_t)(kN / 8) << 17;
       const uint32_t idesc_o = half | 1u << 16 | (dn / 8) << 17;
       const uint32_t tm = __shfl_sync(~0u, tmem, 0);
-      uint32_t done0 = 0, done1 = 0, items = 0;  // blocks of each tile, items so far
+      // Each tile has a warp of its own: one looks after its barriers while the other's
+      // instructions run.
+      const int t = kTiles == 2 && warp == kMma1 ? 1 : 0;
+      uint32_t done = 0, items = 0;          // blocks of this tile, items so far
+      uint32_t turns = 0;                    // turns of this tile at the matrix unit so far
       Ring<C::kSlots> ring;                  // of the next copy, in the order K0, V0, K1, ...
       auto commit = [&](uint64_t &bar) {
         if (elect()) mma_commit(smem_addr(&bar));
@@ -1157,16 +1175,19 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       const int steps = (c.D + 15) / 16;     // of 16 channels
       const uint32_t q_desc = desc_of(sm, 16);
       const uint32_t k_desc = desc_of(sm + C::kOffSlots, 16), v_desc = desc_of(sm + C::kOffSlots, kN * 128);
-      // S of tile t with the keys in slot `at`, which is free after the last tile
-      auto scores = [&](int t, int buf, uint32_t at, bool last) {
+      // S of the keys in slot `at`; the other tile may go when the last half is on its way
+      auto scores = [&](int buf, uint32_t at, bool pass) {
         const uint32_t d = tm + buf * C::kS, q = q_desc + t * (C::kQ / 16), k = k_desc + at * (C::kSlot / 16);
         if (elect()) {
           if (!DIFF && steps == DP / 16) {
 #pragma unroll
-            for (int x = 0; x < DP / 16; ++x)
+            for (int x = 0; x < DP / 16; ++x) {
+              if (x == DP / 32 && pass) bar_arrive(smem_addr(&sh.turn[t ^ 1]));
               mma_ss(d, q + ((x >> 2) * (128 * 128) + (x & 3) * 32) / 16,
                      k + ((x >> 2) * (kN * 128) + (x & 3) * 32) / 16, idesc_s, x > 0);
+            }
           } else {
+            if (pass) bar_arrive(smem_addr(&sh.turn[t ^ 1]));
             // (the halves of a differential query have zeros in the other's channels)
             const int from = DIFF && kTiles == 2 && t ? c.D / 2 / 16 : 0;
             const int to = DIFF && kTiles == 2 && !t ? (c.D / 2 + 15) / 16 : steps;
@@ -1176,17 +1197,17 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
                      k + ((x >> 2) * (kN * 128) + (x & 3) * 32) / 16, idesc_s, x > from);
           }
           mma_commit(smem_addr(&sh.s_full[buf]));
-          if (last) mma_commit(smem_addr(&sh.kv_empty[at]));
+          mma_commit(smem_addr(&sh.kv_empty[at]));
         }
         __syncwarp();
       };
-      auto sums = [&](int t, int buf, uint32_t at, bool add, bool last) {  // O += P V, V in slot `at`
+      auto sums = [&](int buf, uint32_t at, bool add) {  // O += P V, V in slot `at`
         const uint32_t d = tm + C::kO + t * DP, p = tm + buf * C::kS, v = v_desc + at * (C::kSlot / 16);
         if (elect()) {
 #pragma unroll
           for (int x = 0; x < kN / 16; ++x)
             mma_ts(d, p + x * 8, v + x * 2048 / 16, idesc_o, add || x > 0);
-          if (last) mma_commit(smem_addr(&sh.kv_empty[at]));
+          mma_commit(smem_addr(&sh.kv_empty[at]));
         }
         __syncwarp();
       };
@@ -1205,56 +1226,52 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         if (!wait(sh.q_full, items++ & 1)) break;
         fence_after();
         bool ok = true;
-        if constexpr (kTiles == 2) {
-          // tile by tile: the sums of block u, then the scores of block u + 1
-          const int both = two ? 2 : 1;
+        const bool mine = t == 0 || two;
 #pragma unroll 1
-          for (int u = -1; u < nu && ok; ++u) {
-            const Ring<C::kSlots> rv = ring, rk = u < 0 ? ring : ring.after();
-            const bool more = u + 1 < nu;
-            const bool early = more && __all_sync(~0u, bar_try(smem_addr(&sh.kv_full[rk.at]), rk.round));
-            if (u >= 0 && !(ok = wait(sh.kv_full[rv.at], rv.round))) break;
-#pragma unroll 1
-            for (int t = 0; t < both; ++t) {
-              const bool last = t == both - 1;
-              if (u >= 0) {
-                if (!(ok = wait(sh.p_full[t], ((t ? done1 : done0) + u) & 1))) break;
-                fence_after();
-                sums(t, t, rv.at, u > 0, last);
-                if (!more) commit(sh.o_full[t]);
-              }
-              if (more) {
-                if (t == 0 && !early && !(ok = wait(sh.kv_full[rk.at], rk.round))) break;
-                scores(t, t, rk.at, last);
-              }
-            }
-            if (u + 2 == nu) commit(sh.q_empty);
-            ring = more ? rk.after() : rv.after();
-          }
-        } else {
-          // two buffers: the scores of block u + 1 first
-#pragma unroll 1
-          for (int u = -1; u < nu && ok; ++u) {
-            const Ring<C::kSlots> rv = ring, rk = u < 0 ? ring : ring.after();
-            const bool more = u + 1 < nu;
-            const uint32_t n = done0 + u;
+        for (int u = -1; u < nu; ++u) {
+          const Ring<C::kSlots> rv = ring, rk = u < 0 ? ring : ring.after();
+          const bool more = u + 1 < nu;
+          const uint32_t n = done + u;
+          if (kTiles == 1) {
+            // two buffers: the scores of block u + 1, whose buffer is free, then the sums of block u
             if (more) {
               if (!(ok = wait(sh.kv_full[rk.at], rk.round))) break;
-              scores(0, (n + 1) & 1, rk.at, true);
+              scores((n + 1) & 1, rk.at, false);
               if (u + 2 == nu) commit(sh.q_empty);
             }
             if (u >= 0) {
               if (!(ok = wait(sh.kv_full[rv.at], rv.round) && wait(sh.p_full[n & 1], (n >> 1) & 1))) break;
               fence_after();
-              sums(0, n & 1, rv.at, u > 0, true);
+              sums(n & 1, rv.at, u > 0);
               commit(sh.o_full[0]);
               if (!more) commit(sh.o_full[1]);
             }
-            ring = more ? rk.after() : rv.after();
+          } else {
+            // The sums of block u, the scores of block u + 1.  The tiles take turns at the matrix
+            // unit: mixed, the instructions of both would take as long as both.
+            if (u >= 0 && !(ok = wait(sh.kv_full[rv.at], rv.round))) break;
+            if (two && more && !(ok = wait(sh.kv_full[rk.at], rk.round))) break;
+            if (mine) {
+              if (u >= 0 && !(ok = wait(sh.p_full[t], n & 1))) break;
+              if (two && !(ok = wait(sh.turn[t], (turns++ & 1) ^ (t == 0)))) break;
+              fence_after();
+              if (u >= 0) sums(t, rv.at, u > 0);
+            } else if (u >= 0) {
+              commit(sh.kv_empty[rv.at]);
+            }
+            if (more) {
+              if (!two && !(ok = wait(sh.kv_full[rk.at], rk.round))) break;
+              if (mine) scores(t, rk.at, two);
+              else commit(sh.kv_empty[rk.at]);
+              if (u + 2 == nu) commit(sh.q_empty);
+            } else {
+              if (two) arrive(sh.turn[t ^ 1]);
+              if (mine) commit(sh.o_full[t]);
+            }
           }
+          ring = more ? rk.after() : rv.after();
         }
-        done0 += nu;
-        if (two) done1 += nu;
+        if (mine) done += nu;
         if (!ok) break;
       }
       // nothing of the matrix unit is in flight when the tensor memory is given back
@@ -1475,7 +1492,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               if (lane == 0) bar_expect(bar, C::kRaw);
               else bar_arrive(bar);
               __syncwarp();
-              if (has_box) copy_box(dst + lane * box * DP, &map, bar, 0, off, side ? pv : pk);
+              if (has_box) copy_box(dst + lane * box * DP, &map, bar, 0, off, 0, side ? pv : pk);
             } else {
 #pragma unroll 1
               for (int i = 0; i < kN / 32; ++i) {
@@ -1597,12 +1614,14 @@ __global__ void __launch_bounds__(kJoin * 32) k_chunk_join(ChunkArgs a) {
   }
 }
 
-// Boxes of `rows` tokens of the pool's pages; false where the driver refuses them.
+// Boxes of `rows` tokens of the pool's pages; false where the driver refuses them.  bf16: the
+// channels in blocks of 64, one or all of them in a box; where they do not end with a block, and
+// for codes, one block, filled up with zeros.
 using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
                             CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                             CUtensorMapFloatOOBfill);
-bool map_pages(CUtensorMap *map, const CacheView &c, int channels, int rows) {
+bool map_pages(CUtensorMap *map, const CacheView &c, int channels, int rows, int most) {
   static std::atomic<void *> known{nullptr};
   void *fn = known.load(std::memory_order_relaxed);
   if (!fn) {
@@ -1616,11 +1635,14 @@ bool map_pages(CUtensorMap *map, const CacheView &c, int channels, int rows) {
     known.store(fn, std::memory_order_relaxed);
   }
   const bool codes = c.dtype == 1;
-  const cuuint64_t dims[3] = {(cuuint64_t)c.D, (cuuint64_t)c.Tb, c.pages};
-  const cuuint64_t strides[2] = {c.row_bytes, c.page_bytes};
-  const cuuint32_t sizes[3] = {(cuuint32_t)channels, (cuuint32_t)rows, 1}, steps[3] = {1, 1, 1};
+  const bool blocked = !codes && c.D % 64 == 0;
+  const cuuint32_t blocks = blocked ? c.D / 64 : 1;
+  const cuuint64_t dims[4] = {(cuuint64_t)(blocked ? 64 : c.D), (cuuint64_t)c.Tb, blocks, c.pages};
+  const cuuint64_t strides[3] = {c.row_bytes, blocked ? 128u : c.row_bytes, c.page_bytes};
+  const cuuint32_t sizes[4] = {(cuuint32_t)channels, (cuuint32_t)rows, rows == most ? blocks : 1, 1},
+                   steps[4] = {1, 1, 1, 1};
   return reinterpret_cast<Encode>(fn)(
-             map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c.pool, dims,
+             map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.pool, dims,
              strides, sizes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
              codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1667,7 +1689,7 @@ cudaError_t run(ChunkArgs a, cudaStream_t st) {
   CUtensorMap map = {};
   int box = a.c.Tb & -a.c.Tb;
   if (box > C::kN) box = C::kN;
-  if (box < 8 || a.c.pages > 0x7fffffff || !map_pages(&map, a.c, ES == 2 ? 64 : DP, box)) box = 0;
+  if (box < 8 || a.c.pages > 0x7fffffff || !map_pages(&map, a.c, ES == 2 ? 64 : DP, box, C::kN)) box = 0;
   e = launch(kern, dim3((unsigned)grid), C::kThreads, smem, st, a, cut, box, map);
   if (e != cudaSuccess || !cut) return e;
   return launch(k_chunk_join<ES, DP, DIFF>, dim3((unsigned)grid, C::kItem / kJoin), kJoin * 32, 0, st, a);
