@@ -61,8 +61,8 @@ struct Cfg {
   static constexpr int kThreads = (kSoftmax + 8) * 32;
   // registers per thread of the softmax, the loads and the others; their sum over the threads
   // is within what the block is launched with
-  static constexpr int kRegsS = kTiles == 2 ? 200 : 240, kRegsL = kTiles == 2 ? 64 : 120,
-                       kRegsM = kTiles == 2 ? 48 : 72;
+  static constexpr int kRegsS = kTiles == 2 ? 176 : 240, kRegsL = kTiles == 2 ? 80 : 120,
+                       kRegsM = kTiles == 2 ? 80 : 72;
   static constexpr int kRegs = 32 * (kSoftmax * kRegsS + 4 * kRegsL + 4 * kRegsM);
   static constexpr int kOffSlots = kTiles * kQ;
   static constexpr int kOffRaw = kOffSlots + kSlots * kSlot;
@@ -86,6 +86,7 @@ struct Seg {
   int32_t lo, hi, t0;         // tokens that the item sees; the first block's first token
   int32_t nu;                 // blocks; 0: the rows see nothing; -1: the end
   int32_t h, slot, part;      // part: 0 the whole item, 1 and 2: a part, of which slot + 1
+  int32_t twin;               // both tiles have the same rows and every second block
   uint32_t fix;               // values that are not finite were left out
 };
 
@@ -290,6 +291,12 @@ __device__ __forceinline__ uint32_t desc_of(uint32_t addr, uint32_t lbo) {
 template <int N>
 struct Ring {
   uint32_t at = 0, round = 0;
+  __device__ __forceinline__ Ring plus(uint32_t n) const {
+    Ring r;
+    r.at = (at + n) % N;
+    r.round = (round + (at + n) / N) & 1;
+    return r;
+  }
   __device__ __forceinline__ Ring after() const {
     Ring r;
     r.at = at + 1 == N ? 0 : at + 1;
@@ -448,8 +455,6 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
     // ---------------------------------------------------------------- softmax
     regs_more<C::kRegsS>();
     const int tile = warp >> 2, r = (warp & 3) * 32 + lane;
-    // packed row of the item, and the map, of this thread
-    const int rr = !DIFF ? tile * 128 + r : kTiles == 2 ? r : (r >> 5) * 16 + (r & 15);
     const int map = !DIFF ? 0 : kTiles == 2 ? tile : (r >> 4) & 1;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
     const uint32_t tm_o = lanes + C::kO + tile * DP;
@@ -466,6 +471,9 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       if (!wait(sh.seg_full[sidx & 1], (sidx >> 1) & 1)) break;
       const int nu = s.nu;
       if (nu < 0) break;
+      const bool twin = s.twin;
+      // packed row of the item of this thread
+      const int rr = twin ? r : !DIFF ? tile * 128 + r : kTiles == 2 ? r : (r >> 5) * 16 + (r & 15);
       const int p = s.p0 + rr;
       const bool on = p < s.p1;
       const int j = a.by_group.of(p), head = s.h * group + (p - j * group);
@@ -476,7 +484,8 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         if (a.window) lo = (int)max((int64_t)lo, (int64_t)place - a.window + 1);
         hi = place < 0 ? 0 : a.full ? s.len : min(s.len, place + 1);
       }
-      const bool rows = DIFF || s.p0 + tile * 128 < s.p1;  // the tile has some
+      const bool rows = DIFF || twin || s.p0 + tile * 128 < s.p1;  // the tile has some
+      const int u_from = twin ? tile : 0, u_step = twin ? 2 : 1;    // its blocks
       float m = -INFINITY;
       float l = 0.f;
       bool far = false, some_far = false;  // |m| > 2^20; of a row of the warp
@@ -485,19 +494,20 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       if (nu > 0 && rows) {
         float f = a.scale * kLog2e * unit;
         // blocks from wlo to whi are seen by all rows of the warp
-        const int wlo = __reduce_max_sync(~0u, lo), whi = __reduce_min_sync(~0u, hi), first = s.t0;
+        const int wlo = __reduce_max_sync(~0u, lo), whi = __reduce_min_sync(~0u, hi), end = s.t0 + nu * kN;
+        bool fresh = true;  // the first of the tile's blocks
 #pragma unroll 1
-        for (int u = 0; u < nu; ++u) {
+        for (int t0 = s.t0 + u_from * kN; t0 < end; t0 += u_step * kN) {
           const int buf = kTiles == 2 ? tile : (int)(mine & 1);
           const uint32_t phase = kTiles == 2 ? mine & 1 : (mine >> 1) & 1;
           if (!wait(sh.s_full[buf], phase)) break;
           fence_after();
-          if (ES == 1 && u == 0) f *= __uint_as_float((uint32_t)sh.qe[sidx & 1][tile][r] << 23);
+          if (ES == 1 && fresh) f *= __uint_as_float((uint32_t)sh.qe[sidx & 1][twin ? 0 : tile][r] << 23);
           const uint32_t tm_s = lanes + buf * C::kS;
           float x[2][32];
           tm_ld32(x[0], tm_s);
-          const int t0 = first + u * kN;
-          const uint4 hole = sh.holes[(blocks + u) % kHoles];
+          const uint4 &hole_of = sh.holes[(blocks + (t0 - s.t0) / kN) % kHoles];
+          const uint4 hole = hole_of;
           const bool holes = hole.x | hole.y | hole.z | hole.w;
           const bool edge = t0 < wlo || t0 + kN > whi || holes;
           float fx = f;  // x = fx * what is in S
@@ -513,7 +523,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               uint32_t out = 0;  // tokens that this row does not see
               if (edge) {
                 const int from = min(max(lo - t0 - i, 0), 32), to = min(max(hi - t0 - i, 0), 32);
-                const uint32_t *w = reinterpret_cast<const uint32_t *>(&sh.holes[(blocks + u) % kHoles]);
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(&hole_of);
                 out = kN == 128 ? w[i / 32] : (w[i / 16] & 0xffffu) | w[i / 16 + 1] << 16;
                 out |= ~(uint32_t)(((1ull << to) - 1) & ~((1ull << from) - 1));
               }
@@ -539,7 +549,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           // are written over it.
           bool ok = true;
 #pragma unroll 1
-          for (int again = u > 0 ? 0 : 1; again < 2; ++again) {
+          for (int again = fresh ? 1 : 0; again < 2; ++again) {
             if (again) {
               // only rows that pass it change, so that no row's bits depend on another's
               const bool grow = total > C::kFull || m == -INFINITY;
@@ -559,7 +569,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               far = fabsf(m) > 0x1p20f && m != -INFINITY;
               some_far = __any_sync(~0u, far);
               l *= by;
-              if (u > 0) {
+              if (!fresh) {
                 // With two buffers S may be there before the last product with the values is done
                 // (but not before the one before that, so the barrier is one phase ahead at most).
                 if (kTiles == 1 && !(ok = wait(sh.o_full[0], (mine - 1) & 1))) break;
@@ -604,6 +614,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           fence_before();
           arrive(sh.p_full[buf]);
           ++mine;
+          fresh = false;
         }
         blocks += nu;
         // ---- results
@@ -628,7 +639,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           tm_ld32(o, tm_o + d);
           tm_wait_ld();
 #pragma unroll 1
-          for (int u = 0; u < nu; ++u) {
+          for (int u = u_from; u < nu; u += u_step) {
             const int t0 = s.t0 + u * kN;
             if (!on || (t0 >= most && t0 + kN <= least)) continue;
 #pragma unroll 1
@@ -719,6 +730,49 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           if (a.lse)
             for (int i = 0; i < maps; ++i) a.lse[oh * maps + i] = -INFINITY;
         }
+      } else if (twin) {
+        // the sums of both tiles, each of the two threads of a row half of the channels
+        const uint32_t ml = sm + C::kOffStage + warp * 2048 + lane * 8;
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ml), "f"(m), "f"(L) : "memory");
+        fence_before();
+        if (!both()) break;
+        float om, ol;  // of the other
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(om), "=f"(ol) : "r"(ml ^ 8192) : "memory");
+        if (!both()) break;
+        fence_after();
+        const float M = fmaxf(m, om) == -INFINITY ? 0.f : fmaxf(m, om);
+        float by = ex2(m - M), oby = ex2(om - M);
+        const float all = tile ? ol * oby + L * by : L * by + ol * oby;
+        if (!s.part) {
+          const float scale = all == 0.f ? 0.f : unit / all;
+          by *= scale;
+          oby *= scale;
+        }
+        const float f0 = tile ? oby : by, f1 = tile ? by : oby;
+        Part<C, DP> &part =
+            reinterpret_cast<Part<C, DP> *>(a.ws + kCutBytes)[blockIdx.x * 2 + max(s.part - 1, 0)];
+#pragma unroll 1
+        for (int d = tile * (DP / 2); d < min(c.D, (tile + 1) * (DP / 2)); d += 32) {
+          float o[32], o1[32];
+          tm_ld32(o, lanes + C::kO + d);
+          tm_ld32(o1, lanes + C::kO + DP + d);
+          tm_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = o[i] * f0 + o1[i] * f1;
+          if (s.part) emit_part(&part.o[r - lane], d, o);
+          else emit(d, o, 1.f);
+        }
+        if (on && tile == 0) {
+          const float top = fmaxf(m, om);
+          if (s.part) {
+            part.m[r] = top;
+            part.l[r] = all;
+          } else if (a.lse) {
+            a.lse[oh] = (M + log2f(all)) * kLn2;
+          }
+        }
+        fence_before();
+        if (!both()) break;  // (neither tile's sums are overwritten before both are read)
       } else if (rows && (s.part || !DIFF)) {
         Part<C, DP> &part =
             reinterpret_cast<Part<C, DP> *>(a.ws + kCutBytes)[blockIdx.x * 2 + max(s.part - 1, 0)];
@@ -1176,8 +1230,8 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       const uint32_t q_desc = desc_of(sm, 16);
       const uint32_t k_desc = desc_of(sm + C::kOffSlots, 16), v_desc = desc_of(sm + C::kOffSlots, kN * 128);
       // S of the keys in slot `at`; the other tile may go when the last half is on its way
-      auto scores = [&](int buf, uint32_t at, bool pass) {
-        const uint32_t d = tm + buf * C::kS, q = q_desc + t * (C::kQ / 16), k = k_desc + at * (C::kSlot / 16);
+      auto scores = [&](int buf, uint32_t at, bool pass, bool alone = false) {
+        const uint32_t d = tm + buf * C::kS, q = q_desc + (alone ? 0 : t * (C::kQ / 16)), k = k_desc + at * (C::kSlot / 16);
         if (elect()) {
           if (!DIFF && steps == DP / 16) {
 #pragma unroll
@@ -1198,16 +1252,18 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           }
           mma_commit(smem_addr(&sh.s_full[buf]));
           mma_commit(smem_addr(&sh.kv_empty[at]));
+          if (alone) mma_commit(smem_addr(&sh.kv_empty[at]));  // for both tiles
         }
         __syncwarp();
       };
-      auto sums = [&](int buf, uint32_t at, bool add) {  // O += P V, V in slot `at`
+      auto sums = [&](int buf, uint32_t at, bool add, bool alone = false) {  // O += P V, V in slot `at`
         const uint32_t d = tm + C::kO + t * DP, p = tm + buf * C::kS, v = v_desc + at * (C::kSlot / 16);
         if (elect()) {
 #pragma unroll
           for (int x = 0; x < kN / 16; ++x)
             mma_ts(d, p + x * 8, v + x * 2048 / 16, idesc_o, add || x > 0);
           mma_commit(smem_addr(&sh.kv_empty[at]));
+          if (alone) mma_commit(smem_addr(&sh.kv_empty[at]));
         }
         __syncwarp();
       };
@@ -1216,6 +1272,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         Seg &s = sh.seg[sidx & 1];
         if (!wait(sh.seg_full[sidx & 1], (sidx >> 1) & 1)) break;
         const int nu = __shfl_sync(~0u, s.nu, 0);
+        const bool twin = kTiles == 2 && !DIFF && __shfl_sync(~0u, s.twin, 0);
         const bool two = kTiles == 2 && (DIFF || __shfl_sync(~0u, (int)(s.p0 + 128 < s.p1), 0));
         arrive(sh.seg_empty[sidx & 1]);
         if (nu < 0) break;
@@ -1226,6 +1283,29 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         if (!wait(sh.q_full, items++ & 1)) break;
         fence_after();
         bool ok = true;
+        if (twin) {
+          // every second block, with the first tile's queries; the other warp leaves its slots alone
+          Ring<C::kSlots> r = ring.plus(2 * t);
+          int u = t;
+#pragma unroll 1
+          for (; ok; u += 2) {
+            if (!(ok = wait(sh.kv_full[r.at], r.round))) break;
+            fence_after();
+            scores(t, r.at, false, true);
+            const bool more = u + 2 < nu;
+            if (!more) commit(sh.q_empty);
+            r = r.after();
+            if (!(ok = wait(sh.kv_full[r.at], r.round) && wait(sh.p_full[t], done++ & 1))) break;
+            fence_after();
+            sums(t, r.at, u > t, true);
+            if (!more) break;
+            r = r.plus(3);
+          }
+          if (!ok) break;
+          commit(sh.o_full[t]);
+          ring = ring.plus(2 * nu);
+          continue;
+        }
         const bool mine = t == 0 || two;
 #pragma unroll 1
         for (int u = -1; u < nu; ++u) {
@@ -1422,6 +1502,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               s.h = h;
               s.slot = e.slot;
               s.part = nu <= 0 || nu == sp.units ? 0 : u0 == 0 ? 2 : 1;
+              s.twin = kTiles == 2 && !DIFF && s.p1 - s.p0 <= 128 && nu > 1;
               if (s.part == 2) {
                 Cut k;
                 k.q0 = s.q0;
@@ -1548,69 +1629,101 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// Adds up the parts of the items that lie in several thread blocks, in their order: one warp
-// per packed row.  blockIdx.x: the thread block that an item begins in.
+// Adds up the parts of the items that lie in several thread blocks, in their order: a warp per
+// packed row and map, a lane has neighbouring channels.  blockIdx.x: the thread block that an
+// item begins in.  Short code: it runs once, and is fetched while it runs.
 constexpr int kJoin = 8;
 template <int ES, int DP, bool DIFF>
 __global__ void __launch_bounds__(kJoin * 32) k_chunk_join(ChunkArgs a) {
   using C = Cfg<ES, DP, DIFF>;
-  constexpr int kVec = DP / 32, kMaps = DIFF ? 2 : 1;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kVec = DP / 32;
+  __shared__ float s_o[DIFF ? kJoin / 2 : 1][DIFF ? DP : 1];
   const CacheView &c = a.c;
-  const Cut k = reinterpret_cast<const Cut *>(a.ws)[blockIdx.x];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rr = blockIdx.y * kJoin + warp, p = k.p0 + rr;
-  const int parts = min(k.parts, (int)gridDim.x - (int)blockIdx.x);
-  if (parts <= 0 || p >= k.p1) return;
-  const Part<C, DP> *part = reinterpret_cast<const Part<C, DP> *>(a.ws + kCutBytes) + blockIdx.x * 2;
-  const int group = a.q_heads / c.heads;
-  const int j = a.by_group.of(p), head = k.h * group + (p - j * group);
-  const int64_t oh = ((int64_t)k.q0 + j) * a.q_heads + head;
+  const int map = DIFF ? warp & 1 : 0, slot = DIFF ? warp >> 1 : warp;
+  constexpr int kRows = DIFF ? kJoin / 2 : kJoin;
   float unit = 1.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Cut k = reinterpret_cast<const Cut *>(a.ws)[blockIdx.x];
+  const int parts = min(k.parts, (int)gridDim.x - (int)blockIdx.x);
+  if (parts <= 0) return;
+  const Part<C, DP> *part = reinterpret_cast<const Part<C, DP> *>(a.ws + kCutBytes) + blockIdx.x * 2;
   if (ES == 1 && c.scale) unit = c.scale[a.layer * c.heads + k.h];
-  float res[kVec];
-#pragma unroll
-  for (int map = 0; map < kMaps; ++map) {
-    const int r = !DIFF ? rr : C::kTiles == 2 ? map * 128 + rr : (rr >> 4) * 32 + map * 16 + (rr & 15);
-    float M = -INFINITY;
-    for (int i = lane; i < parts; i += 32) M = fmaxf(M, part[2 * i + (i == 0)].m[r]);
-#pragma unroll
-    for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
-    const float m0 = M == -INFINITY ? 0.f : M;
-    float L = 0.f, o[kVec];
+#pragma unroll 1
+  for (int rr = blockIdx.y * kRows + slot; rr < C::kItem; rr += gridDim.y * kRows) {
+    const int p = k.p0 + rr;
+    const bool on = p < k.p1;
+    if (!DIFF && !on) break;
+    const int j = a.by_group.of(p), head = k.h * (a.q_heads / c.heads) + p - j * (a.q_heads / c.heads);
+    const int64_t oh = ((int64_t)k.q0 + j) * a.q_heads + head;
+    const int row = !DIFF ? rr : C::kTiles == 2 ? map * 128 + rr : (rr >> 4) * 32 + map * 16 + (rr & 15);
+    float M = -INFINITY, L = 0.f, o[kVec];
 #pragma unroll
     for (int v = 0; v < kVec; ++v) o[v] = 0.f;
+    if (on) {
+      // the parts' maxima: the first 32 a lane each
+      float m1 = -INFINITY, l1 = 0.f;
+      if (lane < parts) {
+        m1 = part[2 * lane + (lane == 0)].m[row];
+        l1 = part[2 * lane + (lane == 0)].l[row];
+      }
+      M = m1;
+#pragma unroll 1
+      for (int i = lane + 32; i < parts; i += 32) M = fmaxf(M, part[2 * i].m[row]);
+#pragma unroll 1
+      for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
+      const float m0 = M == -INFINITY ? 0.f : M;
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-      const Part<C, DP> &x = part[2 * i + (i == 0)];
-      const float w = ex2(x.m[r] - m0);
-      L += w * x.l[r];
+      for (int i = 0; i < parts; ++i) {
+        const Part<C, DP> &x = part[2 * i + (i == 0)];
+        const float w = ex2((i < 32 ? __shfl_sync(~0u, m1, i & 31) : x.m[row]) - m0);
+        L += w * (i < 32 ? __shfl_sync(~0u, l1, i & 31) : x.l[row]);
 #pragma unroll
-      for (int v = 0; v < kVec; ++v) o[v] += w * x.o[r][v * 32 + lane];
+        for (int v = 0; v < kVec; v += 2) {
+          const float2 y = *reinterpret_cast<const float2 *>(&x.o[row][lane * kVec + v]);
+          o[v] += w * y.x;
+          o[v + 1] += w * y.y;
+        }
+      }
+      if (lane == 0 && a.lse) a.lse[oh * (DIFF ? 2 : 1) + map] = (m0 + log2f(L)) * kLn2;
     }
     float by = L == 0.f ? 0.f : unit / L;
-    if (map) by *= a.lambda[head];
+    if (DIFF) {
+      // the second map's warp hands its result to the first's
+      if (on && map) by *= a.lambda[head];
+      if (map)
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) res[v] = map ? res[v] - o[v] * by : o[v] * by;
-    if (lane == 0 && a.lse) a.lse[oh * kMaps + map] = (m0 + log2f(L)) * kLn2;
-  }
-  float n = 1.f;
-  if (DIFF && a.norm) {
-    float q = 0.f;
+        for (int v = 0; v < kVec; ++v) s_o[slot][lane * kVec + v] = o[v] * by;
+      __syncthreads();
+      if (!map) {
+        float q = 0.f;
 #pragma unroll
-    for (int v = 0; v < kVec; ++v)
-      if (v * 32 + lane < c.D) q = fmaf(res[v], res[v], q);
-#pragma unroll
-    for (int s = 16; s; s >>= 1) q += __shfl_xor_sync(~0u, q, s);
-    n = q == 0.f ? 0.f : rsqrtf(q / c.D + a.eps);
-  }
-#pragma unroll
-  for (int v = 0; v < kVec; ++v) {
-    const int d = v * 32 + lane;
-    if (d < c.D) {
-      const __nv_bfloat16 y = __float2bfloat16_rn(res[v] * n * (DIFF && a.norm ? a.norm[d] : 1.f));
-      a.out[oh * c.D + d] = *reinterpret_cast<const uint16_t *>(&y);
+        for (int v = 0; v < kVec; ++v) {
+          o[v] = o[v] * by - s_o[slot][lane * kVec + v];
+          if (lane * kVec + v < c.D) q = fmaf(o[v], o[v], q);
+        }
+        by = 1.f;
+        if (a.norm) {
+#pragma unroll 1
+          for (int s = 16; s; s >>= 1) q += __shfl_xor_sync(~0u, q, s);
+          by = q == 0.f ? 0.f : rsqrtf(q / c.D + a.eps);
+        }
+      }
+      __syncthreads();
     }
+    if (on && !map)
+#pragma unroll
+      for (int v = 0; v < kVec; v += 2) {
+        const int d = lane * kVec + v;
+        if (d < c.D) {
+          float f0 = by, f1 = by;
+          if (DIFF && a.norm) {
+            f0 *= a.norm[d];
+            f1 *= a.norm[d + 1];
+          }
+          *reinterpret_cast<uint32_t *>(a.out + oh * c.D + d) = pack2<2>(o[v] * f0, o[v + 1] * f1);
+        }
+      }
   }
 }
 
@@ -1692,7 +1805,9 @@ cudaError_t run(ChunkArgs a, cudaStream_t st) {
   if (box < 8 || a.c.pages > 0x7fffffff || !map_pages(&map, a.c, ES == 2 ? 64 : DP, box, C::kN)) box = 0;
   e = launch(kern, dim3((unsigned)grid), C::kThreads, smem, st, a, cut, box, map);
   if (e != cudaSuccess || !cut) return e;
-  return launch(k_chunk_join<ES, DP, DIFF>, dim3((unsigned)grid, C::kItem / kJoin), kJoin * 32, 0, st, a);
+  constexpr int kRows = DIFF ? kJoin / 2 : kJoin;
+  return launch(k_chunk_join<ES, DP, DIFF>, dim3((unsigned)grid, (unsigned)(C::kItem / kRows)), kJoin * 32,
+                0, st, a);
 }
 
 template <int ES, bool DIFF>
