@@ -37,9 +37,6 @@ namespace skv {
 namespace {
 
 constexpr int kMostBlocks = 160;  // thread blocks of a launch
-// An item costs a thread block this many blocks of tokens more than it has: queries are
-// loaded, results written and the pipeline runs empty in between.
-constexpr int kItemCost = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kHoles = 16;       // blocks whose missing tokens are remembered
@@ -52,6 +49,11 @@ struct Cfg {
   static constexpr int kTiles = DP <= 128 ? 2 : 1;       // tiles of 128 rows
   static constexpr int kN = DP <= 128 ? 128 : 64;        // tokens of a block
   static constexpr int kItem = (DIFF ? 64 : 128) * kTiles;  // packed rows of an item
+  // An item costs a thread block this many blocks of tokens more than it has: queries are loaded,
+  // results written and the pipeline runs empty in between.  us with 2 / 4 / 8, bf16: a prompt of
+  // 4096 tokens 83.8 / 82.1 / 86.0, differential 159 / 137 / 147, windows with 256 channels 104.5 /
+  // 101.1 / 100.3 (6: 100.1); e4m3: ragged turns 200 / 187 / 182, differential 207 / 195 / 186.
+  static constexpr int kItemCost = ES == 1 ? 8 : DP == 256 ? 6 : 4;
   static constexpr int kQ = 128 * DP * 2;                // bytes of a tile of queries
   static constexpr int kSlot = kN * DP * 2;              // bytes of a block of keys or values
   static constexpr int kSlots = DP == 64 ? (ES == 2 ? 10 : 8) : (ES == 2 ? 4 : 3);
@@ -493,6 +495,8 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       if (ES == 1 && c.scale) unit = c.scale[a.layer * c.heads + s.h];
       if (nu > 0 && rows) {
         float f = a.scale * kLog2e * unit;
+        // (of all rows alike: with e4m3 a row's own f may be too small to have a sign)
+        const bool negative = f < 0.f;
         // blocks from wlo to whi are seen by all rows of the warp
         const int wlo = __reduce_max_sync(~0u, lo), whi = __reduce_min_sync(~0u, hi), end = s.t0 + nu * kN;
         bool fresh = true;  // the first of the tile's blocks
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           // The rare cases put x itself in S: masks, a negative f, and scores beyond 2^20, whose
           // differences from m are exact only when they are rounded before, as m was.
           auto settle = [&]() {
-            const bool mul = edge || f < 0.f || far;
+            const bool mul = edge || negative || far;
 #pragma unroll 1
             for (int i = 0; i < kN; i += 32) {
               float x[32];
@@ -537,7 +541,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
             tm_wait_st();
             fx = mul ? 1.f : f;
           };
-          bool settled = edge || f < 0.f || some_far;
+          const bool settled = edge || negative || some_far;
           if (settled) {
             settle();
             tm_ld32(x[0], tm_s);
@@ -604,7 +608,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               }
             }
             total = (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
-            if (again == 0 && !__any_sync(~0u, total > C::kFull || m == -INFINITY)) break;
+            if (again == 0 && !__any_sync(~0u, on && (total > C::kFull || m == -INFINITY))) break;
           }
           if (!ok) break;
 #pragma unroll
@@ -953,41 +957,30 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
 #pragma unroll 1
         for (int t = 0; t < kTiles; ++t) {
           const uint32_t dst = sm + t * C::kQ;
+          // rows behind the last are left as they are: nothing of them gets out of their lanes
+          const int rows = DIFF && kTiles == 1 ? 128 : min(p1 - p0 - (DIFF ? 0 : t * 128), 128);
           if (ES == 2) {
-            // packed row -> (token, head), step by step
-            int row = w * 32 + sub;
-            const int step = DIFF && kTiles == 1 ? 0 : kRpi;
-            int p = p0 + (!DIFF ? t * 128 + row : row);
-            int j = a.by_group.of(p), g = p - j * group;
-            const int dj = a.by_group.of(step), dg = step - dj * group;
 #pragma unroll 1
-            for (int i = 0; i < 32 / kRpi; ++i, row += kRpi) {
-              int of = t;
-              if (DIFF && kTiles == 1) {
-                p = p0 + (row >> 5) * 16 + (row & 15);
-                of = (row >> 4) & 1;
-                j = a.by_group.of(p);
-                g = p - j * group;
-              }
+            for (int row0 = w * kRpi; row0 < rows; row0 += 4 * kRpi) {
+              const int row = row0 + sub;
+              const int rr = !DIFF ? t * 128 + row : kTiles == 2 ? row : (row >> 5) * 16 + (row & 15);
+              const int p = p0 + rr, j = a.by_group.of(p), g = p - j * group;
               bool on = p < p1 && ch * 8 < c.D;
               if (DIFF) {
                 // halves end at a multiple of 8 channels
-                const int half = c.D / 2;
-                if (of == 0 ? ch * 8 >= half : ch * 8 < half) on = false;
+                const bool second = kTiles == 2 ? t : (row >> 4) & 1;
+                if (second ? ch * 8 < c.D / 2 : ch * 8 >= c.D / 2) on = false;
               }
               const uint16_t *src = a.q + ((int64_t)q0 + j) * a.qs + (int64_t)(h * group + g) * a.qhs + ch * 8;
               cp_async16(dst + swz(128, row, ch), on ? src : a.q, on);
-              p += step;
-              j += dj;
-              g += dg;
-              if (g >= group) {
-                g -= group;
-                ++j;
-              }
             }
           } else {
             // a thread per row: fp16 after a power of two, the largest channel in [1, 2)
             const int row = w * 32 + lane;
+            if (row >= rows) {
+              sh.qe[sidx & 1][t][row] = 127;
+              continue;
+            }
             int rr = !DIFF ? t * 128 + row : row, of = t;
             if (DIFF && kTiles == 1) {
               rr = (row >> 5) * 16 + (row & 15);
@@ -999,8 +992,8 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
             if (DIFF) (of ? from : to) = c.D / 16;
             if (p >= p1) to = from;
             float mx = 0.f;
-  #pragma unroll 1
-          for (int k = from; k < to; ++k) {
+#pragma unroll 1
+            for (int k = from; k < to; ++k) {
               const uint4 v = *reinterpret_cast<const uint4 *>(src + k * 8);
               const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -1363,7 +1356,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       // -------------------------------------------------------------- the work
       // Costs of all sequences; every lane owns `per` neighbouring ones.
       const int per = (a.batch + 31) / 32, b0 = lane * per;
-      auto cost_of = [&](const Span &sp) -> uint32_t { return cut ? sp.units + kItemCost : 1; };
+      auto cost_of = [&](const Span &sp) -> uint32_t { return cut ? sp.units + C::kItemCost : 1; };
       auto one_cost = [&](const Entry &e) -> uint64_t {  // of one kv head, this lane alone
         uint64_t x = 0;
 #pragma unroll 1
@@ -1399,12 +1392,12 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         own += (uint64_t)x * c.heads;
       }
       uint64_t before = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll 1
+      for (int o = 1; o < 32 && o < a.batch; o <<= 1) {
         const uint64_t y = __shfl_up_sync(~0u, before, o);
         if (lane >= o) before += y;
       }
-      const uint64_t all = __shfl_sync(~0u, before, 31);
+      const uint64_t all = __shfl_sync(~0u, before, min(a.batch, 32) - 1);
       before -= own;
       uint32_t sidx = 0;
       Seg s;
@@ -1421,7 +1414,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       const uint32_t W = (uint32_t)all;
       const bool good = all > 0 && all <= 0x7fffffffull;  // (starts that decrease may add up to more)
       if (all > 0x7fffffffull && lane == 0) atomicOr(c.status, kCacheArg);
-      const uint32_t nblk = good ? max(1u, min(cut ? W / 4 : W, gridDim.x)) : 1;
+      const uint32_t nblk = good ? max(1u, min(cut ? W / 2 : W, gridDim.x)) : 1;
       uint32_t pos = 0, stop = 0;
       if (good && blockIdx.x < nblk) {
         pos = deal(W, nblk, blockIdx.x);
@@ -1452,7 +1445,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         for (;;) {  // 32 items at a time
           const uint32_t mine = i + lane < e.items ? cost_of(span_of<C>(a, group, e, i + lane)) : 0;
           uint32_t y = mine;
-#pragma unroll
+#pragma unroll 1
           for (int o = 1; o < 32; o <<= 1) {
             const uint32_t z = __shfl_up_sync(~0u, y, o);
             if (lane >= o) y += z;
@@ -1486,8 +1479,8 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
             const uint32_t cost = cost_of(sp);
             const int c0 = (int)(pos - at);
             const int c1 = (int)min(cost, (uint32_t)c0 + (stop - pos));
-            const int u0 = cut ? max(c0 - kItemCost, 0) : 0;
-            const int nu = cut ? c1 - kItemCost - u0 : sp.units;
+            const int u0 = cut ? max(c0 - C::kItemCost, 0) : 0;
+            const int nu = cut ? c1 - C::kItemCost - u0 : sp.units;
             if (nu > 0 || (sp.units == 0 && c1 == (int)cost)) {
               s.q0 = e.q0;
               s.p0 = i * C::kItem;

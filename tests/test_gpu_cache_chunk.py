@@ -210,6 +210,17 @@ def test_large_and_growing_scores(dtype, d):
 
 
 @pytest.mark.parametrize("dtype", [0, 1], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 256])
+def test_rows_of_very_different_size_with_a_negative_scale(dtype, d):
+    """Rows whose scores have no sign left next to large ones, in one warp."""
+    c = filled(dtype, 1, 1, d, 16, 1, 700)
+    q = queries(20, 4, d).float()
+    q[::2] *= 2.0 ** -126
+    run(c, dtype, 0, [0], [700], [20], 4, q=q.bfloat16(), scale=-0.3)
+    run(c, dtype, 0, [0], [700], [20], 4, q=(q * 2.0 ** -10).bfloat16(), scale=-2.0 ** -20)
+
+
+@pytest.mark.parametrize("dtype", [0, 1], ids=["bf16", "e4m3"])
 def test_strides_in_place_padding_and_rows_of_no_sequence(dtype):
     c = filled(dtype, 1, 2, 64, 16, 2, 90)
     g = torch.Generator(device="cuda").manual_seed(4)
