@@ -501,7 +501,8 @@ int skv_cache_init(const skv_cache *cache, skv_stream_t stream);
 
 /* The status gathered by the calls on this cache since the last
  * skv_cache_status (or skv_cache_init), which it clears: SKV_OK, SKV_ERR_ARG,
- * SKV_ERR_CAPACITY (no free pages).  Synchronizes `stream`. */
+ * SKV_ERR_CAPACITY (no free pages), SKV_ERR_CUDA (a kernel gave up).  Synchronizes
+ * `stream`. */
 int skv_cache_status(const skv_cache *cache, skv_stream_t stream);
 
 /* Workspace bytes of skv_cache_reserve and skv_cache_fork with up to n
@@ -688,10 +689,15 @@ size_t skv_cache_attend_chunk_workspace_bytes(const skv_cache *cache, int32_t q_
  *   out          device bf16 [tokens][q_heads][head_dim], 16-byte aligned; may be q
  *                itself when q has that layout.
  *   lse          device fp32 [tokens][q_heads], or NULL.
- * head_dim up to 256.  Products and sums are fp32; results do not depend on what else
- * runs.  A slot, length or page out of range is reported (SKV_ERR_ARG); that
- * sequence's rows are empty, or that page's tokens are left out.  Starts that decrease or
- * leave 0 .. tokens are reported, and that sequence's rows left as they are. */
+ * head_dim up to 256.  Products and sums are fp32 (the matrix unit's); before they meet
+ * the values the weights round to bf16 (2^-8; bf16 caches) or to fp16 (2^-11, a weight
+ * below 2^-22 of the row's largest to 2^-33 of that one; e4m3 caches).  The result does not
+ * depend on what else runs, nor a row's on what other rows hold: items of rows are split
+ * and joined in a fixed order for given starts, lens, max_len and device.  A slot, length
+ * or page out of range is reported (SKV_ERR_ARG); that sequence's rows are empty, or that
+ * page's tokens are left out.  Starts that decrease or leave 0 .. tokens are reported, and
+ * that sequence's rows left as they are.  A kernel that waits for a part of itself in vain
+ * gives up after two seconds (SKV_ERR_CUDA in skv_cache_status). */
 int skv_cache_attend_chunk(const skv_cache *cache, int32_t layer, const skv_chunk *chunk,
                            const void *q, int64_t q_stride, int64_t q_head_stride,
                            int32_t q_heads, float softmax_scale, void *out, float *lse,
@@ -715,7 +721,8 @@ typedef struct {
 
 /* Differential attention of the new tokens of each sequence (starts NULL: one each) over
  * the pages of one layer; arguments, rows that see nothing and errors as
- * skv_cache_attend_chunk, but head_dim a multiple of 16 and
+ * skv_cache_attend_chunk (one token each: weights as skv_cache_attend), but head_dim a
+ * multiple of 16 and
  *   lse          device fp32 [tokens][q_heads][2], or NULL. */
 int skv_cache_attend_diff(const skv_cache *cache, int32_t layer, const skv_chunk *chunk,
                           const skv_diff *diff, const void *q, int64_t q_stride,

@@ -12,11 +12,24 @@
 //   S = Q K^T   tcgen05.mma, both operands in shared memory, S in tensor memory;
 //   P = 2^(S f - m), one thread per row, written over S as 16-bit numbers;
 //   O += P V    tcgen05.mma, P in tensor memory, V in shared memory, O in tensor memory.
-// The warps of a block have roles: 4 per tile for the softmax (one thread per row), 4 that
-// load (cp.async to a ring of slots; e4m3 codes become fp16 on the way), one that issues the
-// matrix instructions, one that deals the work.  With two tiles the matrix unit works on one
-// tile while the softmax of the other runs; with one (more than 128 channels, whose sums take
-// half of the tensor memory), S has two buffers.
+// The warps of a block have roles: 4 per tile for the softmax (one thread per row), 4 that load
+// (whole boxes of pages by the TMA, else rows by cp.async, to a ring of slots; e4m3 codes, which a
+// warp of their own brings, become fp16 on the way), one per tile that issues its matrix
+// instructions, one that deals the work.  With two tiles the matrix unit works on one tile while
+// the softmax of the other runs: they take turns, since mixed the instructions of both take as long
+// as both (2048 tokens on 8192, 64 heads of 128: 415 us against 367).  With one tile (more than 128
+// channels, whose sums take half of the tensor memory) S has two buffers.  Items of up to 128 rows
+// let both tiles work on every second block with the same rows (9 tokens on 131071, e4m3: 90 us
+// against 110).  bf16 weights round to bf16 (2^-8 of each): in two parts, as with one new token,
+// the second product would take twice as long, and it is a third to half of the work.
+//
+// What bounds it: a tile's chain of scores, weights and sums.  128 x 128 scores take a tile 1350
+// clocks (512 of them the rate of the exponentials), its two products 1024, and the barriers
+// between them 600; two tiles overlap to 3400 clocks a block where the products need 2048, 1340
+// TFLOP/s (68% of the library's product) on long caches.  Blocks of 64 tokens with two buffers of S
+// per tile took 574 us for those 358, 4 slots of keys and values instead of 5 with room for the
+// results the same.  A block of threads needs 10 us before its first scores (the code itself is
+// fetched) and the join 3 to 10 us.
 //
 // Work is dealt as in skv_cache_attend.cuh: the blocks of all items in a row, cut evenly over one
 // wave of persistent thread blocks whatever the lengths; items that lie in several leave partial
@@ -238,6 +251,8 @@ __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.
 template <int R>
 __device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
+// x f, and 0 where f is (sums of a row that sees nothing may be 0 times infinity)
+__device__ __forceinline__ float times(float x, float f) { return f == 0.f ? 0.f : x * f; }
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -687,7 +702,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           uint32_t w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float x0 = o[k * 8 + 2 * i] * by, x1 = o[k * 8 + 2 * i + 1] * by;
+            float x0 = times(o[k * 8 + 2 * i], by), x1 = times(o[k * 8 + 2 * i + 1], by);
             if (DIFF && a.norm && d + k * 8 < c.D) {
               x0 *= a.norm[d + k * 8 + 2 * i];
               x1 *= a.norm[d + k * 8 + 2 * i + 1];
@@ -762,7 +777,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           tm_ld32(o1, lanes + C::kO + DP + d);
           tm_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = o[i] * f0 + o1[i] * f1;
+          for (int i = 0; i < 32; ++i) o[i] = times(o[i], f0) + times(o1[i], f1);
           if (s.part) emit_part(&part.o[r - lane], d, o);
           else emit(d, o, 1.f);
         }
@@ -786,8 +801,14 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           float o[32];
           tm_ld32(o, tm_o + d);
           tm_wait_ld();
-          if (s.part) emit_part(&part.o[tile * 128 + r - lane], d, o);
-          else emit(d, o, by);
+          if (s.part) {
+            if (m == -INFINITY)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            emit_part(&part.o[tile * 128 + r - lane], d, o);
+          } else {
+            emit(d, o, by);
+          }
         }
         if (on && s.part) {
           part.m[tile * 128 + r] = m;
@@ -815,7 +836,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
             tm_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              o[i] = o[i] * f0 - o1[i] * f1;
+              o[i] = times(o[i], f0) - times(o1[i], f1);
               if (d + i < c.D) q = fmaf(o[i], o[i], q);
             }
             if (a.norm) tm_st32(lanes + C::kO + d, o);
@@ -849,7 +870,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               tm_wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                const float x = o[i] * by, y = __shfl_xor_sync(~0u, x, 16);
+                const float x = times(o[i], by), y = __shfl_xor_sync(~0u, x, 16);
                 o[i] = map ? y - x : x - y;
                 if (pass == 0 && d + i < c.D) q = fmaf(o[i], o[i], q);
               }

@@ -171,6 +171,26 @@ def test_infinite_values_that_some_rows_see(d):
     assert torch.equal(o2.nan_to_num(nan=0.0), want.nan_to_num(nan=0.0))
 
 
+@pytest.mark.parametrize("dtype", [0, 1], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("d,n", [(64, 40), (128, 3000), (256, 40), (256, 3000)])
+def test_rows_without_a_place_see_nothing(dtype, d, n):
+    """More new tokens than the sequence has, all of which see all of it, among whose values are
+    infinities and NaN; in one block of threads and in several."""
+    c = filled(dtype, 1, 1, d, 64, 1, n)
+    new = n + 5
+    q = queries(new, 2, d)
+    args = (0, ints([0]), ints([n]), ints([0, new]), q, n)
+    out, lse = c.attend_chunk(*args, causal=False, lse=True)
+    check(c, dtype, 0, [0], [n], [0, new], q, out, lse, causal=False)
+    for t in (3, n - 1):
+        c.pool[int(c.table[0, 0, 1, 0, t // 64]), t % 64, 7] = 0x7F80 if dtype == 0 else 0x7F
+    o2, l2 = c.attend_chunk(*args, causal=False, lse=True)
+    c.status()
+    assert torch.equal(lse, l2) and torch.all(o2[:5] == 0) and torch.all(l2[:5] == -math.inf)
+    rest = [i for i in range(d) if i != 7]
+    assert torch.equal(o2[:, :, rest], out[:, :, rest]) and not torch.any(torch.isfinite(o2[5:, :, 7]))
+
+
 def test_special_scores():
     c = filled(0, 1, 1, 64, 16, 1, 40)
     q = torch.ones(8, 1, 64, device="cuda").bfloat16()
