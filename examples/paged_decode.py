@@ -6,7 +6,7 @@ decoded straight into the pages of a serving cache.  The sequence is forked into
 continuations that share the prompt's full pages, every continuation appends new
 tokens (rotary positions, keys and values written to their pages) and attends to
 its cache; then all but one are dropped, the pool is compacted and the last one goes
-on.  Every step is checked against plain torch.
+on, at last with several tokens at once.  Every step is checked against plain torch.
 
     python examples/paged_decode.py [--e4m3] [--tokens 700] [--steps 3] [--branches 3]
 """
@@ -66,14 +66,40 @@ def values(cache, slot, layer, side, head, n):
     return x if cache.scale is None else x * cache.scale[layer, head].double()
 
 
-def check_attention(cache, layer, slots, lens, q, out):
+def check_attention(cache, layer, slots, lens, q, out, most=2.0 ** -7):
     group = q.shape[1] // cache.heads
     for b, (slot, n) in enumerate(zip(slots, lens)):
         for h in range(q.shape[1]):
             k, v = (values(cache, slot, layer, s, h // group, n) for s in (0, 1))
             w = torch.softmax(k @ q[b, h].double() / math.sqrt(cache.head_dim), 0)
             off = (out[b, h].double() - w @ v).abs() / (w @ v.abs())
-            assert float(off.max()) < 2.0 ** -7, float(off.max())
+            assert float(off.max()) < most, float(off.max())
+
+
+def drafted(cache, rope, slot, length, m, group, g):
+    """m new tokens of one sequence in one call per layer; each sees those before it."""
+    h, d = cache.heads, cache.head_dim
+    s, old, new = i32([slot]), i32([length]), i32([length + m])
+    cache.reserve(s, old, new)
+    at = torch.arange(length, length + m, dtype=torch.int32, device="cuda")
+    lam = torch.rand(h * group, generator=g, device="cuda")
+    for layer in range(cache.layers):
+        qkv = torch.randn(m, h * (group + 2), d, generator=g, device="cuda").bfloat16()
+        q, k, v = qkv.split([h * group, h, h], 1)
+        q = cache.append(layer, s.expand(m).contiguous(), at, q, k, v, rope,
+                         at.expand(3, m).contiguous())
+        args = dict(starts=i32([0, m]), max_len=length + m)
+        out = cache.attend_chunk(layer, s, new, q=q, **args)
+        check_attention(cache, layer, [slot] * m, range(length + 1, length + m + 1), q, out, 2.0 ** -6)
+        out = cache.attend_diff(layer, s, new, q, lam, **args)
+        for i in range(m):
+            for j in range(h * group):
+                kk, vv = (values(cache, slot, layer, side, j // group, length + i + 1) for side in (0, 1))
+                w = [torch.softmax(kk[:, c] @ q[i, j, c].double() / math.sqrt(d / 2), 0)
+                     for c in (slice(0, d // 2), slice(d // 2, d))]
+                off = out[i, j].double() - (w[0] - lam[j].double() * w[1]) @ vv
+                assert float((off.abs() / ((w[0] + w[1]) @ vv.abs())).max()) < 2.0 ** -6
+    cache.status()
 
 
 def main(argv=None):
@@ -82,6 +108,7 @@ def main(argv=None):
     ap.add_argument("--tokens", type=int, default=700)
     ap.add_argument("--steps", type=int, default=3)
     ap.add_argument("--branches", type=int, default=3)
+    ap.add_argument("--drafted", type=int, default=4)
     a = ap.parse_args(argv)
     base = synth.WORKLOADS["qwen3-0.6b-e4m3" if a.e4m3 else "qwen3-0.6b-bf16"]
     spec = base.scaled(name="paged-decode", L=2, H=2, T=a.tokens, calib_draws=min(2, base.calib_draws))
@@ -90,7 +117,7 @@ def main(argv=None):
 
     # a cache with room for the prompt and its branches; slot 0 takes the prompt
     rows = spec.L * 2 * spec.H
-    blocks = -(-(n + a.steps + 1) // spec.Tb)
+    blocks = -(-(n + a.steps + 1 + a.drafted) // spec.Tb)
     cache = P.PagedCache(spec.dtype, spec.L, spec.H, spec.D, spec.Tb,
                          num_pages=rows * (blocks + 2 * a.branches) + 5, max_seqs=1 + a.branches,
                          max_blocks=blocks,
@@ -149,6 +176,11 @@ def main(argv=None):
     assert int((cache.refs > 0).nonzero().max()) + 1 == after
     step(branches[-1:], n + a.steps)
     print("compacted from %d to %d pages, and one more step" % (before, after))
+
+    # several tokens at once, plain and differential attention
+    at = n + a.steps + 1
+    drafted(cache, rope, branches[-1], at, a.drafted, group, g)
+    print("%d drafted tokens at once" % a.drafted)
 
 
 if __name__ == "__main__":
