@@ -1207,8 +1207,10 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
             }
           }
           if (any) s.fix = 1;
-          arrive(sh.raw_empty[rawr.at]);
+          // (also before raw_empty: the next bulk copy to this place comes after what was written
+          // to it above, and by the rows that kFetch copied)
           fence_async();
+          arrive(sh.raw_empty[rawr.at]);
           arrive(sh.kv_full[ring.at]);
           ring = ring.after();
           rawr = rawr.after();
