@@ -939,9 +939,10 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           if (gone) atomicOr(c.status, kCacheArg);
         }
       };
-      // A block that all rows see, in whole boxes of existing pages, is copied by the TMA: lane i
-      // has box i.  Other blocks are copied row by row (zeros where there is nothing).
-      // (The pages of the next such block are looked up meanwhile.)
+      // A block that all rows see is copied by the TMA in whole boxes: lane i has box i.  Other
+      // blocks are copied row by row (zeros where there is nothing).  Nothing that is in memory decides
+      // which: the four warps bring a block's bytes together, also when its table entries change
+      // between their look-ups.  (The pages of the next such block are looked up meanwhile.)
       uint32_t pk = 0, pv = 0, next_k = 0, next_v = 0;
       int off = 0, at_blk = 0, at_off = 0, at_u = -1;
       const bool has_box = lane * box < kN;
@@ -962,17 +963,22 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           next_v = tab_v[at_blk];
         }
       };
-      auto boxes = [&](int u) -> bool {
-        if (!inside(u)) return false;
+      auto boxes = [&](int u) {
         if (at_u != u) look(u);
         pk = next_k;
         pv = next_v;
         off = at_off;
         if (inside(u + 1)) look(u + 1);
-        return __all_sync(~0u, !has_box || (pk < c.pages && pv < c.pages));
-      };
-      auto no_holes = [&](int u) {
-        if (lane == 0) reinterpret_cast<uint32_t *>(&sh.holes[(blocks + u) % kHoles])[w] = 0;
+        // a box without a page: behind the pool's last one the TMA finds zeros
+        const bool none = has_box && !(pk < c.pages && pv < c.pages);
+        if (none) pk = pv = (uint32_t)c.pages;
+        const uint32_t lost = __ballot_sync(~0u, none);
+        uint32_t gone = 0;  // tokens of this warp's part of the block
+        if (lost) gone = __ballot_sync(~0u, lane < kRpw && (lost >> (w * kRpw + lane % kRpw) / box & 1));
+        if (lane == 0) {
+          reinterpret_cast<uint32_t *>(&sh.holes[(blocks + u) % kHoles])[w] = gone;
+          if (gone) atomicOr(c.status, kCacheArg);
+        }
       };
       auto queries = [&]() {
 #pragma unroll 1
@@ -1081,8 +1087,8 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           const bool is_v = n & 1;
           if (!is_v) {
             bulk_before = n == 0 || bulk;
-            bulk = boxes(u);
-            if (bulk) no_holes(u);
+            bulk = inside(u);
+            if (bulk) boxes(u);
             else find(u);
           }
           if (!wait(sh.kv_empty[ring.at], ring.round ^ 1)) {
