@@ -751,12 +751,12 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         }
       } else if (twin) {
         // the sums of both tiles, each of the two threads of a row half of the channels
-        const uint32_t ml = sm + C::kOffStage + warp * 2048 + lane * 8;
-        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ml), "f"(m), "f"(L) : "memory");
+        auto ml_of = [&](int warp) { return sm + C::kOffStage + warp * 2048 + lane * 8; };
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ml_of(warp)), "f"(m), "f"(L) : "memory");
         fence_before();
         if (!both()) break;
         float om, ol;  // of the other
-        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(om), "=f"(ol) : "r"(ml ^ 8192) : "memory");
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(om), "=f"(ol) : "r"(ml_of(warp ^ 4)) : "memory");
         if (!both()) break;
         fence_after();
         const float M = fmaxf(m, om) == -INFINITY ? 0.f : fmaxf(m, om);
