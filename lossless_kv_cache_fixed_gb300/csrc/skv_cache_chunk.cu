@@ -251,8 +251,6 @@ __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.
 template <int R>
 __device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-// x f, and 0 where f is (sums of a row that sees nothing may be 0 times infinity)
-__device__ __forceinline__ float times(float x, float f) { return f == 0.f ? 0.f : x * f; }
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -683,6 +681,21 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         }
         tm_wait_st();
       }
+      if (nu > 0 && rows && __any_sync(~0u, l == 0.f)) {
+        // Sums of rows that see nothing may be 0 times infinity.  They become 0 here, so that below a
+        // factor of 0 (a tile's weight next to the other's, lambda, the norm of an infinite row) is a
+        // number like others, whose product with an infinity is NaN.
+#pragma unroll 1
+        for (int d = 0; d < DP; d += 32) {
+          float o[32];
+          tm_ld32(o, tm_o + d);
+          tm_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i];
+          tm_st32(tm_o + d, o);
+        }
+        tm_wait_st();
+      }
       // Results leave through shared memory, so that 4 lanes write 64 bytes of one row: a lane's
       // own row in 16-byte pieces would be 32 rows per store (10000 clocks a tile, 2000 so).
       const bool emits = on && !(DIFF && kTiles == 1 && lane >= 16);
@@ -702,7 +715,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           uint32_t w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float x0 = times(o[k * 8 + 2 * i], by), x1 = times(o[k * 8 + 2 * i + 1], by);
+            float x0 = o[k * 8 + 2 * i] * by, x1 = o[k * 8 + 2 * i + 1] * by;
             if (DIFF && a.norm && d + k * 8 < c.D) {
               x0 *= a.norm[d + k * 8 + 2 * i];
               x1 *= a.norm[d + k * 8 + 2 * i + 1];
@@ -777,7 +790,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           tm_ld32(o1, lanes + C::kO + DP + d);
           tm_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = times(o[i], f0) + times(o1[i], f1);
+          for (int i = 0; i < 32; ++i) o[i] = __fadd_rn(__fmul_rn(o[i], f0), __fmul_rn(o1[i], f1));
           if (s.part) emit_part(&part.o[r - lane], d, o);
           else emit(d, o, 1.f);
         }
@@ -801,14 +814,8 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           float o[32];
           tm_ld32(o, tm_o + d);
           tm_wait_ld();
-          if (s.part) {
-            if (m == -INFINITY)
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = 0.f;
-            emit_part(&part.o[tile * 128 + r - lane], d, o);
-          } else {
-            emit(d, o, by);
-          }
+          if (s.part) emit_part(&part.o[tile * 128 + r - lane], d, o);
+          else emit(d, o, by);
         }
         if (on && s.part) {
           part.m[tile * 128 + r] = m;
@@ -819,7 +826,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       } else if (DIFF) {
         if (on && a.lse) a.lse[oh * 2 + map] = (m0 + log2f(L)) * kLn2;
         float by = L == 0.f ? 0.f : unit / L;
-        if (map && on) by *= a.lambda[head];
+        if (map && on && L != 0.f) by *= a.lambda[head];
         float n = 1.f, q = 0.f;
         if constexpr (kTiles == 2) {
           // each of the two threads of a row takes half of the channels of both maps
@@ -836,7 +843,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
             tm_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              o[i] = times(o[i], f0) - times(o1[i], f1);
+              o[i] = __fsub_rn(__fmul_rn(o[i], f0), __fmul_rn(o1[i], f1));
               if (d + i < c.D) q = fmaf(o[i], o[i], q);
             }
             if (a.norm) tm_st32(lanes + C::kO + d, o);
@@ -870,7 +877,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               tm_wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                const float x = times(o[i], by), y = __shfl_xor_sync(~0u, x, 16);
+                const float x = __fmul_rn(o[i], by), y = __shfl_xor_sync(~0u, x, 16);
                 o[i] = map ? y - x : x - y;
                 if (pass == 0 && d + i < c.D) q = fmaf(o[i], o[i], q);
               }
@@ -1712,7 +1719,7 @@ __global__ void __launch_bounds__(kJoin * 32) k_chunk_join(ChunkArgs a) {
     float by = L == 0.f ? 0.f : unit / L;
     if (DIFF) {
       // the second map's warp hands its result to the first's
-      if (on && map) by *= a.lambda[head];
+      if (on && map && L != 0.f) by *= a.lambda[head];
       if (map)
 #pragma unroll
         for (int v = 0; v < kVec; ++v) s_o[slot][lane * kVec + v] = o[v] * by;

@@ -1,0 +1,82 @@
+"""Infinities, NaN and scores beyond the ordinary that rows do see, in chunk and differential
+attention.  What exact arithmetic gives is asked for, whatever route the row takes: in one block
+of threads or several, in one tile or two, one token or a chunk."""
+import math
+
+import pytest
+import torch
+
+from cache_helpers import ints
+from chunk_helpers import one_map, rows_of, seen
+from test_gpu_cache_attend import filled
+from test_gpu_cache_chunk import queries
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def place(c, side, t, head=0):
+    """A token's row of the pool, layer 0 of sequence 0."""
+    tb = c.page_tokens
+    pool = c.pool.view(torch.bfloat16) if c.pool.dtype == torch.int16 else c.pool
+    return pool[int(c.table[0, 0, side, head, t // tb]), t % tb]
+
+
+FORMS = [(300, None), (9000, None), (150, 60), (300, 40), (300, 150), (9000, 40), (2500, 300)]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,new", FORMS)
+def test_an_infinite_value_with_a_norm(d, n, new):
+    """Heads with lambda above, below and at 0.  The difference is NaN, infinite and NaN in the value's
+    channel; with a norm the root of the mean square is infinite or NaN with it."""
+    c = filled(0, 1, 1, d, 64, 1, n)
+    rows = new or 1
+    q = queries(rows, 3, d)
+    lam = torch.tensor([0.5, -0.5, 0.0], device="cuda")
+    norm = torch.rand(d, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda") + 0.2
+    args = (0, ints([0]), ints([n]), q, lam, n)
+    starts = None if new is None else ints([0, new])
+    plain, lse = c.attend_diff(*args, starts=starts, lse=True)
+    normed = c.attend_diff(*args, starts=starts, norm=norm)
+    t = n - rows // 2 - 1
+    place(c, 1, t)[5] = math.inf
+    first = t - (n - rows)                         # rows from here on see it
+    rest = [i for i in range(d) if i != 5]
+    o, l = c.attend_diff(*args, starts=starts, lse=True)
+    assert torch.equal(l, lse) and torch.equal(o[:first], plain[:first])
+    assert torch.equal(o[first:][:, :, rest], plain[first:][:, :, rest])
+    assert torch.all(torch.isnan(o[first:, 0, 5])) and torch.all(torch.isnan(o[first:, 2, 5]))
+    assert torch.all(o[first:, 1, 5] == math.inf)
+    o = c.attend_diff(*args, starts=starts, norm=norm)
+    assert torch.equal(o[:first], normed[:first])
+    assert torch.all(torch.isnan(o[first:, 0])) and torch.all(torch.isnan(o[first:, 2]))
+    assert torch.all(torch.isnan(o[first:, 1, 5])) and torch.all(o[first:, 1][:, rest] == 0)
+    c.status()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,new", [(300, 5), (3000, 5), (20000, 60), (3000, 100)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_values_of_tokens_whose_weight_is_next_to_nothing(d, n, new, bad):
+    """Scores of the odd blocks lie 150 below those of the even ones; an infinity or NaN among the
+    values of the former is not lost, other channels keep their bits."""
+    c = filled(0, 1, 1, d, 64, 1, n)
+    for t in range(n):
+        place(c, 0, t).zero_()
+        place(c, 0, t)[0] = 0.0 if t // 128 % 2 else 150.0
+    q = torch.zeros(new, 2, d, device="cuda").bfloat16()
+    q[:, :, 0] = 1.0
+    args = (0, ints([0]), ints([n]), ints([0, new]), q, n)
+    out, lse = c.attend_chunk(*args, scale=1.0, lse=True)
+    place(c, 1, 131)[7] = bad
+    o, l = c.attend_chunk(*args, scale=1.0, lse=True)
+    rest = [i for i in range(d) if i != 7]
+    assert torch.equal(l, lse) and torch.equal(o[:, :, rest], out[:, :, rest])
+    assert not torch.any(torch.isfinite(o[:, :, 7]))
+    c.status()
