@@ -528,10 +528,12 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           const bool holes = hole.x | hole.y | hole.z | hole.w;
           const bool edge = t0 < wlo || t0 + kN > whi || holes;
           float fx = f;  // x = fx * what is in S
+          bool product = false;  // S of this row holds x
           // The rare cases put x itself in S: masks, a negative f, and scores beyond 2^20, whose
-          // differences from m are exact only when they are rounded before, as m was.
+          // differences from m are exact only when they are rounded before, as m was.  (Row by row:
+          // which of its neighbours are such cases does not change a row's bits.)
           auto settle = [&]() {
-            const bool mul = edge || negative || far;
+            const bool mul = !product && (edge || negative || far);
 #pragma unroll 1
             for (int i = 0; i < kN; i += 32) {
               float x[32];
@@ -552,10 +554,10 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               tm_st32(tm_s + i, x);
             }
             tm_wait_st();
-            fx = mul ? 1.f : f;
+            product |= mul;
+            fx = product ? 1.f : f;
           };
-          const bool settled = edge || negative || some_far;
-          if (settled) {
+          if (edge || negative || some_far) {
             settle();
             tm_ld32(x[0], tm_s);
           }
@@ -583,7 +585,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               const float mn = grow ? (fabsf(top) < 0x1p23f ? top - C::kLift : top) : m;
               const float by = mn == -INFINITY ? 1.f : ex2(m - mn);
               m = mn;
-              far = fabsf(m) > 0x1p20f && m != -INFINITY;
+              far = on && fabsf(m) > 0x1p20f && m != -INFINITY;
               some_far = __any_sync(~0u, far);
               l *= by;
               if (!fresh) {
@@ -601,7 +603,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
                   tm_st32(tm_o + d, o);
                 }
               }
-              if (some_far && !settled) settle();
+              if (__any_sync(~0u, far && !product)) settle();
               tm_ld32(x[0], tm_s);
             }
             const float m0 = m == -INFINITY ? 0.f : m;

@@ -80,3 +80,34 @@ def test_values_of_tokens_whose_weight_is_next_to_nothing(d, n, new, bad):
     assert torch.equal(l, lse) and torch.equal(o[:, :, rest], out[:, :, rest])
     assert not torch.any(torch.isfinite(o[:, :, 7]))
     c.status()
+
+
+@pytest.mark.parametrize("dtype", [0, 1], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [4, 90])
+@pytest.mark.parametrize("n", [600, 5000])
+def test_scores_that_get_huge_next_to_rows_whose_are(dtype, d, new, n):
+    """Of two heads, neighbours in a warp, one has huge scores from the first token on, the other from
+    token 400 on, which takes all of the weight: its result is that token's value."""
+    c = filled(dtype, 1, 1, d, 64, 1, n, scaled=False)
+    for t in range(n):
+        row = place(c, 0, t)
+        row.zero_()
+        row[0] = 1.0 if dtype == 0 else 0x38           # 1
+    place(c, 0, 400)[1] = 2.0 ** 14 if dtype == 0 else 0x7E      # 448
+    q = torch.zeros(new, 2, d, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(6)
+    q[:, 0, 0] = 2.0 ** 25
+    q[:, 1, 1] = 2.0 ** 26 * (1 + 63 / 64 * torch.rand(new, generator=g, device="cuda")) * (1 if dtype == 0 else 2.0 ** 4)
+    q = q.bfloat16()
+    args = (0, ints([0]), ints([n]), ints([0, new]))
+    out, lse = c.attend_chunk(*args, q, n, lse=True)
+    k, v = rows_of(c, dtype, 0, 0, 0, n)
+    assert torch.equal(out[:, 1].double(), v[400].expand(new, d))
+    want = q[:, 1, 1].double() * k[400, 1] * d ** -0.5
+    assert torch.all((lse[:, 1].double() - want).abs() <= 2.0 ** -21 * want)
+    calm = q.clone()
+    calm[:, 0, 0] = 1.0
+    o, l = c.attend_chunk(*args, calm, n, lse=True)        # the other head does not matter
+    assert torch.equal(o[:, 1], out[:, 1]) and torch.equal(l[:, 1], lse[:, 1])
+    c.status()
