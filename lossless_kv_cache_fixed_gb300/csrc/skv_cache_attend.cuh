@@ -719,13 +719,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
       __syncthreads();
       for (int hh = warp; hh < nh; hh += kWarps) {
         const int64_t oh = (int64_t)b * a.q_heads + h0 + hh;
-        float q = 0.f;
-        for (int d = lane; a.norm && d < c.D; d += 32) {
-          const float y = so[hh * C::kPad + d] - so[(hh + kTileHeads) * C::kPad + d];
-          q = fmaf(y, y, q);
-        }
-        for (int x = 16; x; x >>= 1) q += __shfl_xor_sync(~0u, q, x);
-        const float r = !a.norm ? 1.f : q == 0.f ? 0.f : rsqrtf(q / c.D + a.eps);
+        Squares q;
+        for (int d = lane; a.norm && d < c.D; d += 32)
+          q.add(so[hh * C::kPad + d] - so[(hh + kTileHeads) * C::kPad + d]);
+        q.add_lanes(16);
+        const float r = !a.norm ? 1.f : q.inverse(c.D, a.eps);
         for (int d = lane * 2; d < c.D; d += 64) {
           float y[2];
 #pragma unroll
@@ -927,7 +925,8 @@ template <int ES, int DP, int NT>
 __global__ void __launch_bounds__(kWide * 32) k_attend_join_diff(AttendArgs a, int head_tiles, int grid) {
   using C = Cfg<ES, DP, NT>;
   constexpr int kVec = DP / 32;
-  __shared__ float s_w[2][kMostParts], s_o[kWide][2][DP], s_m[2][kWide], s_l[2][kWide], s_q[kWide];
+  __shared__ float s_w[2][kMostParts], s_o[kWide][2][DP], s_m[2][kWide], s_l[2][kWide];
+  __shared__ Squares s_q[kWide];
   const CacheView &c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Row r = row_of<C, true>(a, head_tiles, grid, blockIdx.x);
@@ -1003,15 +1002,15 @@ __global__ void __launch_bounds__(kWide * 32) k_attend_join_diff(AttendArgs a, i
     y = o[0] * f0 - o[1] * f1;
   }
   if (a.norm) {
-    float q = y * y;
-#pragma unroll
-    for (int s = 16; s; s >>= 1) q += __shfl_xor_sync(~0u, q, s);
+    Squares q;
+    q.add(y);
+    q.add_lanes(16);
     if (lane == 0) s_q[warp] = q;
     __syncthreads();
-    q = 0.f;
+    q = s_q[0];
 #pragma unroll
-    for (int w = 0; w < kWide; ++w) q += s_q[w];
-    if (d < c.D) y *= (q == 0.f ? 0.f : rsqrtf(q / c.D + a.eps)) * a.norm[d];
+    for (int w = 1; w < kWide; ++w) q.add(s_q[w]);
+    if (d < c.D) y = y * q.inverse(c.D, a.eps) * a.norm[d];
   }
   if (d < c.D) {
     const __nv_bfloat16 v = __float2bfloat16_rn(y);

@@ -829,7 +829,8 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         if (on && a.lse) a.lse[oh * 2 + map] = (m0 + log2f(L)) * kLn2;
         float by = L == 0.f ? 0.f : unit / L;
         if (map && on && L != 0.f) by *= a.lambda[head];
-        float n = 1.f, q = 0.f;
+        float n = 1.f;
+        Squares q;
         if constexpr (kTiles == 2) {
           // each of the two threads of a row takes half of the channels of both maps
           sh.l[map][r] = by;
@@ -846,7 +847,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               o[i] = __fsub_rn(__fmul_rn(o[i], f0), __fmul_rn(o1[i], f1));
-              if (d + i < c.D) q = fmaf(o[i], o[i], q);
+              if (a.norm && d + i < c.D) q.add(o[i]);
             }
             if (a.norm) tm_st32(lanes + C::kO + d, o);
             else emit(d, o, 1.f);
@@ -854,10 +855,12 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           if (a.norm) {
             tm_wait_st();
             if (!both()) break;  // (both have read the factors)
-            sh.l[map][r] = q;
+            sh.l[map][r] = q.root();
             if (!both()) break;
-            q = sh.l[0][r] + sh.l[1][r];
-            n = q == 0.f ? 0.f : rsqrtf(q / c.D + a.eps);
+            q = Squares();
+            q.add(sh.l[0][r]);
+            q.add(sh.l[1][r]);
+            n = q.inverse(c.D, a.eps);
 #pragma unroll 1
             for (int d = map * (DP / 2); d < min(c.D, (map + 1) * (DP / 2)); d += 32) {
               float o[32];
@@ -881,11 +884,11 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               for (int i = 0; i < 32; ++i) {
                 const float x = __fmul_rn(o[i], by), y = __shfl_xor_sync(~0u, x, 16);
                 o[i] = map ? y - x : x - y;
-                if (pass == 0 && d + i < c.D) q = fmaf(o[i], o[i], q);
+                if (pass == 0 && d + i < c.D) q.add(o[i]);
               }
               if (pass == 1) emit(d, o, n);
             }
-            if (pass == 0) n = q == 0.f ? 0.f : rsqrtf(q / c.D + a.eps);
+            if (pass == 0) n = q.inverse(c.D, a.eps);
           }
         }
       }
@@ -1727,17 +1730,16 @@ __global__ void __launch_bounds__(kJoin * 32) k_chunk_join(ChunkArgs a) {
         for (int v = 0; v < kVec; ++v) s_o[slot][lane * kVec + v] = o[v] * by;
       __syncthreads();
       if (!map) {
-        float q = 0.f;
+        Squares q;
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
           o[v] = o[v] * by - s_o[slot][lane * kVec + v];
-          if (lane * kVec + v < c.D) q = fmaf(o[v], o[v], q);
+          if (lane * kVec + v < c.D) q.add(o[v]);
         }
         by = 1.f;
         if (a.norm) {
-#pragma unroll 1
-          for (int s = 16; s; s >>= 1) q += __shfl_xor_sync(~0u, q, s);
-          by = q == 0.f ? 0.f : rsqrtf(q / c.D + a.eps);
+          q.add_lanes(16);
+          by = q.inverse(c.D, a.eps);
         }
       }
       __syncthreads();

@@ -60,6 +60,46 @@ def test_an_infinite_value_with_a_norm(d, n, new):
     c.status()
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,new", FORMS)
+@pytest.mark.parametrize("power", [-120, -60, -20, 40, 64, 90])
+def test_the_norm_of_small_and_large_results(d, n, new, power):
+    """Without eps the normalised result does not change when all values take the same power of two,
+    although the squares of the results leave the range of a float."""
+    c = filled(0, 1, 1, d, 64, 1, n)
+    rows = new or 1
+    q = queries(rows, 2, d)
+    lam = torch.tensor([0.5, -0.5], device="cuda")
+    norm = torch.rand(d, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda") + 0.2
+    args = (0, ints([0]), ints([n]), q, lam, n)
+    more = dict(starts=None if new is None else ints([0, new]), norm=norm)
+    v = c.table[0, 0, 1, 0].long()
+    pool = c.pool.view(torch.bfloat16)
+    x = pool[v]
+    pool[v] = torch.where(x.abs() < 2.0 ** -5, 0.0, x)     # (no power of two makes a subnormal)
+    want = c.attend_diff(*args, eps=0.0, **more)
+    one = c.attend_diff(*args, eps=1e-5, **more)
+    pool[v] = (pool[v].float() * 2.0 ** power).bfloat16()
+    got = c.attend_diff(*args, eps=0.0, **more)
+    assert torch.all(torch.isfinite(want)) and torch.any(want != 0)
+    # (2^-22 of the sum of squares and of each product; half a step of bf16 on either side)
+    off = (got.double() - want.double()).abs()
+    assert torch.all(off <= 2.0 ** -7 * want.double().abs() + 2.0 ** -18)
+    # with eps: large results do not feel it, small ones have the root of eps for a divisor
+    got = c.attend_diff(*args, eps=1e-5, **more).double()
+    if power > 0:
+        assert torch.all((got - want.double()).abs() <= 2.0 ** -7 * want.double().abs() + 2.0 ** -18)
+    elif power < -20:
+        plain = c.attend_diff(*args, eps=0.0, starts=more["starts"]).double()
+        ref = plain * norm.double() / math.sqrt(1e-5)
+        # (`plain` is bf16: below 2^-126 its half step is 2^-134 whatever its size, which enters times
+        # norm / sqrt(eps); the same of the result itself)
+        half = 2.0 ** -134
+        assert torch.all((got - ref).abs() <= 2.0 ** -7 * ref.abs() + half * (norm.double() / math.sqrt(1e-5) + 2))
+    assert torch.all(torch.isfinite(one))
+    c.status()
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("n,new", [(300, 5), (3000, 5), (20000, 60), (3000, 100)])
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
