@@ -137,6 +137,11 @@ struct Div {
 // channels times 2^-70 and 2^70.
 struct Squares {
   float q = 0.f, big = 0.f, tiny = 0.f;
+  // whether a sum of squares does without the other two (where eps is 2^-60 or more, squares
+  // below 2^-80 do not count next to it)
+  static __device__ __forceinline__ bool enough(float q, float eps) {
+    return q <= 0x1p100f && (q >= 0x1p-80f || eps >= 0x1p-60f);
+  }
   __device__ __forceinline__ void add(float x) {
     const float b = x * 0x1p-70f, t = x * 0x1p70f;
     q = fmaf(x, x, q);
@@ -148,23 +153,20 @@ struct Squares {
     big += o.big;
     tiny += o.tiny;
   }
-  __device__ __forceinline__ void add_lanes(int most) {  // of 2 * most lanes
-    for (int s = most; s; s >>= 1) {
+  __device__ __forceinline__ void add_lanes() {
+    for (int s = 16; s; s >>= 1) {
       q += __shfl_xor_sync(~0u, q, s);
       big += __shfl_xor_sync(~0u, big, s);
       tiny += __shfl_xor_sync(~0u, tiny, s);
     }
   }
-  __device__ __forceinline__ float root() const {
-    return big >= 0x1p-60f ? sqrtf(big) * 0x1p70f : q < 0x1p-80f ? sqrtf(tiny) * 0x1p-70f : sqrtf(q);
-  }
-  // 1 / sqrt(mean + eps), 0 for a result of zeros.  (Where eps is 2^-60 or more, squares below 2^-80
-  // do not count next to it; a float holds eps times 2^140 where it is less.)
+  // 1 / sqrt(mean + eps), 0 for a result of zeros
   __device__ __forceinline__ float inverse(int n, float eps) const {
+    if (enough(q, eps)) return rsqrtf(q / n + eps);
     if (big >= 0x1p-60f) return rsqrtf(big / n + eps * 0x1p-70f * 0x1p-70f) * 0x1p-70f;
-    if (q < 0x1p-80f && eps < 0x1p-60f)
-      return tiny == 0.f ? 0.f : rsqrtf(tiny / n + eps * 0x1p70f * 0x1p70f) * 0x1p70f;
-    return rsqrtf(q / n + eps);
+    if (tiny == 0.f) return 0.f;
+    // (eps is below 2^-60, or the sum is NaN)
+    return rsqrtf(tiny / n + eps * 0x1p70f * 0x1p70f) * 0x1p70f;
   }
 };
 

@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
         Squares q;
         for (int d = lane; a.norm && d < c.D; d += 32)
           q.add(so[hh * C::kPad + d] - so[(hh + kTileHeads) * C::kPad + d]);
-        q.add_lanes(16);
+        q.add_lanes();
         const float r = !a.norm ? 1.f : q.inverse(c.D, a.eps);
         for (int d = lane * 2; d < c.D; d += 64) {
           float y[2];
@@ -1004,7 +1004,7 @@ __global__ void __launch_bounds__(kWide * 32) k_attend_join_diff(AttendArgs a, i
   if (a.norm) {
     Squares q;
     q.add(y);
-    q.add_lanes(16);
+    q.add_lanes();
     if (lane == 0) s_q[warp] = q;
     __syncthreads();
     q = s_q[0];

@@ -388,6 +388,125 @@ struct Part {
 };
 constexpr size_t kCutBytes = (sizeof(Cut) * kMostBlocks + 255) / 256 * 256;
 
+// What follows runs rarely and is kept out of the loops' code.
+// Scores of a row in tensor memory times f, where mul says so; with edge those of tokens outside
+// [from, to) of the block, and the missing ones, become -infinity.
+template <int N>
+__device__ __noinline__ void settle_scores(uint32_t tm_s, bool mul, float f, bool edge, int from, int to,
+                                           const uint32_t *missing) {
+#pragma unroll 1
+  for (int i = 0; i < N; i += 32) {
+    float x[32];
+    tm_ld32(x, tm_s + i);
+    tm_wait_ld();
+    uint32_t out = 0;  // tokens that this row does not see
+    if (edge) {
+      const int a = min(max(from - i, 0), 32), b = min(max(to - i, 0), 32);
+      out = N == 128 ? missing[i / 32] : (missing[i / 16] & 0xffffu) | missing[i / 16 + 1] << 16;
+      out |= ~(uint32_t)(((1ull << b) - 1) & ~((1ull << a) - 1));
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      x[k] = mul ? __fmul_rn(x[k], f) : x[k];
+      if (out >> k & 1) x[k] = -INFINITY;
+    }
+    tm_st32(tm_s + i, x);
+  }
+  tm_wait_st();
+}
+// The largest of a row's scores in tensor memory times f.
+template <int N>
+__device__ __noinline__ float top_score(uint32_t tm_s, float f) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int i = 0; i < N; i += 32) {
+    float x[32];
+    tm_ld32(x, tm_s + i);
+    tm_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) top = fmaxf(top, __fmul_rn(x[k], f));
+  }
+  return top;
+}
+// A row's sums in tensor memory times f.
+template <int N>
+__device__ __noinline__ void scale_sums(uint32_t tm_o, float f) {
+#pragma unroll 1
+  for (int d = 0; d < N; d += 32) {
+    float o[32];
+    tm_ld32(o, tm_o + d);
+    tm_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] *= f;
+    tm_st32(tm_o + d, o);
+  }
+}
+// Sums become 0 where `none` says so.
+template <int N>
+__device__ __noinline__ void clear_sums(uint32_t tm_o, bool none) {
+#pragma unroll 1
+  for (int d = 0; d < N; d += 32) {
+    float o[32];
+    tm_ld32(o, tm_o + d);
+    tm_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i];
+    tm_st32(tm_o + d, o);
+  }
+  tm_wait_st();
+}
+// Adds the values that were left out of a row's sums because they are not finite: those of tokens
+// [lo, hi) that the row sees in blocks that some row of the item does not see in whole.
+template <int ES, int N>
+__device__ __noinline__ void add_not_finite(uint32_t tm_o, const CacheView &c, Div by_page, const uint32_t *tab,
+                                            bool on, int lo, int hi, int most, int least, int t0, int end,
+                                            int step) {
+#pragma unroll 1
+  for (int d = 0; d < c.D; d += 32) {
+    float o[32];
+    tm_ld32(o, tm_o + d);
+    tm_wait_ld();
+#pragma unroll 1
+    for (int b = t0; b < end; b += step) {
+      if (!on || (b >= most && b + N <= least)) continue;
+#pragma unroll 1
+      for (int t = max(b, lo); t < min(b + N, hi); ++t) {
+        const int blk = by_page.of(t);
+        const uint32_t pk = tab[blk], pv = tab[(int64_t)c.heads * c.blocks + blk];
+        if (pk >= c.pages || pv >= c.pages) continue;
+        const uint8_t *row = c.pool + (uint64_t)pv * c.page_bytes + (uint32_t)(t - blk * c.Tb) * c.row_bytes;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if (d + i >= c.D) continue;
+          if (ES == 2) {
+            const uint16_t w = reinterpret_cast<const uint16_t *>(row)[d + i];
+            if ((w & 0x7f80) == 0x7f80) o[i] += __uint_as_float((uint32_t)w << 16);
+          } else if ((row[d + i] & 0x7f) == 0x7f) {
+            o[i] = NAN;
+          }
+        }
+      }
+    }
+    __syncwarp();
+    tm_st32(tm_o + d, o);
+  }
+  tm_wait_st();
+}
+// The norm of a row of n channels in tensor memory, whatever power of two they lie at.
+__device__ __noinline__ float inverse_norm(uint32_t tm, int n, float eps) {
+  Squares all;
+#pragma unroll 1
+  for (int d = 0; d < n; d += 32) {
+    float o[32];
+    tm_ld32(o, tm + d);
+    tm_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (d + i < n) all.add(o[i]);
+  }
+  return all.inverse(n, eps);
+}
+
 template <int ES, int DP, bool DIFF>
 __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
     ChunkArgs a, int cut, int box, const __grid_constant__ CUtensorMap map) {
@@ -534,30 +653,12 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           // which of its neighbours are such cases does not change a row's bits.)
           auto settle = [&]() {
             const bool mul = !product && (edge || negative || far);
-#pragma unroll 1
-            for (int i = 0; i < kN; i += 32) {
-              float x[32];
-              tm_ld32(x, tm_s + i);
-              tm_wait_ld();
-              uint32_t out = 0;  // tokens that this row does not see
-              if (edge) {
-                const int from = min(max(lo - t0 - i, 0), 32), to = min(max(hi - t0 - i, 0), 32);
-                const uint32_t *w = reinterpret_cast<const uint32_t *>(&hole_of);
-                out = kN == 128 ? w[i / 32] : (w[i / 16] & 0xffffu) | w[i / 16 + 1] << 16;
-                out |= ~(uint32_t)(((1ull << to) - 1) & ~((1ull << from) - 1));
-              }
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                x[k] = mul ? __fmul_rn(x[k], f) : x[k];
-                if (out >> k & 1) x[k] = -INFINITY;
-              }
-              tm_st32(tm_s + i, x);
-            }
-            tm_wait_st();
+            settle_scores<kN>(tm_s, mul, f, edge, lo - t0, hi - t0, reinterpret_cast<const uint32_t *>(&hole_of));
             product |= mul;
             fx = product ? 1.f : f;
           };
           if (edge || negative || some_far) {
+            tm_wait_ld();  // (no load is under way where a function is called)
             settle();
             tm_ld32(x[0], tm_s);
           }
@@ -568,19 +669,12 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           // are written over it.
           bool ok = true;
 #pragma unroll 1
-          for (int again = fresh ? 1 : 0; again < 2; ++again) {
-            if (again) {
+          for (bool grows = fresh;;) {
+            if (grows) {
+              tm_wait_ld();
               // only rows that pass it change, so that no row's bits depend on another's
               const bool grow = total > C::kFull || m == -INFINITY;
-              float top = -INFINITY;
-#pragma unroll 1
-              for (int i = 0; i < kN; i += 32) {
-                float y[32];
-                tm_ld32(y, tm_s + i);
-                tm_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 32; ++k) top = fmaxf(top, __fmul_rn(y[k], fx));
-              }
+              const float top = top_score<kN>(tm_s, fx);
               // (beyond 2^23 a float has no room for kLift)
               const float mn = grow ? (fabsf(top) < 0x1p23f ? top - C::kLift : top) : m;
               const float by = mn == -INFINITY ? 1.f : ex2(m - mn);
@@ -593,15 +687,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
                 // (but not before the one before that, so the barrier is one phase ahead at most).
                 if (kTiles == 1 && !(ok = wait(sh.o_full[0], (mine - 1) & 1))) break;
                 fence_after();
-#pragma unroll 1
-                for (int d = 0; d < DP; d += 32) {
-                  float o[32];
-                  tm_ld32(o, tm_o + d);
-                  tm_wait_ld();
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) o[i] *= by;
-                  tm_st32(tm_o + d, o);
-                }
+                scale_sums<DP>(tm_o, by);
               }
               if (__any_sync(~0u, far && !product)) settle();
               tm_ld32(x[0], tm_s);
@@ -623,7 +709,8 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               }
             }
             total = (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
-            if (again == 0 && !__any_sync(~0u, on && (total > C::kFull || m == -INFINITY))) break;
+            if (grows || !__any_sync(~0u, on && (total > C::kFull || m == -INFINITY))) break;
+            grows = true;
           }
           if (!ok) break;
 #pragma unroll
@@ -652,52 +739,13 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         const int least = a.full ? s.len : min(s.len, s.base + a.by_group.of(s.p0) + 1);
         const uint32_t *tab =
             c.table + ((int64_t)s.slot * c.rows + ((int64_t)a.layer * 2) * c.heads + s.h) * c.blocks;
-#pragma unroll 1
-        for (int d = 0; d < c.D; d += 32) {
-          float o[32];
-          tm_ld32(o, tm_o + d);
-          tm_wait_ld();
-#pragma unroll 1
-          for (int u = u_from; u < nu; u += u_step) {
-            const int t0 = s.t0 + u * kN;
-            if (!on || (t0 >= most && t0 + kN <= least)) continue;
-#pragma unroll 1
-            for (int t = max(t0, lo); t < min(t0 + kN, hi); ++t) {
-              const uint32_t pk = tab[a.by_page.of(t)], pv = tab[(int64_t)c.heads * c.blocks + a.by_page.of(t)];
-              if (pk >= c.pages || pv >= c.pages) continue;
-              const uint8_t *row = c.pool + (uint64_t)pv * c.page_bytes + (uint32_t)(t - a.by_page.of(t) * c.Tb) * c.row_bytes;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                if (d + i >= c.D) continue;
-                if (ES == 2) {
-                  const uint16_t w = reinterpret_cast<const uint16_t *>(row)[d + i];
-                  if ((w & 0x7f80) == 0x7f80) o[i] += __uint_as_float((uint32_t)w << 16);
-                } else if ((row[d + i] & 0x7f) == 0x7f) {
-                  o[i] = NAN;
-                }
-              }
-            }
-          }
-          __syncwarp();
-          tm_st32(tm_o + d, o);
-        }
-        tm_wait_st();
+        add_not_finite<ES, kN>(tm_o, c, a.by_page, tab, on, lo, hi, most, least, s.t0 + u_from * kN,
+                               s.t0 + nu * kN, u_step * kN);
       }
-      if (nu > 0 && rows && __any_sync(~0u, l == 0.f)) {
-        // Sums of rows that see nothing may be 0 times infinity.  They become 0 here, so that below a
-        // factor of 0 (a tile's weight next to the other's, lambda, the norm of an infinite row) is a
-        // number like others, whose product with an infinity is NaN.
-#pragma unroll 1
-        for (int d = 0; d < DP; d += 32) {
-          float o[32];
-          tm_ld32(o, tm_o + d);
-          tm_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i];
-          tm_st32(tm_o + d, o);
-        }
-        tm_wait_st();
-      }
+      // Sums of rows that see nothing may be 0 times infinity.  They become 0 here, so that below a factor
+      // of 0 (a tile's weight next to the other's, lambda, the norm of an infinite row) is a number like
+      // others, whose product with an infinity is NaN.
+      if (nu > 0 && rows && __any_sync(~0u, l == 0.f)) clear_sums<DP>(tm_o, l == 0.f);
       // Results leave through shared memory, so that 4 lanes write 64 bytes of one row: a lane's
       // own row in 16-byte pieces would be 32 rows per store (10000 clocks a tile, 2000 so).
       const bool emits = on && !(DIFF && kTiles == 1 && lane >= 16);
@@ -829,8 +877,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         if (on && a.lse) a.lse[oh * 2 + map] = (m0 + log2f(L)) * kLn2;
         float by = L == 0.f ? 0.f : unit / L;
         if (map && on && L != 0.f) by *= a.lambda[head];
-        float n = 1.f;
-        Squares q;
+        float n = 1.f, q = 0.f;
         if constexpr (kTiles == 2) {
           // each of the two threads of a row takes half of the channels of both maps
           sh.l[map][r] = by;
@@ -847,20 +894,25 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               o[i] = __fsub_rn(__fmul_rn(o[i], f0), __fmul_rn(o1[i], f1));
-              if (a.norm && d + i < c.D) q.add(o[i]);
+              if (d + i < c.D) q = fmaf(o[i], o[i], q);
             }
             if (a.norm) tm_st32(lanes + C::kO + d, o);
             else emit(d, o, 1.f);
           }
           if (a.norm) {
             tm_wait_st();
+            fence_before();
             if (!both()) break;  // (both have read the factors)
-            sh.l[map][r] = q.root();
+            sh.l[map][r] = q;
             if (!both()) break;
-            q = Squares();
-            q.add(sh.l[0][r]);
-            q.add(sh.l[1][r]);
-            n = q.inverse(c.D, a.eps);
+            q = sh.l[0][r] + sh.l[1][r];
+            n = rsqrtf(q / c.D + a.eps);
+            const bool odd = on && !Squares::enough(q, a.eps);
+            if (__any_sync(~0u, odd)) {  // (each of a row's threads takes all channels)
+              fence_after();
+              const float m = inverse_norm(lanes + C::kO, c.D, a.eps);
+              if (odd) n = m;
+            }
 #pragma unroll 1
             for (int d = map * (DP / 2); d < min(c.D, (map + 1) * (DP / 2)); d += 32) {
               float o[32];
@@ -874,7 +926,9 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         } else {
           // lanes i and i + 16 have a row's two maps
 #pragma unroll 1
-          for (int pass = a.norm ? 0 : 1; pass < 2; ++pass) {
+          for (int pass = a.norm ? 0 : 2; pass < 3; ++pass) {
+            Squares all;  // second pass, where a row asks for it
+            if (pass == 1 && !__any_sync(~0u, on && !Squares::enough(q, a.eps))) continue;
 #pragma unroll 1
             for (int d = 0; d < c.D; d += 32) {
               float o[32];
@@ -884,11 +938,13 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               for (int i = 0; i < 32; ++i) {
                 const float x = __fmul_rn(o[i], by), y = __shfl_xor_sync(~0u, x, 16);
                 o[i] = map ? y - x : x - y;
-                if (pass == 0 && d + i < c.D) q.add(o[i]);
+                if (pass == 0 && d + i < c.D) q = fmaf(o[i], o[i], q);
+                if (pass == 1 && d + i < c.D) all.add(o[i]);
               }
-              if (pass == 1) emit(d, o, n);
+              if (pass == 2) emit(d, o, n);
             }
-            if (pass == 0) n = q.inverse(c.D, a.eps);
+            if (pass == 0) n = rsqrtf(q / c.D + a.eps);
+            if (pass == 1 && !Squares::enough(q, a.eps)) n = all.inverse(c.D, a.eps);
           }
         }
       }
@@ -1730,16 +1786,25 @@ __global__ void __launch_bounds__(kJoin * 32) k_chunk_join(ChunkArgs a) {
         for (int v = 0; v < kVec; ++v) s_o[slot][lane * kVec + v] = o[v] * by;
       __syncthreads();
       if (!map) {
-        Squares q;
+        float q = 0.f;
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
           o[v] = o[v] * by - s_o[slot][lane * kVec + v];
-          if (lane * kVec + v < c.D) q.add(o[v]);
+          if (lane * kVec + v < c.D) q = fmaf(o[v], o[v], q);
         }
         by = 1.f;
         if (a.norm) {
-          q.add_lanes(16);
-          by = q.inverse(c.D, a.eps);
+#pragma unroll 1
+          for (int s = 16; s; s >>= 1) q += __shfl_xor_sync(~0u, q, s);
+          by = rsqrtf(q / c.D + a.eps);
+          if (!Squares::enough(q, a.eps)) {  // the whole warp
+            Squares all;
+#pragma unroll
+            for (int v = 0; v < kVec; ++v)
+              if (lane * kVec + v < c.D) all.add(o[v]);
+            all.add_lanes();
+            by = all.inverse(c.D, a.eps);
+          }
         }
       }
       __syncthreads();
