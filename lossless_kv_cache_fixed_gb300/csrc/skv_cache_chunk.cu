@@ -506,6 +506,58 @@ __device__ __noinline__ float inverse_norm(uint32_t tm, int n, float eps) {
   }
   return all.inverse(n, eps);
 }
+// q . k over n channels, a multiple of 8
+template <int ES>
+__device__ __noinline__ float half_score(const uint16_t *q, const uint8_t *k, int n) {
+  float y = 0.f;
+#pragma unroll 1
+  for (int d = 0; d < n; d += 2) {
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(q + d);
+    uint32_t u;
+    if (ES == 2) {
+      u = *reinterpret_cast<const uint32_t *>(k + d * 2);
+      y = fmaf(__uint_as_float(w << 16), __uint_as_float(u << 16), y);
+      y = fmaf(__uint_as_float(w & 0xffff0000u), __uint_as_float(u & 0xffff0000u), y);
+    } else {
+      uint32_t none;
+      e4m3x4(*reinterpret_cast<const uint16_t *>(k + d), u, none);
+      const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&u));
+      y = fmaf(__uint_as_float(w << 16), v.x, y);
+      y = fmaf(__uint_as_float(w & 0xffff0000u), v.y, y);
+    }
+  }
+  return y;
+}
+// Scores in tensor memory that are NaN, of the tokens from t0 on: made again of this row's half of the
+// channels alone (map), times by.  (Tokens that the row does not see are not NaN by now.)
+template <int ES, int N>
+__device__ __noinline__ void own_half(uint32_t tm_s, const CacheView &c, bool on, int t0, Div by_page,
+                                      const uint32_t *tab, const uint16_t *q, int map, float by) {
+#pragma unroll 1
+  for (int i = 0; i < N; i += 32) {
+    float x[32];
+    tm_ld32(x, tm_s + i);
+    tm_wait_ld();
+    uint32_t bad = 0;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) bad |= (uint32_t)(x[k] != x[k]) << k;
+    if (!on) bad = 0;
+#pragma unroll 1
+    for (; bad; bad &= bad - 1) {
+      const int at = __ffs(bad) - 1, t = t0 + i + at, blk = by_page.of(t);
+      const uint32_t pk = tab[blk];
+      if (pk >= c.pages) continue;
+      const float y = half_score<ES>(
+          q, c.pool + (uint64_t)pk * c.page_bytes + (uint32_t)(t - blk * c.Tb) * c.row_bytes + map * (c.row_bytes / 2),
+          c.D / 2);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) x[k] = k == at ? y * by : x[k];
+    }
+    __syncwarp();
+    tm_st32(tm_s + i, x);
+  }
+  tm_wait_st();
+}
 
 template <int ES, int DP, bool DIFF>
 __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
@@ -632,6 +684,9 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         // blocks from wlo to whi are seen by all rows of the warp
         const int wlo = __reduce_max_sync(~0u, lo), whi = __reduce_min_sync(~0u, hi), end = s.t0 + nu * kN;
         bool fresh = true;  // the first of the tile's blocks
+        // Where a step of 16 channels has some of both halves, or a tile rows of both maps, the zeros of a
+        // row's query meet the other half's keys, and 0 * infinity is NaN.
+        const bool mixed = DIFF && (kTiles == 1 || c.D % 32);
 #pragma unroll 1
         for (int t0 = s.t0 + u_from * kN; t0 < end; t0 += u_step * kN) {
           const int buf = kTiles == 2 ? tile : (int)(mine & 1);
@@ -667,7 +722,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
           // The weights with the m so far.  Where they add up to more than kFull, or a row has
           // not seen a token yet, m grows and they are made again: S is there until the weights
           // are written over it.
-          bool ok = true;
+          bool ok = true, looked = !mixed;
 #pragma unroll 1
           for (bool grows = fresh;;) {
             if (grows) {
@@ -709,7 +764,23 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
               }
             }
             total = (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
-            if (grows || !__any_sync(~0u, on && (total > C::kFull || m == -INFINITY))) break;
+            // (with two maps NaN too: see below)
+            if (!__any_sync(~0u, on && ((DIFF ? !(total <= C::kFull) : total > C::kFull) || m == -INFINITY))) break;
+            if (DIFF && !looked && __any_sync(~0u, on && total != total)) {
+              // a NaN may be of the other half's channels: those scores are made again
+              // (e4m3: S is of q over a power of two)
+              const float by = ES == 1 ? 1.f / __uint_as_float((uint32_t)sh.qe[sidx & 1][tile][r] << 23) : 1.f;
+              own_half<ES, kN>(
+                  tm_s, c, on, t0, a.by_page,
+                  c.table + ((int64_t)s.slot * c.rows + ((int64_t)a.layer * 2) * c.heads + s.h) * c.blocks,
+                  a.q + ((int64_t)s.q0 + j) * a.qs + (int64_t)head * a.qhs + map * (c.D / 2), map,
+                  product ? by * f : by);
+              looked = true;
+              grows = false;
+              tm_ld32(x[0], tm_s);
+              continue;
+            }
+            if (grows) break;
             grows = true;
           }
           if (!ok) break;

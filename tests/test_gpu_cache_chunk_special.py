@@ -151,3 +151,60 @@ def test_scores_that_get_huge_next_to_rows_whose_are(dtype, d, new, n):
     o, l = c.attend_chunk(*args, calm, n, lse=True)        # the other head does not matter
     assert torch.equal(o[:, 1], out[:, 1]) and torch.equal(l[:, 1], lse[:, 1])
     c.status()
+
+
+@pytest.mark.parametrize("dtype", [0, 1], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [16, 48, 64, 80, 128, 192, 256])
+@pytest.mark.parametrize("n,new", [x for x in FORMS if x[1]])
+@pytest.mark.parametrize("half", [0, 1])
+def test_keys_that_are_not_finite_in_one_half(dtype, d, n, new, half):
+    """An infinity that gives a token no weight in one map, or a NaN, has no effect on the other map."""
+    c = filled(dtype, 1, 1, d, 64, 1, n, seed=d)
+    rows = new or 1
+    q = queries(rows, 3, d, 5)
+    lam = torch.tensor([0.5, -0.3, 1.1], device="cuda")
+    ch = half * d // 2 + d // 2 - 1
+    q[:, :, ch] = q[:, :, ch].abs() + 0.1
+    args = (0, ints([0]), ints([n]), q, lam, n)
+    starts = None if new is None else ints([0, new])
+    k, v = rows_of(c, dtype, 0, 0, 0, n)
+    ok = seen(n - rows + torch.arange(rows, device="cuda"), n, 0, 0, True)
+    at = torch.cat([torch.arange(2, n, 61), torch.tensor([n - rows])]).tolist()
+    for t in at:
+        if dtype == 0:
+            place(c, 0, t)[ch] = -math.inf
+        else:
+            place(c, 0, t)[ch] = 0x7F
+    o, l = c.attend_diff(*args, starts=starts, lse=True)
+    there = ok.clone()
+    there[:, at] = False                               # what the map with the infinities sees
+    for h in range(3):
+        res = []
+        for m in (0, 1):
+            part = slice(m * d // 2, (m + 1) * d // 2)
+            see = there if m == half and dtype == 0 else ok
+            w = k.clone()
+            w[at, ch] = 0.0 if m == half else w[at, ch]
+            res.append(one_map(dtype, q[:, h, part].double(), w[:, part], v, see, (d // 2) ** -0.5))
+            if m != half or dtype == 0:
+                assert torch.all((l[:, h, m].double() - res[m][1]).abs() <= res[m][3]), (h, m)
+        if dtype == 0:
+            f = float(lam[h])
+            ref = res[0][0] - f * res[1][0]
+            tol = res[0][2] + abs(f) * res[1][2] + 2.0 ** -22 * ref.abs()
+            assert torch.all((o[:, h].double() - ref).abs() <= tol + 2.0 ** -8 * (ref.abs() + tol)), h
+        else:
+            last = ok[:, at].any(1)
+            assert torch.all(torch.isnan(l[last, h, half])) and torch.all(torch.isnan(o[last, h]))
+    # a NaN: its map and the result are NaN where the token is seen
+    t = n - rows // 2 - 1
+    place(c, 0, t)[ch] = math.nan if dtype == 0 else 0xFF
+    o2, l2 = c.attend_diff(*args, starts=starts, lse=True)
+    first = t - (n - rows)
+    assert torch.all(torch.isnan(o2[first:])) and torch.all(torch.isnan(l2[first:, :, half]))
+    for h in range(3):
+        m = 1 - half
+        part = slice(m * d // 2, (m + 1) * d // 2)
+        _, rl, _, tl = one_map(dtype, q[:, h, part].double(), k[:, part], v, ok, (d // 2) ** -0.5)
+        assert torch.all((l2[:, h, m].double() - rl).abs() <= tl)
+    c.status()
