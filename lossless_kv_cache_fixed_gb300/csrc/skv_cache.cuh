@@ -2,6 +2,7 @@
 // skv_cache_append.cu, skv_cache_attend*, skv_cache_chunk.cu) and their C ABI
 // (skv_cache_api.cu) share.  Not installed; not part of the ABI.
 #pragma once
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -131,6 +132,35 @@ struct Div {
     return (int)(((uint32_t)n + __umulhi((uint32_t)n, mul)) >> shift);
   }
 };
+
+// four e4m3 codes to halves: the two in the low 16 bits, the two in the high
+__device__ __forceinline__ void e4m3x4(uint32_t v, uint32_t &lo, uint32_t &hi) {
+  asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
+}
+// q . k over n channels, a multiple of 8 (e4m3 codes or bf16): scores that a matrix product did not give
+template <int ES>
+static __device__ __noinline__ float half_score(const uint16_t *q, const uint8_t *k, int n) {
+  float y = 0.f;
+#pragma unroll 1
+  for (int d = 0; d < n; d += 2) {
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(q + d);
+    uint32_t u;
+    if (ES == 2) {
+      u = *reinterpret_cast<const uint32_t *>(k + d * 2);
+      y = fmaf(__uint_as_float(w << 16), __uint_as_float(u << 16), y);
+      y = fmaf(__uint_as_float(w & 0xffff0000u), __uint_as_float(u & 0xffff0000u), y);
+    } else {
+      uint32_t none;
+      e4m3x4(*reinterpret_cast<const uint16_t *>(k + d), u, none);
+      const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&u));
+      y = fmaf(__uint_as_float(w << 16), v.x, y);
+      y = fmaf(__uint_as_float(w & 0xffff0000u), v.y, y);
+    }
+  }
+  return y;
+}
 
 // The mean square of a result's channels, whatever power of two they lie at: the squares of
 // numbers beyond 2^64 or below 2^-63 leave the range of a float, so two more sums are taken of the

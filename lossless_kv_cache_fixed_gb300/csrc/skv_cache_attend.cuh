@@ -124,12 +124,6 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// four e4m3 codes to halves: the two in the low 16 bits, the two in the high
-__device__ __forceinline__ void e4m3x4(uint32_t v, uint32_t &lo, uint32_t &hi) {
-  asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(v));
-}
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -530,6 +524,53 @@ __global__ void __launch_bounds__(kThreads, (Cfg<ES, DP, NT>::kPerSm)) k_attend(
                 mma<ES>(x[mt][n], a0, a1, a2, a3, qf[n][k + kk][0], qf[n][k + kk][1]);
             }
           }
+        }
+      }
+      if (DIFF) {
+        // The zeros of a column's query meet the other half's keys, and 0 * infinity is NaN: scores that
+        // are NaN are made again of the column's own half.  (Their sum tells, one addition each.)
+        float all = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < C::kTok / 16; ++mt)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) all += x[mt][n][i];
+        if (__any_sync(~0u, all != all)) {
+          uint32_t todo = 0;
+#pragma unroll
+          for (int mt = 0; mt < C::kTok / 16; ++mt)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                todo |= (uint32_t)(x[mt][n][i] != x[mt][n][i]) << ((mt * NT + n) * 4 + i);
+#pragma unroll 1
+          for (; todo; todo &= todo - 1) {
+            const int at = __ffs(todo) - 1, n = at / 4 % NT;
+            const int t = t0 + at / (4 * NT) * 16 + g8 + (at & 2) * 4, col = n * 8 + 2 * j + (at & 1);
+            const int map = col >= kTileHeads, hq = col - map * kTileHeads;
+            if (hq >= nh || t < sp.begin || t >= sp.end) continue;
+            const uint32_t pk = tab_k[t / c.Tb];
+            if (pk >= c.pages) continue;
+            // (x is of q over a power of two: f has it)
+            float s = a.scale * kLog2e;
+            if (ES == 1 && c.scale) s *= c.scale[a.layer * c.heads + h];
+            const float fc = at & 1 ? (NT == 2 && n ? f[NT - 1][1] : f[0][1])
+                                    : (NT == 2 && n ? f[NT - 1][0] : f[0][0]);
+            const float y = half_score<ES>(
+                a.q + (int64_t)b * a.qs + (int64_t)(h0 + hq) * a.qhs + map * (c.D / 2),
+                c.pool + (uint64_t)pk * c.page_bytes + (uint32_t)(t % c.Tb) * c.row_bytes + map * (c.row_bytes / 2),
+                c.D / 2) * (ES == 1 && fc != 0.f ? s / fc : 1.f);
+#pragma unroll
+            for (int mt = 0; mt < C::kTok / 16; ++mt)
+#pragma unroll
+              for (int m = 0; m < NT; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if ((mt * NT + m) * 4 + i == at) x[mt][m][i] = y;
+          }
+          __syncwarp();
         }
       }
       // scale, mask, running maximum

@@ -283,11 +283,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&v);
 }
-__device__ __forceinline__ void e4m3x4(uint32_t v, uint32_t &lo, uint32_t &hi) {
-  asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(v));
-}
 
 // Tiles in shared memory: blocks of 64 channels, in each a row of 128 bytes per token (or
 // packed row), whose 16-byte chunks are permuted by the row (128-byte swizzle).  As an operand
@@ -505,28 +500,6 @@ __device__ __noinline__ float inverse_norm(uint32_t tm, int n, float eps) {
       if (d + i < n) all.add(o[i]);
   }
   return all.inverse(n, eps);
-}
-// q . k over n channels, a multiple of 8
-template <int ES>
-__device__ __noinline__ float half_score(const uint16_t *q, const uint8_t *k, int n) {
-  float y = 0.f;
-#pragma unroll 1
-  for (int d = 0; d < n; d += 2) {
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(q + d);
-    uint32_t u;
-    if (ES == 2) {
-      u = *reinterpret_cast<const uint32_t *>(k + d * 2);
-      y = fmaf(__uint_as_float(w << 16), __uint_as_float(u << 16), y);
-      y = fmaf(__uint_as_float(w & 0xffff0000u), __uint_as_float(u & 0xffff0000u), y);
-    } else {
-      uint32_t none;
-      e4m3x4(*reinterpret_cast<const uint16_t *>(k + d), u, none);
-      const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&u));
-      y = fmaf(__uint_as_float(w << 16), v.x, y);
-      y = fmaf(__uint_as_float(w & 0xffff0000u), v.y, y);
-    }
-  }
-  return y;
 }
 // Scores in tensor memory that are NaN, of the tokens from t0 on: made again of this row's half of the
 // channels alone (map), times by.  (Tokens that the row does not see are not NaN by now.)
