@@ -657,8 +657,9 @@ int skv_cache_attend(const skv_cache *cache, int32_t layer, const int32_t *slots
  *   batch        sequences.
  *   tokens       rows of q and out; rows that no sequence names are left as they are.
  *   max_len      host: no lens[i] is larger (it sizes the launch); heads * (tokens *
- *                q_heads / heads / 64 + batch) * (max_len / 64 + 4) must be below 2^31,
- *                without starts also batch * q_heads * (max_len / 64 + 4).
+ *                q_heads / heads / 64 + batch) * (max_len / 64 + 12) must be below 2^31,
+ *                without starts also batch * q_heads * (max_len / 64 + 4); tokens *
+ *                q_heads below 2^31 - 512.
  *   window       tokens that a token sees, itself included; 0: no window.
  *   flags        SKV_CHUNK_FULL or 0.
  *   reserved     0.

@@ -87,11 +87,12 @@ int attend_chunk(const skv_cache *cache, int32_t layer, const skv_chunk *k, cons
       k->window < 0 || k->max_len < 0 || k->max_len > INT_MAX - 1024)
     return SKV_ERR_ARG;
   if (!k->starts && k->tokens != k->batch) return SKV_ERR_ARG;
-  // the units of all rows, and the rows of all heads, are 32-bit
+  // The units of all rows are 32-bit: an item has max_len / 64 + 2 blocks at most and counts for up
+  // to 8 more (kItemCost).  So are the rows of all heads, up to the end of the last item (256 rows).
   const int64_t group = q_heads / c.heads;
   const int64_t items = (k->tokens * group / 64 + k->batch) * c.heads;
-  if (k->tokens * (int64_t)q_heads > INT_MAX || items > INT_MAX ||
-      items * (k->max_len / 64 + 4) > INT_MAX ||
+  if (k->tokens * (int64_t)q_heads > INT_MAX - 512 || items > INT_MAX ||
+      items * (k->max_len / 64 + 12) > INT_MAX ||
       (!k->starts && (int64_t)k->batch * q_heads * (k->max_len / 64 + 4) > INT_MAX))
     return SKV_ERR_ARG;
   a.lambda = a.norm = nullptr;
