@@ -698,7 +698,8 @@ size_t skv_cache_attend_chunk_workspace_bytes(const skv_cache *cache, int32_t q_
  * or page out of range is reported (SKV_ERR_ARG); that sequence's rows are empty, or that
  * page's tokens are left out.  Starts that decrease or leave 0 .. tokens are reported, and
  * that sequence's rows left as they are.  A kernel that waits for a part of itself in vain
- * gives up after two seconds (SKV_ERR_CUDA in skv_cache_status). */
+ * gives up after two seconds, in batches of 10^5 sequences or with max_len of 10^7 and
+ * more a few more (SKV_ERR_CUDA in skv_cache_status). */
 int skv_cache_attend_chunk(const skv_cache *cache, int32_t layer, const skv_chunk *chunk,
                            const void *q, int64_t q_stride, int64_t q_head_stride,
                            int32_t q_heads, float softmax_scale, void *out, float *lse,

@@ -212,6 +212,7 @@ struct ChunkArgs {
   uint8_t *ws;
   float scale, eps;
   int32_t batch, tokens, q_heads, layer, max_len, window, full;
+  long long patience;  // clocks that a wait may take
 };
 size_t chunk_ws_bytes(const CacheView &c, int32_t q_heads);
 cudaError_t launch_chunk(const ChunkArgs &a, cudaStream_t st);

@@ -53,7 +53,10 @@ constexpr int kMostBlocks = 160;  // thread blocks of a launch
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kHoles = 16;       // blocks whose missing tokens are remembered
-constexpr long long kPatience = 4000000000;  // clocks that a barrier may take before a block gives up
+// Clocks that a barrier may take before a block gives up (2 s), and as many more as its two long waits may
+// take in earnest: for the first work of a batch, every sequence of which is looked at, and for room for
+// the next item while one of up to max_len tokens is worked on.
+constexpr long long kPatience = 4000000000, kPerSequence = 1 << 13, kPerBlock = 1 << 16;
 
 constexpr uint32_t kDescHigh = 1024 >> 4 | 1u << 14 | 2u << 29;  // see desc_of
 
@@ -549,7 +552,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
                 kMma1 = kTiles == 2 ? kLoad0 + 7 : kMma;
 
   // Waits for a phase of a barrier, with a limit: then the block gives up and says so.
-  auto wait1 = [&](uint64_t &bar, uint32_t parity) -> bool {
+  auto wait1 = [&](uint64_t &bar, uint32_t parity, long long patience = kPatience) -> bool {
     const uint32_t b = smem_addr(&bar);
     if (bar_try(b, parity)) return true;
     // (the device's clock; the global timer takes a microsecond to read)
@@ -559,13 +562,17 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       for (int i = 0; i < 32; ++i)
         if (bar_try(b, parity)) return true;
       if (*reinterpret_cast<volatile uint32_t *>(&sh.dead)) return false;
-    } while (clock64() - from < kPatience);
+    } while (clock64() - from < patience);
     *reinterpret_cast<volatile uint32_t *>(&sh.dead) = 1;
     atomicOr(c.status, kCacheStuck);
     return false;
   };
   auto wait = [&](uint64_t &bar, uint32_t parity) -> bool {
     const bool ok = wait1(bar, parity);
+    return __all_sync(~0u, ok);
+  };
+  auto wait_work = [&](uint32_t sidx) -> bool {  // for segment sidx
+    const bool ok = wait1(sh.seg_full[sidx & 1], (sidx >> 1) & 1, a.patience);
     return __all_sync(~0u, ok);
   };
   auto arrive = [&](uint64_t &bar) {  // one arrival per warp
@@ -627,7 +634,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
 #pragma unroll 1
     for (uint32_t sidx = 0;; ++sidx) {
       Seg &s = sh.seg[sidx & 1];
-      if (!wait(sh.seg_full[sidx & 1], (sidx >> 1) & 1)) break;
+      if (!wait_work(sidx)) break;
       const int nu = s.nu;
       if (nu < 0) break;
       const bool twin = s.twin;
@@ -1010,7 +1017,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
 #pragma unroll 1
     for (uint32_t sidx = 0; alive; ++sidx) {
       Seg &s = sh.seg[sidx & 1];
-      if (!wait(sh.seg_full[sidx & 1], (sidx >> 1) & 1)) break;
+      if (!wait_work(sidx)) break;
       const int nu = s.nu;
       const int q0 = s.q0, p0 = s.p0, p1 = s.p1, h = s.h, lo = s.lo, hi = s.hi, first = s.t0, slot = s.slot;
       // blocks before `most` or that end after `least` are masked for some rows
@@ -1404,7 +1411,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
 #pragma unroll 1
       for (uint32_t sidx = 0;; ++sidx) {
         Seg &s = sh.seg[sidx & 1];
-        if (!wait(sh.seg_full[sidx & 1], (sidx >> 1) & 1)) break;
+        if (!wait_work(sidx)) break;
         const int nu = __shfl_sync(~0u, s.nu, 0);
         const bool twin = kTiles == 2 && !DIFF && __shfl_sync(~0u, s.twin, 0);
         const bool two = kTiles == 2 && (DIFF || __shfl_sync(~0u, (int)(s.p0 + 128 < s.p1), 0));
@@ -1545,7 +1552,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
       s.fix = 0;
       // hands a segment to the other warps (lane 0)
       auto hand = [&]() -> bool {
-        if (!wait1(sh.seg_empty[sidx & 1], ((sidx >> 1) & 1) ^ 1)) return false;
+        if (!wait1(sh.seg_empty[sidx & 1], ((sidx >> 1) & 1) ^ 1, a.patience)) return false;
         sh.seg[sidx & 1] = s;
         bar_arrive(smem_addr(&sh.seg_full[sidx & 1]));
         ++sidx;
@@ -1674,7 +1681,7 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
 #pragma unroll 1
       for (uint32_t sidx = 0; alive; ++sidx) {
         Seg &s = sh.seg[sidx & 1];
-        if (!wait(sh.seg_full[sidx & 1], (sidx >> 1) & 1)) break;
+        if (!wait_work(sidx)) break;
         const int nu = s.nu, lo = s.lo, hi = s.hi, first = s.t0;
         const uint32_t *tab_k =
             c.table + ((int64_t)s.slot * c.rows + ((int64_t)a.layer * 2) * c.heads + s.h) * c.blocks;
@@ -1919,6 +1926,7 @@ cudaError_t run(ChunkArgs a, cudaStream_t st) {
   using C = Cfg<ES, DP, DIFF>;
   a.by_group = Div(a.q_heads / a.c.heads);
   a.by_page = Div(a.c.Tb);
+  a.patience = kPatience + a.batch * kPerSequence + a.max_len / C::kN * kPerBlock;
   constexpr size_t smem = C::kOffMisc + sizeof(Misc<C>);
   static_assert(smem <= 227 * 1024, "shared memory of a block");
   const int sms = sm_count();
