@@ -322,6 +322,11 @@ class PagedCache:
             raise _bad("%s: bf16 [tokens, heads, head_dim], channels contiguous" % what)
         return st[0] if n > 1 else 0, st[1] if shape[1] > 1 else 0
 
+    def _numbers(self, what, layer, *counts):
+        """ctypes cuts what does not fit its 32 bits without a word."""
+        if not 0 <= layer < self.layers or not 0 <= min(counts) <= max(counts) < 1 << 31:
+            raise _bad("%s: layer, max_len or window" % what)
+
     def _check(self, rc, what):
         if rc:
             raise SkvError(rc, what)
@@ -461,6 +466,7 @@ class PagedCache:
                                      rope and rope.freqs, rope and rope.axis_of_pair),
                             lambda: self.append(layer, slots, at, q, k, v, rope, positions, q_out))
         n = slots.numel()
+        self._numbers("append", layer, n)
         self._ints("append", n, slots, at)
         ks = self._heads("append: k", k, n, self.heads)
         vs = self._heads("append: v", v, n, self.heads)
@@ -502,6 +508,7 @@ class PagedCache:
                             lambda: self.attend(layer, slots, lens, q, max_len, begins, scale,
                                                 out, lse))
         n = slots.numel()
+        self._numbers("attend", layer, max_len)
         self._ints("attend", n, slots, lens)
         if begins is not None:
             self._ints("attend", n, begins)
@@ -541,6 +548,7 @@ class PagedCache:
         """The call that attend_chunk (diff None) and attend_diff share; maps: sums of
         exponentials per row and head."""
         batch, d = slots.numel(), self.head_dim
+        self._numbers(what, layer, max_len, window)
         self._ints(what, batch, slots, lens)
         if begins is not None:
             self._ints(what, batch, begins)
