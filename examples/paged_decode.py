@@ -77,20 +77,28 @@ def check_attention(cache, layer, slots, lens, q, out, most=2.0 ** -7):
 
 
 def drafted(cache, rope, slot, length, m, group, g):
-    """m new tokens of one sequence in one call per layer; each sees those before it."""
+    """m new tokens of one sequence in one call per layer; each sees those before it.  The last
+    layer's heads are differential: their two halves of channels are two maps, so pairs of channels that
+    turn together lie within a half (neighbours, the same frequencies in both halves)."""
     h, d = cache.heads, cache.head_dim
     s, old, new = i32([slot]), i32([length]), i32([length + m])
     cache.reserve(s, old, new)
     at = torch.arange(length, length + m, dtype=torch.int32, device="cuda")
     lam = torch.rand(h * group, generator=g, device="cuda")
+    freqs = 1e6 ** (-2.0 * torch.arange(d // 4, device="cuda").double() / (d // 2))
+    halves = P.Rope(freqs.repeat(2), interleaved=True)
     for layer in range(cache.layers):
+        diff = layer == cache.layers - 1
         qkv = torch.randn(m, h * (group + 2), d, generator=g, device="cuda").bfloat16()
         q, k, v = qkv.split([h * group, h, h], 1)
-        q = cache.append(layer, s.expand(m).contiguous(), at, q, k, v, rope,
-                         at.expand(3, m).contiguous())
+        turn = halves if diff else rope
+        q = cache.append(layer, s.expand(m).contiguous(), at, q, k, v, turn,
+                         at.expand(turn.axes, m).contiguous())
         args = dict(starts=i32([0, m]), max_len=length + m)
-        out = cache.attend_chunk(layer, s, new, q=q, **args)
-        check_attention(cache, layer, [slot] * m, range(length + 1, length + m + 1), q, out, 2.0 ** -6)
+        if not diff:
+            out = cache.attend_chunk(layer, s, new, q=q, **args)
+            check_attention(cache, layer, [slot] * m, range(length + 1, length + m + 1), q, out, 2.0 ** -6)
+            continue
         out = cache.attend_diff(layer, s, new, q, lam, **args)
         for i in range(m):
             for j in range(h * group):

@@ -710,7 +710,11 @@ int skv_cache_attend_chunk(const skv_cache *cache, int32_t layer, const skv_chun
  *   out[i][h] = sum_t (w1_t - lambda[h] * w2_t) v_t,
  *   w1 = softmax_t(softmax_scale * q1 . k1_t),  w2 = softmax_t(softmax_scale * q2 . k2_t),
  *   lse[i][h][m] = the log of the sum of exponentials of map m, m < 2,
- * and, with a norm, out[i][h] times norm / sqrt(mean of its squares + eps).
+ * and, with a norm, out[i][h] times norm / sqrt(mean of its squares + eps).  Rotary
+ * positions turn each half by itself: skv_cache_append with SKV_ROPE_INTERLEAVED,
+ * rotary_dim = head_dim and the head_dim / 4 frequencies of a half given twice.  (Its other
+ * pairs, p and p + rotary_dim/2, take a channel of either half; then neither map's scores
+ * would depend on the distance of two tokens alone.)
  *   lambda       device fp32 [q_heads].
  *   norm         device fp32 [head_dim], or NULL.
  *   eps          not negative.

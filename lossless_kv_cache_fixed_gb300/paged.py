@@ -618,7 +618,9 @@ class PagedCache:
         [q_heads]; norm: float32 [D] or None, with it each head's result is divided by
         the root of its mean square + eps and multiplied by norm.  scale: default 1 /
         sqrt(D / 2).  Returns out [tokens, q_heads, D], with lse=True also the logs of both
-        sums of exponentials [tokens, q_heads, 2]."""
+        sums of exponentials [tokens, q_heads, 2].  Positions: append with
+        Rope(freqs.repeat(2), interleaved=True), freqs those of one half (pairs of channels
+        must not lie in both)."""
         if stream is not None:
             return self._on(stream, (slots, lens, q, lam, starts, norm, begins, out),
                             lambda: self.attend_diff(layer, slots, lens, q, lam, max_len, starts,
