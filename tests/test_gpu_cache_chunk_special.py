@@ -208,3 +208,28 @@ def test_keys_that_are_not_finite_in_one_half(dtype, d, n, new, half):
         _, rl, _, tl = one_map(dtype, q[:, h, part].double(), k[:, part], v, ok, (d // 2) ** -0.5)
         assert torch.all((l2[:, h, m].double() - rl).abs() <= tl)
     c.status()
+
+
+@pytest.mark.parametrize("dtype", [0, 1], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 256])
+def test_the_c_call_without_starts(dtype, d):
+    """starts NULL: one new token per sequence, as starts = 0 .. batch."""
+    import ctypes
+
+    from cache_helpers import skv
+    P = skv()
+    lens = [3000, 0, 77, 1234, 1]
+    c = filled(dtype, 1, 2, d, 64, 5, 3000)
+    q = queries(5, 8, d)
+    slots, n = ints([4, 2, 0, 1, 3]), ints(lens)
+    want, wl = c.attend_chunk(0, slots, n, ints(range(6)), q, 3000, lse=True)
+    out, lse = torch.empty_like(want), torch.empty_like(wl)
+    nb = P.skv_cache_attend_chunk_workspace_bytes(c.struct, 8)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    k = P.SkvChunk(5, 5, 3000, 0, 0, 0, slots.data_ptr(), n.data_ptr(), None, None)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    rc = P.skv_cache_attend_chunk(c.struct, 0, k, q.data_ptr(), q.stride(0), q.stride(1), 8, d ** -0.5,
+                                  out.data_ptr(), lse.data_ptr(), ws.data_ptr(), nb, stream)
+    assert rc == P.SKV_OK
+    c.status()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
