@@ -727,8 +727,10 @@ typedef struct {
 
 /* Differential attention of the new tokens of each sequence (starts NULL: one each) over
  * the pages of one layer; arguments, rows that see nothing and errors as
- * skv_cache_attend_chunk (one token each: weights as skv_cache_attend), but head_dim a
- * multiple of 16 and
+ * skv_cache_attend_chunk.  The difference may be small next to either map, so weights of
+ * bf16 caches meet the values as two bf16 parts (2^-16 of each); of e4m3 caches as in
+ * skv_cache_attend_chunk, with starts NULL as in skv_cache_attend.  head_dim is a multiple
+ * of 16 and
  *   lse          device fp32 [tokens][q_heads][2], or NULL. */
 int skv_cache_attend_diff(const skv_cache *cache, int32_t layer, const skv_chunk *chunk,
                           const skv_diff *diff, const void *q, int64_t q_stride,

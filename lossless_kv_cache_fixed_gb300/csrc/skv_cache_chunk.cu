@@ -20,8 +20,9 @@
 // as both (2048 tokens on 8192, 64 heads of 128: 415 us against 367).  With one tile (more than 128
 // channels, whose sums take half of the tensor memory) S has two buffers.  Items of up to 128 rows
 // let both tiles work on every second block with the same rows (9 tokens on 131071, e4m3: 90 us
-// against 110).  bf16 weights round to bf16 (2^-8 of each): in two parts, as with one new token,
-// the second product would take twice as long, and it is a third to half of the work.
+// against 110).  bf16 weights round to bf16 (2^-8 of each): in two parts, as with one new token and in
+// differential attention, the second product takes twice as long and the weights half as long again
+// (a prompt of 4096 tokens 116 us against 85.5, 2048 tokens on 8192 557 against 380).
 //
 // What bounds it: a tile's chain of scores, weights and sums.  128 x 128 scores take a tile 1350
 // clocks (512 of them the rate of the exponentials), its two products 1024, and the barriers
@@ -89,12 +90,18 @@ struct Cfg {
   // tensor memory columns
   static constexpr int kS = kN;            // S of a tile (or buffer); P in the first half
   static constexpr int kO = 2 * kN;        // O, DP columns per tile
-  // A row's m grows, to kLift below its maximum, when a block's weights add up to more than kFull
-  // (so no weight is larger).  e4m3: weights meet the values as fp16, which ends at 2^16, holds
+  // A row's m grows, to kLift below its maximum, when a block's weights add up to more than 2^kMost
+  // (so no weight is larger; with two parts, when one is larger).  e4m3: weights meet the values as fp16, which ends at 2^16, holds
   // 11 bits down to 2^-14 and nothing below 2^-25; with the largest weight at 2^8 to 2^15, and
   // 128 of them at most 2^15, weights keep 11 bits down to 2^-22 of it and the others are off
   // by 2^-33 of it at most.  bf16 has a float's exponent.
-  static constexpr float kLift = ES == 1 ? 8.f : 0.f, kFull = ES == 1 ? 0x1p15f : 0x1p20f;
+  // Differential attention of bf16 caches: weights meet the values as two bf16 parts (2^-16 in all), since
+  // the difference of two maps that attend to the same tokens is small next to either: one token with most
+  // of both maps' weight, lambda 0.8, 1.4% off in the worst row with one part, 0.26% with two (the
+  // result's rounding), for 176 us in place of 139 (a prompt of 4096 tokens).
+  static constexpr int kParts = ES == 2 && DIFF ? 2 : 1;
+  static constexpr float kLift = ES == 1 ? 8.f : 0.f;
+  static constexpr int kMost = ES == 1 ? 15 : 20;
 };
 
 // What a thread block works on: blocks of tokens of one item.
@@ -287,6 +294,17 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// Two weights as two bf16 parts each: their upper halves, and what these leave.  The rest is kept above 0
+// (2^-18 of the weight more), so that no weight above 0 meets an infinite value as 0 times it.  (Single
+// multiply-adds, which negate for nothing: 180 us against 194 with pairs.)
+__device__ __forceinline__ float rest(float e) {
+  return fmaf(e, 1.f + 0x1p-18f, -__uint_as_float(__float_as_uint(e) & 0xffff0000u));
+}
+__device__ __forceinline__ void two_parts(float2 e, uint32_t &high, uint32_t &low) {
+  high = __byte_perm(__float_as_uint(e.x), __float_as_uint(e.y), 0x7632);
+  low = pack2<2>(rest(e.x), rest(e.y));
+}
+
 // Tiles in shared memory: blocks of 64 channels, in each a row of 128 bytes per token (or
 // packed row), whose 16-byte chunks are permuted by the row (128-byte swizzle).  As an operand
 // whose rows are the rows (Q, K) the matrix unit steps 8 rows by 1024 bytes; as one whose rows
@@ -438,6 +456,20 @@ __device__ __noinline__ void scale_sums(uint32_t tm_o, float f) {
     for (int i = 0; i < 32; ++i) o[i] *= f;
     tm_st32(tm_o + d, o);
   }
+}
+// Whether any of a row's scores in tensor memory is NaN (or infinities of both signs are there).
+template <int N>
+__device__ __noinline__ bool any_nan(uint32_t tm_s) {
+  float all = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < N; i += 32) {
+    float x[32];
+    tm_ld32(x, tm_s + i);
+    tm_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) all += x[k];
+  }
+  return all != all;
 }
 // Sums become 0 where `none` says so.
 template <int N>
@@ -697,75 +729,131 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
             settle();
             tm_ld32(x[0], tm_s);
           }
-          uint32_t w[kN / 2];
           float total = 0.f;
-          // The weights with the m so far.  Where they add up to more than kFull, or a row has
-          // not seen a token yet, m grows and they are made again: S is there until the weights
-          // are written over it.
-          bool ok = true, looked = !mixed;
-#pragma unroll 1
-          for (bool grows = fresh;;) {
-            if (grows) {
+          bool ok = true;
+          // m grows, in some rows, to the largest score
+          auto grow = [&](bool more, float top) {
+            // (beyond 2^23 a float has no room for kLift)
+            const float mn = more ? (fabsf(top) < 0x1p23f ? top - C::kLift : top) : m;
+            const float by = mn == -INFINITY ? 1.f : ex2(m - mn);
+            m = mn;
+            far = on && fabsf(m) > 0x1p20f && m != -INFINITY;
+            some_far = __any_sync(~0u, far);
+            l *= by;
+            if (!fresh) {
+              // With two buffers S may be there before the last product with the values is done
+              // (but not before the one before that, so the barrier is one phase ahead at most).
+              if (kTiles == 1 && !(ok = wait(sh.o_full[0], (mine - 1) & 1))) return;
+              fence_after();
+              scale_sums<DP>(tm_o, by);
+            }
+            if (__any_sync(~0u, far && !product)) settle();
+          };
+          // a NaN may be of the other half's channels: those scores are made again
+          auto look = [&]() {
+            // (e4m3: S is of q over a power of two)
+            const float by = ES == 1 ? 1.f / __uint_as_float((uint32_t)sh.qe[sidx & 1][tile][r] << 23) : 1.f;
+            own_half<ES, kN>(
+                tm_s, c, on, t0, a.by_page,
+                c.table + ((int64_t)s.slot * c.rows + ((int64_t)a.layer * 2) * c.heads + s.h) * c.blocks,
+                a.q + ((int64_t)s.q0 + j) * a.qs + (int64_t)head * a.qhs + map * (c.D / 2), map,
+                product ? by * f : by);
+          };
+          if constexpr (C::kParts == 2) {
+            // The two parts of 32 tokens lie where their scores were, so m is settled before.
+            if (mixed) {
               tm_wait_ld();
-              // only rows that pass it change, so that no row's bits depend on another's
-              const bool grow = total > C::kFull || m == -INFINITY;
-              const float top = top_score<kN>(tm_s, fx);
-              // (beyond 2^23 a float has no room for kLift)
-              const float mn = grow ? (fabsf(top) < 0x1p23f ? top - C::kLift : top) : m;
-              const float by = mn == -INFINITY ? 1.f : ex2(m - mn);
-              m = mn;
-              far = on && fabsf(m) > 0x1p20f && m != -INFINITY;
-              some_far = __any_sync(~0u, far);
-              l *= by;
-              if (!fresh) {
-                // With two buffers S may be there before the last product with the values is done
-                // (but not before the one before that, so the barrier is one phase ahead at most).
-                if (kTiles == 1 && !(ok = wait(sh.o_full[0], (mine - 1) & 1))) break;
-                fence_after();
-                scale_sums<DP>(tm_o, by);
-              }
-              if (__any_sync(~0u, far && !product)) settle();
+              const bool nan = any_nan<kN>(tm_s);  // (all lanes: its loads are the whole warp's)
+              if (__any_sync(~0u, on && nan)) look();
+              tm_ld32(x[0], tm_s);
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kN; i += 32) {
+              const float *y = x[(i >> 5) & 1];
+              tm_wait_ld();
+              tm_ld32(x[((i >> 5) & 1) ^ 1], tm_s + (i + 32 < kN ? i + 32 : 0));
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(y[k], y[k + 1]));
+            }
+            top = __fmul_rn(top, fx);
+            // only rows that pass it change, so that no row's bits depend on another's
+            const bool more = top - m > C::kMost;
+            if (__any_sync(~0u, on && more)) {
+              tm_wait_ld();
+              grow(more, top);
+              if (!ok) break;
               tm_ld32(x[0], tm_s);
             }
             const float m0 = m == -INFINITY ? 0.f : m;
             const float2 f2 = make_float2(fx, fx), m2 = make_float2(-m0, -m0);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
+            // (rolled up and without a load ahead: 178 us; two or four at a time with one 180 and 185)
+#pragma unroll 1
             for (int i = 0; i < kN; i += 32) {
-              float *y = x[(i >> 5) & 1];
+              if (i) tm_ld32(x[0], tm_s + i);
               tm_wait_ld();
-              if (i + 32 < kN) tm_ld32(x[((i >> 5) & 1) ^ 1], tm_s + i + 32);
+              uint32_t w[32];
 #pragma unroll
               for (int k = 0; k < 32; k += 2) {
-                const float2 z = fma2(make_float2(y[k], y[k + 1]), f2, m2);
+                const float2 z = fma2(make_float2(x[0][k], x[0][k + 1]), f2, m2);
                 const float2 e = make_float2(ex2(z.x), ex2(z.y));
                 sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], e);
-                w[(i + k) / 2] = pack2<ES>(e.x, e.y);
+                two_parts(e, w[k / 2], w[16 + k / 2]);
               }
+              tm_st16(tm_s + i, w);
+              tm_st16(tm_s + i + 16, w + 16);
             }
             total = (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
-            // (with two maps NaN too: see below)
-            if (!__any_sync(~0u, on && ((DIFF ? !(total <= C::kFull) : total > C::kFull) || m == -INFINITY))) break;
-            if (DIFF && !looked && __any_sync(~0u, on && total != total)) {
-              // a NaN may be of the other half's channels: those scores are made again
-              // (e4m3: S is of q over a power of two)
-              const float by = ES == 1 ? 1.f / __uint_as_float((uint32_t)sh.qe[sidx & 1][tile][r] << 23) : 1.f;
-              own_half<ES, kN>(
-                  tm_s, c, on, t0, a.by_page,
-                  c.table + ((int64_t)s.slot * c.rows + ((int64_t)a.layer * 2) * c.heads + s.h) * c.blocks,
-                  a.q + ((int64_t)s.q0 + j) * a.qs + (int64_t)head * a.qhs + map * (c.D / 2), map,
-                  product ? by * f : by);
-              looked = true;
-              grows = false;
-              tm_ld32(x[0], tm_s);
-              continue;
-            }
-            if (grows) break;
-            grows = true;
-          }
-          if (!ok) break;
+          } else {
+            uint32_t w[kN / 2];
+            // The weights with the m so far.  Where they add up to more than 2^kMost, or a row has
+            // not seen a token yet, m grows and they are made again: S is there until the weights
+            // are written over it.
+            bool looked = !mixed;
+            constexpr float kFull = 1 << C::kMost;
+#pragma unroll 1
+            for (bool grows = fresh;;) {
+              if (grows) {
+                tm_wait_ld();
+                // only rows that pass it change, so that no row's bits depend on another's
+                grow(total > kFull || m == -INFINITY, top_score<kN>(tm_s, fx));
+                if (!ok) break;
+                tm_ld32(x[0], tm_s);
+              }
+              const float m0 = m == -INFINITY ? 0.f : m;
+              const float2 f2 = make_float2(fx, fx), m2 = make_float2(-m0, -m0);
+              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int i = 0; i < kN / 2; i += 16) tm_st16(tm_s + i, w + i);
+              for (int i = 0; i < kN; i += 32) {
+                float *y = x[(i >> 5) & 1];
+                tm_wait_ld();
+                if (i + 32 < kN) tm_ld32(x[((i >> 5) & 1) ^ 1], tm_s + i + 32);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                  const float2 z = fma2(make_float2(y[k], y[k + 1]), f2, m2);
+                  const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                  sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], e);
+                  w[(i + k) / 2] = pack2<ES>(e.x, e.y);
+                }
+              }
+              total = (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+              // (with two maps NaN too: see below)
+              if (!__any_sync(~0u, on && ((DIFF ? !(total <= kFull) : total > kFull) || m == -INFINITY))) break;
+              if (DIFF && !looked && __any_sync(~0u, on && total != total)) {
+                look();
+                looked = true;
+                grows = false;
+                tm_ld32(x[0], tm_s);
+                continue;
+              }
+              if (grows) break;
+              grows = true;
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < kN / 2; i += 16) tm_st16(tm_s + i, w + i);
+          }
           l += total;
           tm_wait_st();
           fence_before();
@@ -1401,8 +1489,14 @@ __global__ void __launch_bounds__((Cfg<ES, DP, DIFF>::kThreads), 1) k_chunk(
         const uint32_t d = tm + C::kO + t * DP, p = tm + buf * C::kS, v = v_desc + at * (C::kSlot / 16);
         if (elect()) {
 #pragma unroll
-          for (int x = 0; x < kN / 16; ++x)
-            mma_ts(d, p + x * 8, v + x * 2048 / 16, idesc_o, add || x > 0);
+          for (int x = 0; x < kN / 16; ++x) {
+            if (C::kParts == 1) {
+              mma_ts(d, p + x * 8, v + x * 2048 / 16, idesc_o, add || x > 0);
+            } else {  // the parts of 32 tokens' weights lie next to each other
+              mma_ts(d, p + (x >> 1) * 32 + (x & 1) * 8, v + x * 2048 / 16, idesc_o, add || x > 0);
+              mma_ts(d, p + (x >> 1) * 32 + (x & 1) * 8 + 16, v + x * 2048 / 16, idesc_o, true);
+            }
+          }
           mma_commit(smem_addr(&sh.kv_empty[at]));
           if (alone) mma_commit(smem_addr(&sh.kv_empty[at]));
         }
