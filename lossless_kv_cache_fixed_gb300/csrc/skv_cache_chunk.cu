@@ -17,20 +17,21 @@
 // warp of their own brings, become fp16 on the way), one per tile that issues its matrix
 // instructions, one that deals the work.  With two tiles the matrix unit works on one tile while
 // the softmax of the other runs: they take turns, since mixed the instructions of both take as long
-// as both (2048 tokens on 8192, 64 heads of 128: 415 us against 367).  With one tile (more than 128
+// as both (2048 tokens on 6144, 64 heads of 128, in the version of that step: 415 us against 367; now
+// 376 to 390 by GPU).  With one tile (more than 128
 // channels, whose sums take half of the tensor memory) S has two buffers.  Items of up to 128 rows
 // let both tiles work on every second block with the same rows (9 tokens on 131071, e4m3: 90 us
 // against 110).  bf16 weights round to bf16 (2^-8 of each): in two parts, as with one new token and in
 // differential attention, the second product takes twice as long and the weights half as long again
-// (a prompt of 4096 tokens 116 us against 85.5, 2048 tokens on 8192 557 against 380).
+// (a prompt of 4096 tokens 103 us against 85.5, 2048 tokens on 6144 522 against 379).
 //
 // What bounds it: a tile's chain of scores, weights and sums.  128 x 128 scores take a tile 1350
 // clocks (512 of them the rate of the exponentials), its two products 1024, and the barriers
-// between them 600; two tiles overlap to 3400 clocks a block where the products need 2048, 1340
-// TFLOP/s (68% of the library's product) on long caches.  Blocks of 64 tokens with two buffers of S
-// per tile took 574 us for those 358, 4 slots of keys and values instead of 5 with room for the
-// results the same.  A block of threads needs 10 us before its first scores (the code itself is
-// fetched) and the join 3 to 10 us.
+// between them 600; two tiles overlap to 3400 clocks a block where the products need 2048: 1260
+// TFLOP/s (64% of the library's product) with 2048 tokens on 6144.  Blocks of 64 tokens with two
+// buffers of S per tile took 574 us where this took 358 at the time, 4 slots of keys and values instead
+// of 5 with room for the results the same.  A block of threads needs 10 us before its first scores
+// (the code itself is fetched) and the join 3 to 10 us.
 //
 // Work is dealt as in skv_cache_attend.cuh: the blocks of all items in a row, cut evenly over one
 // wave of persistent thread blocks whatever the lengths; items that lie in several leave partial
@@ -69,7 +70,9 @@ struct Cfg {
   // An item costs a thread block this many blocks of tokens more than it has: queries are loaded,
   // results written and the pipeline runs empty in between.  us with 2 / 4 / 8, bf16: a prompt of
   // 4096 tokens 83.8 / 82.1 / 86.0, differential 159 / 137 / 147, windows with 256 channels 104.5 /
-  // 101.1 / 100.3 (6: 100.1); e4m3: ragged turns 200 / 187 / 182, differential 207 / 195 / 186.
+  // 101.1 / 100.3 (6: 100.1); e4m3: ragged turns 200 / 187 / 182, differential 207 / 195 / 186.  64
+  // channels, bf16: a prompt 71.8 / 71.1 / 77.3, differential (weights in one part) 135 / 121 / 130;
+  // e4m3: ragged turns 135.5 / 132.2 / 133.9, a prompt 82.6 / 76.5 / 81.5 (4 would do for them).
   static constexpr int kItemCost = ES == 1 ? 8 : DP == 256 ? 6 : 4;
   static constexpr int kQ = 128 * DP * 2;                // bytes of a tile of queries
   static constexpr int kSlot = kN * DP * 2;              // bytes of a block of keys or values
@@ -88,13 +91,13 @@ struct Cfg {
   static constexpr int kOffStage = kOffRaw + kRaws * kRaw;  // results on their way out, 2 KB a warp
   static constexpr int kOffMisc = kOffStage + kSoftmax * 2048;
   // tensor memory columns
-  static constexpr int kS = kN;            // S of a tile (or buffer); P in the first half
+  static constexpr int kS = kN;            // S of a tile (or buffer); P in the first half, two parts all over it
   static constexpr int kO = 2 * kN;        // O, DP columns per tile
   // A row's m grows, to kLift below its maximum, when a block's weights add up to more than 2^kMost
-  // (so no weight is larger; with two parts, when one is larger).  e4m3: weights meet the values as fp16, which ends at 2^16, holds
-  // 11 bits down to 2^-14 and nothing below 2^-25; with the largest weight at 2^8 to 2^15, and
-  // 128 of them at most 2^15, weights keep 11 bits down to 2^-22 of it and the others are off
-  // by 2^-33 of it at most.  bf16 has a float's exponent.
+  // (so no weight is larger; with two parts, when one is larger).  e4m3: weights meet the values as
+  // fp16, which ends at 2^16, holds 11 bits down to 2^-14 and nothing below 2^-25; with the largest
+  // weight at 2^8 to 2^15, and 128 of them at most 2^15, weights keep 11 bits down to 2^-22 of it and
+  // the others are off by 2^-33 of it at most.  bf16 has a float's exponent.
   // Differential attention of bf16 caches: weights meet the values as two bf16 parts (2^-16 in all), since
   // the difference of two maps that attend to the same tokens is small next to either: one token with most
   // of both maps' weight, lambda 0.8, 1.4% off in the worst row with one part, 0.26% with two (the
