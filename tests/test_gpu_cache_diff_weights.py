@@ -86,3 +86,37 @@ def test_growing_scores(d, n, new):
             tol = tol + 2.0 ** -22 * ref.abs() + 1e-30
             off = (out[:, h].double() - ref).abs()
             assert torch.all(off <= tol + 2.0 ** -8 * (ref.abs() + tol)), (h, mul)
+
+
+@pytest.mark.parametrize("dtype", [0, 1], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 80, 128, 256])
+@pytest.mark.parametrize("n,new", [(600, 4), (600, 90), (5000, 90), (600, None)])
+def test_scores_that_get_huge_next_to_rows_whose_are(dtype, d, n, new):
+    """Of two heads, neighbours in a warp, one has huge scores from the first token on, the other from
+    token 400 on, which takes all of the first map's weight: with lambda 0 its result is that token's
+    value, whatever the other head holds."""
+    c = filled(dtype, 1, 1, d, 64, 1, n, scaled=False)
+    pool = c.pool.view(torch.bfloat16) if dtype == 0 else c.pool
+    t = torch.arange(n, device="cuda")
+    rows = c.table[0, 0, 0, 0, t // 64].long()
+    pool[rows, t % 64] = 0
+    pool[rows, t % 64, 0] = 1.0 if dtype == 0 else 0x38                  # 1
+    pool[rows[400], 400 % 64, 1] = 2.0 ** 14 if dtype == 0 else 0x7E     # 448
+    m = new or 1
+    q = torch.zeros(m, 2, d, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(6)
+    q[:, 0, 0] = 2.0 ** 25
+    q[:, 1, 1] = 2.0 ** 26 * (1 + 63 / 64 * torch.rand(m, generator=g, device="cuda")) * (1 if dtype == 0 else 2.0 ** 4)
+    q = q.bfloat16()
+    more = dict(starts=None if new is None else ints([0, new]), lse=True)
+    lam = torch.zeros(2, device="cuda")
+    out, lse = c.attend_diff(0, ints([0]), ints([n]), q, lam, n, **more)
+    k, v = rows_of(c, dtype, 0, 0, 0, n)
+    assert torch.equal(out[:, 1].double(), v[400].expand(m, d))
+    want = q[:, 1, 1].double() * k[400, 1] * (d // 2) ** -0.5
+    assert torch.all((lse[:, 1, 0].double() - want).abs() <= 2.0 ** -21 * want)
+    calm = q.clone()
+    calm[:, 0, 0] = 1.0
+    o, l = c.attend_diff(0, ints([0]), ints([n]), calm, lam, n, **more)
+    assert torch.equal(o[:, 1], out[:, 1]) and torch.equal(l[:, 1], lse[:, 1])
+    c.status()
